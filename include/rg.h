@@ -113,10 +113,15 @@ typedef enum {
     RG_ERR_ALIGN = -4,   /* W, dY, dX or out not 16-byte aligned                           */
     RG_ERR_CUDA = -5,    /* a CUDA runtime/driver call or a launch failed                  */
     RG_ERR_TIMEOUT = -6, /* a bounded device-side wait gave up (reported by rg_check)      */
-    RG_ERR_RANGE = -7    /* a finite dY value lay outside the 16-bit operand kind's range
+    RG_ERR_RANGE = -7,   /* a finite dY value lay outside the 16-bit operand kind's range
                             (fp16: |dY| >= 65520) and became inf in the tensor-core
                             operand copy: the call's dX holds inf or NaN (reported by
-                            rg_check; rerun with RG_VARIANT_SIMT32 or a scaled dY)       */
+                            rg_check; rerun with RG_VARIANT_SIMT32 or a scaled dY).
+                            Paged cache: a finite key, value or query outside the fp16
+                            operands' range (rg_kv_write, rg_kv_attend)                */
+    RG_ERR_INDEX = -8    /* paged cache: a length, a first token or a page number in a device
+                            array lies outside the batch or the cache (reported by rg_check;
+                            the sequence counts as empty, the page's tokens as not there)  */
 } rg_status;
 
 /* Kernel variants of rg_out_prod_variant. */
@@ -335,6 +340,118 @@ size_t rg_mul_mat_workspace_bytes(int wtype, int64_t N, int64_t K, int64_t T);
 int rg_out_prod_lora(int variant, int wtype, const void* W, int64_t N, int64_t K, const float* dY,
                      int64_t T, float* dX, float beta, const float* lora_a, const float* lora_b,
                      int64_t rank, float scale, void* stream);
+
+/*
+ * The paged key/value cache of a decoder's attention, and the attention over
+ * it: what a model served through rg_mul_mat runs between its projections.
+ *
+ * A cache is a pool of `pages` pages of page_tokens tokens each, one layer's
+ * keys and values of all kv heads.  Its storage type is F16, BF16, Q8_0 or
+ * Q4_0; a block of the last two is 32 consecutive dimensions of one token and
+ * head (Q8_0: value d*q, Q4_0: d*(q-8), d fp16, as the weight types).  The
+ * bytes inside a page follow the kernels (csrc/rg_kv.cuh): they are written
+ * and read through the calls below, and copied or moved page by page.
+ *
+ * A batch is a list of sequences, each a row of page numbers.  Its newest
+ * tokens lie packed, one sequence after another, in the arrays of a call:
+ * sequence s has the rows new_start[s] .. new_start[s+1] - 1, and its length
+ * with them is kv_len[s], so its i-th new token is at position
+ *     p = kv_len[s] - (new_start[s+1] - new_start[s]) + i,
+ * on page page_table[s][p / page_tokens].  All three arrays are in device
+ * memory and read by the kernels, so a captured graph serves every step.
+ *
+ * The kernels check what they read: a sequence whose numbers lie outside the
+ * batch (more new tokens than max_new, rows beyond `tokens`, a length beyond
+ * max_pages pages) counts as empty, a page number outside the pool as a page
+ * that is not there, and either is reported as RG_ERR_INDEX.  A position
+ * below 0 (kv_len less than the new tokens, as for a padding sequence of
+ * length 0) is no error: the token is not stored, reads back as zeros, and
+ * sees nothing.  Rows that belong to no sequence are left as they are.
+ * Page numbers past a sequence's length are not looked at.
+ *
+ * Activations (`atype`: RG_F32, RG_F16 or RG_BF16) are addressed by element
+ * strides of tokens and heads, the head_dim values of a row contiguous:
+ * x[token * x_t + head * x_h + d], so parts of a fused projection can be
+ * passed in place.  Rows are 16-byte aligned: pointers, and strides times
+ * the element size, multiples of 16 (RG_ERR_ALIGN); strides at least
+ * head_dim (RG_ERR_ARG).
+ */
+typedef struct rg_kv_cache {
+  int32_t type;         /* RG_F16, RG_BF16, RG_Q8_0 or RG_Q4_0 (else RG_ERR_TYPE)      */
+  int32_t head_dim;     /* 64, 128 or 256 (else RG_ERR_SHAPE)                          */
+  int32_t kv_heads;     /* 1 .. 4096                                                   */
+  int32_t page_tokens;  /* a multiple of 16, at most 4096 (else RG_ERR_SHAPE)          */
+  int64_t pages;        /* in the pool                                                 */
+  void* data;           /* device, 16-byte aligned: pages * rg_kv_page_bytes() bytes   */
+} rg_kv_cache;
+
+typedef struct rg_kv_batch {
+  int32_t seqs;
+  int32_t max_pages;          /* columns of page_table                                  */
+  int32_t max_new;            /* no sequence has more new tokens (sets the launch)      */
+  int32_t reserved;           /* 0                                                      */
+  int64_t tokens;             /* rows of the packed arrays                              */
+  const int32_t* new_start;   /* device [seqs + 1], ascending                           */
+  const int32_t* kv_len;      /* device [seqs]                                          */
+  const int32_t* page_table;  /* device [seqs][max_pages]                               */
+} rg_kv_batch;
+
+/* Bytes of one page (0 for a type, head_dim, kv_heads or page_tokens that a
+ * cache cannot have). */
+size_t rg_kv_page_bytes(int type, int head_dim, int kv_heads, int page_tokens);
+
+/* Store the batch's new tokens: k, v [tokens][kv_heads][head_dim] (either may
+ * be NULL and is then left out, not both).  F16 and BF16 round to nearest.
+ * Q8_0: d = fp16(max|x| / 127), q = nearest even of x * (127 / max|x|).
+ * Q4_0: with t the first value of the largest magnitude, d = fp16(t / -8),
+ * q = nearest even of x * (-8 / t), plus 8, clamped to 0..15.  A d that
+ * rounds to zero stores zeros; a block with a value that is not finite reads
+ * back as NaN.  A finite value beyond fp16 (|x| > 65504; BF16 caches: none)
+ * is reported as RG_ERR_RANGE.  One launch, no workspace. */
+int rg_kv_write(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* k, int64_t k_t,
+                int64_t k_h, const void* v, int64_t v_t, int64_t v_h, void* stream);
+
+/* Read the batch's new tokens' positions back (for whole contexts: a batch
+ * whose new tokens are all of a sequence's), rounded once to atype.  k or v
+ * may be NULL and is then left out.  One launch, no workspace. */
+int rg_kv_read(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, void* k, int64_t k_t, int64_t k_h,
+               void* v, int64_t v_t, int64_t v_h, void* stream);
+
+/*
+ * Attention of the batch's new tokens over the cache, which holds them
+ * already (rg_kv_write first).  For the token at position p of sequence s and
+ * query head h < heads, with kv head h / (heads / kv_heads):
+ *
+ *     out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q . k_j),
+ *     over the positions j <= p, and j > p - window when window > 0;
+ *
+ * a token that sees no position gets zeros.  q, out: [tokens][heads]
+ * [head_dim].  heads: a multiple of kv_heads, at most 1024 times it
+ * (RG_ERR_SHAPE).  scale: finite (RG_ERR_ARG).
+ *
+ * Scores, softmax statistics and sums are F32.  The matrix units take 16-bit
+ * operands (fp16; bf16 for a BF16 cache): F32 queries, decoded Q8_0 and Q4_0
+ * values and the probabilities are rounded once to them, each a relative
+ * error of at most 2^-11 (bf16: 2^-8).  Queries and cached values beyond
+ * fp16's range are reported as RG_ERR_RANGE (queries here, cached values when
+ * they are stored).  Keys and values at positions a token may not see do not
+ * reach its result, whatever they hold, NaN included.  Results do not change
+ * from call to call on one kind of GPU; they depend on the batch in the order
+ * of summation only.
+ *
+ * The workspace (rg_kv_attend_workspace_bytes) comes from the library's
+ * stream-ordered pool, or from the caller in rg_kv_attend_ws (256-byte
+ * aligned; RG_ERR_ARG if too small), which allocates nothing.
+ */
+int rg_kv_attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* q, int64_t q_t,
+                 int64_t q_h, int heads, void* out, int64_t o_t, int64_t o_h, float scale, int window, void* stream);
+int rg_kv_attend_ws(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* q, int64_t q_t,
+                    int64_t q_h, int heads, void* out, int64_t o_t, int64_t o_h, float scale, int window,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace bytes of one rg_kv_attend call on the current device (0
+ * for descriptions that it refuses and for an empty batch). */
+size_t rg_kv_attend_workspace_bytes(const rg_kv_cache* cache, const rg_kv_batch* batch, int heads);
 
 /* The variant RG_VARIANT_AUTO picks for this shape (ignores RG_VARIANT). */
 int rg_select_variant(int wtype, int64_t N, int64_t K, int64_t T);

@@ -14,3 +14,6 @@ from .quant_out_prod import (  # noqa: F401
     dequant, row_bytes, out_prod, abs_bound, out_prod_at, q4_k_scale_min, mul_mat, mul_mat_bound,
     out_prod_lora, lora_bound, lora_at, batch_weight, out_prod_batched, mul_mat_at,
 )
+from .kv_attention import (  # noqa: F401
+    kv_row_bytes, kv_page_bytes, kv_quantise, kv_values, kv_places, kv_store, kv_attend, bf16_round,
+)

@@ -18,7 +18,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librg.so")
 
 RG_OK, RG_ERR_ARG, RG_ERR_TYPE, RG_ERR_SHAPE = 0, -1, -2, -3
-RG_ERR_ALIGN, RG_ERR_CUDA, RG_ERR_TIMEOUT, RG_ERR_RANGE = -4, -5, -6, -7
+RG_ERR_ALIGN, RG_ERR_CUDA, RG_ERR_TIMEOUT, RG_ERR_RANGE, RG_ERR_INDEX = -4, -5, -6, -7, -8
 RG_VARIANT_AUTO, RG_VARIANT_TC, RG_VARIANT_SMALLT, RG_VARIANT_SIMT32 = 0, 1, 2, 3
 RG_VARIANT_TC_SINGLE, RG_VARIANT_TC_PAIR = 4, 5
 VARIANTS = {"auto": 0, "tc": 1, "smallt": 2, "simt32": 3, "tc1": 4, "tc2": 5}
@@ -33,6 +33,19 @@ class rg_plan_info(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class rg_kv_cache(ctypes.Structure):
+    """include/rg.h rg_kv_cache (kv_cache() fills one in)."""
+    _fields_ = [("type", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class rg_kv_batch(ctypes.Structure):
+    """include/rg.h rg_kv_batch (kv_batch() fills one in)."""
+    _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("tokens", ctypes.c_int64), ("new_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
 # (name, restype, argtypes) of every exported function
@@ -62,6 +75,12 @@ SIGNATURES = [
     ("rg_mul_mat_workspace_bytes", _SZ, [_I, _I64, _I64, _I64]),
     ("rg_out_prod_batched", _I, [_I, _I, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _VP, _I64, _I64,
                                  _I64, _I64, _I64, _VP, _I64, _I64, _I64, _I64, _I64, _F, _VP]),
+    ("rg_kv_page_bytes", _SZ, [_I, _I, _I, _I]),
+    ("rg_kv_write", _I, [_VP, _VP, _I, _VP, _I64, _I64, _VP, _I64, _I64, _VP]),
+    ("rg_kv_read", _I, [_VP, _VP, _I, _VP, _I64, _I64, _VP, _I64, _I64, _VP]),
+    ("rg_kv_attend", _I, [_VP, _VP, _I, _VP, _I64, _I64, _I, _VP, _I64, _I64, _F, _I, _VP]),
+    ("rg_kv_attend_ws", _I, [_VP, _VP, _I, _VP, _I64, _I64, _I, _VP, _I64, _I64, _F, _I, _VP, _SZ, _VP]),
+    ("rg_kv_attend_workspace_bytes", _SZ, [_VP, _VP, _I]),
 ]
 
 RG_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -155,6 +174,52 @@ def rg_out_prod_lora(variant, wtype, W, N, K, dY, T, dX, beta, lora_a, lora_b, r
                      stream=None) -> int:
     return load().rg_out_prod_lora(variant, wtype, _ptr(W), N, K, _ptr(dY), T, _ptr(dX), beta,
                                    _ptr(lora_a), _ptr(lora_b), rank, scale, _stream(stream))
+
+
+def kv_cache(type, head_dim, kv_heads, page_tokens, pages, data) -> rg_kv_cache:
+    """A paged cache's description over device memory that the caller keeps."""
+    return rg_kv_cache(type, head_dim, kv_heads, page_tokens, pages, _ptr(data))
+
+
+def kv_batch(new_start, kv_len, page_table, tokens, max_new, seqs=None, max_pages=None) -> rg_kv_batch:
+    """A batch's description over device int32 arrays that the caller keeps
+    (seqs and max_pages from page_table's shape unless given)."""
+    seqs = page_table.shape[0] if seqs is None else seqs
+    max_pages = page_table.shape[1] if max_pages is None else max_pages
+    return rg_kv_batch(seqs, max_pages, max_new, 0, tokens, _ptr(new_start), _ptr(kv_len), _ptr(page_table))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def rg_kv_page_bytes(type, head_dim, kv_heads, page_tokens) -> int:
+    return load().rg_kv_page_bytes(type, head_dim, kv_heads, page_tokens)
+
+
+def rg_kv_write(cache, batch, atype, k, k_t, k_h, v, v_t, v_h, stream=None) -> int:
+    return load().rg_kv_write(_ref(cache), _ref(batch), atype, _ptr(k), k_t, k_h, _ptr(v), v_t, v_h,
+                              _stream(stream))
+
+
+def rg_kv_read(cache, batch, atype, k, k_t, k_h, v, v_t, v_h, stream=None) -> int:
+    return load().rg_kv_read(_ref(cache), _ref(batch), atype, _ptr(k), k_t, k_h, _ptr(v), v_t, v_h,
+                             _stream(stream))
+
+
+def rg_kv_attend(cache, batch, atype, q, q_t, q_h, heads, out, o_t, o_h, scale, window=0, stream=None) -> int:
+    return load().rg_kv_attend(_ref(cache), _ref(batch), atype, _ptr(q), q_t, q_h, heads, _ptr(out), o_t, o_h,
+                               scale, window, _stream(stream))
+
+
+def rg_kv_attend_ws(cache, batch, atype, q, q_t, q_h, heads, out, o_t, o_h, scale, window, workspace,
+                    workspace_bytes, stream=None) -> int:
+    return load().rg_kv_attend_ws(_ref(cache), _ref(batch), atype, _ptr(q), q_t, q_h, heads, _ptr(out), o_t, o_h,
+                                  scale, window, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rg_kv_attend_workspace_bytes(cache, batch, heads) -> int:
+    return load().rg_kv_attend_workspace_bytes(_ref(cache), _ref(batch), heads)
 
 
 def rg_workspace_bytes(variant, wtype, N, K, T) -> int:

@@ -63,7 +63,8 @@ const Env& env() {
   return e;
 }
 
-// Facts about the current device, queried once per device.
+}  // namespace
+
 int current_dev(DevInfo** out) {
   int d = 0;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return RG_ERR_CUDA;
@@ -86,6 +87,8 @@ int current_dev(DevInfo** out) {
   *out = &g_dev[d];
   return RG_OK;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -201,6 +204,8 @@ thread_local cudaEvent_t t_prof_after = nullptr;
 cudaMemPool_t g_pool[kMaxDevices];
 bool g_pool_ready[kMaxDevices];
 
+}  // namespace
+
 int pool_for(int d, cudaMemPool_t* out) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (!g_pool_ready[d]) {
@@ -218,6 +223,8 @@ int pool_for(int d, cudaMemPool_t* out) {
   *out = g_pool[d];
   return RG_OK;
 }
+
+namespace {
 
 // Device address of g_noalloc_scratch on device d (which must be current),
 // looked up once per device.  Host code must not use the symbol itself: on
@@ -848,6 +855,8 @@ const char* rg_strerror(int status) {
     case RG_ERR_TIMEOUT: return "a bounded device-side wait gave up";
     case RG_ERR_RANGE:
       return "a dY value lay outside the 16-bit tensor-core operand range (fp16: |dY| >= 65520)";
+    case RG_ERR_INDEX:
+      return "a device array of lengths or page numbers holds a value outside the cache or the batch";
     default: return "unknown status";
   }
 }

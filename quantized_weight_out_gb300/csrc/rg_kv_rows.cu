@@ -1,0 +1,615 @@
+// rg_kv_rows.cu - attention of few rows a sequence over the paged cache: single
+// tokens, drafted tokens, short chunks.
+//
+// The rows of a kv head (new tokens x the query heads that share it) are the M
+// side of m16n8k16 products, 16 or 32 at a time; the cache is the N side and
+// is read once, decoded in registers.  With one running maximum and sum a row
+// (out = sum_j 2^(z_j - m) v_j / sum_j 2^(z_j - m), z = score * scale * log2 e)
+// keys can be taken in any order and in parts that are joined later by
+// 2^(m_part - m), so the cache's length is the axis that work is split along:
+//   - all (sequence, kv head, row block) items' 64-token tiles form one line, cut
+//     into equal shares, one a CTA, whatever the sequences' lengths;
+//   - inside a CTA every warp takes each fourth granule, with a ring of its own
+//     that one lane fills by bulk copies (no barrier between warps);
+//   - the warps' results are joined in shared memory; an item cut by a share's
+//     border leaves partial sums that a second kernel joins, in a fixed order.
+// The maximum is a reference that only moves when a score passes it by 2^8:
+// probabilities are at most 2^15, the range fp16 has to spare, and the
+// accumulators are rescaled a few times a row instead of at every granule.
+// Scores, statistics and accumulators are F32; queries (F32 ones), decoded
+// values and probabilities are rounded once to fp16 (a BF16 cache: bf16).
+#include "rg_kv_launch.h"
+#include "rg_kv_rows.cuh"
+
+namespace rg {
+namespace kv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 64;            // tokens: a granule a warp
+constexpr float kNone = -3.0e38f;    // the reference before any visible score
+constexpr float kHead = 7.0f;        // probabilities are scaled by 2^7
+constexpr float kSlack = 8.0f;       // scores may pass the reference by this
+
+template <int TYPE, int D, int MT>
+struct Cfg {
+  static constexpr int BM = 16 * MT;
+  static constexpr bool QREG = MT * D <= 128;              // queries in registers (32 words a lane)
+  static constexpr int GB = granule_bytes(TYPE, D);
+  static constexpr int STAGE = 2 * GB;
+  static constexpr int RANK = MT * D;                      // 64 .. 256: accumulator registers a lane are half of it
+  static constexpr int MINB = STAGE >= 16384 ? 1 : RANK <= 64 ? 4 : RANK <= 128 ? 3 : 2;
+  static constexpr int QBYTES = QREG ? 0 : MT * (D / 32) * 1024;
+  static constexpr int MERGE_LD = D + 8;
+  static constexpr int MERGE = kWarps * BM * MERGE_LD * 4;
+  static constexpr int ROOM = (227 * 1024) / MINB - 2048 - QBYTES;
+  static constexpr int FIT = ROOM / (kWarps * STAGE);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + QBYTES;
+  static_assert(STAGES >= 2, "a ring needs two stages");
+};
+
+// One partial result: m[BM], l[BM], O[BM][D] (unnormalised, relative to 2^m).
+__host__ __device__ constexpr int64_t part_floats(int bm, int dim) { return static_cast<int64_t>(bm) * (dim + 2); }
+
+// The first part of an item that several CTAs share, for the joining kernel.
+struct Desc {
+  int last;    // last CTA with a part of it; -1: none starts here
+  int rows;    // valid rows
+  int token;   // row 0's packed token ...
+  int lead;    // ... and the row's index in the kv head's group
+  int head;    // kv head
+};
+
+struct Shape {
+  int rb, t0, nt;  // row blocks; first tile; tiles
+};
+__device__ __forceinline__ Shape shape_of(const Seq& q, int group, int bm, int window) {
+  Shape s{0, 0, 0};
+  if (q.n == 0) return s;
+  s.rb = (q.n * group + bm - 1) / bm;
+  const int first = max(q.len - q.n, 0);
+  s.t0 = window ? max(0, first - window + 1) / kTile : 0;
+  // a sequence that sees nothing still has its rows to write: one tile
+  s.nt = max(1, (q.len + kTile - 1) / kTile - s.t0);
+  return s;
+}
+
+__device__ __forceinline__ void store_out(const Attend& a, int token, int head, int d, const float (&v)[4]) {
+  const int64_t at = token * a.o_t + head * a.o_h + d;
+  if (a.atype == RG_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else if (a.atype == RG_F16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
+// Eight query values as four operand words; finite values beyond fp16 are reported.
+template <bool BF>
+__device__ __forceinline__ uint4 query8(const Attend& a, int token, int head, int d, int* status) {
+  const int64_t at = token * a.q_t + head * a.q_h + d;
+  float x[8];
+  if (a.atype == RG_F32) {
+    load8<RG_F32>(a.q, at, x);
+  } else if (BF == (a.atype == RG_BF16)) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));  // already the operand type
+  } else if (a.atype == RG_F16) {
+    load8<RG_F16>(a.q, at, x);
+  } else {
+    load8<RG_BF16>(a.q, at, x);
+  }
+  uint32_t w[4];
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = pack16<BF>(x[2 * i], x[2 * i + 1]);
+    over |= overflowed16<BF>(x[2 * i], w[i]) || overflowed16<BF>(x[2 * i + 1], w[i] >> 16);
+  }
+  if (over) report_range(status);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int TYPE, int D, int MT>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
+    attend_rows_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
+  using C = Cfg<TYPE, D, MT>;
+  constexpr bool BF = TYPE == RG_BF16;
+  constexpr int BLK = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kWarps][C::STAGES];
+  __shared__ int usable[kWarps][C::STAGES];
+  __shared__ float sm_m[kWarps][C::BM], sm_l[kWarps][C::BM];
+  __shared__ long long sh_sum[kWarps];
+  __shared__ long long sh_acc;
+  __shared__ int sh_seq, sh_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int G = a.group;
+
+  if (lane < C::STAGES) mbar_init(smem_addr(&full[warp][lane]), 1);
+  if (tid == 0) sh_abort = 0;
+  fence_mbar_init();
+
+  // this CTA's share [lo, hi) of the line of tiles
+  auto tiles_of = [&](int s) -> long long {
+    const Seq q = load_seq(b, c.page_tokens, s, ctl.status);
+    const Shape sh = shape_of(q, G, C::BM, a.window);
+    return static_cast<long long>(sh.rb) * sh.nt * c.kv_heads;
+  };
+  long long sum = 0;
+  for (int s = tid; s < b.seqs; s += 32 * kWarps) sum += tiles_of(s);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) sh_sum[warp] = sum;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sh_sum[w];
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = per * blockIdx.x, hi = min(total, lo + per);
+  if (lo >= hi) {
+    if (tid == 0) desc[blockIdx.x].last = -1;
+    return;
+  }
+  if (warp == 0) {  // the sequence that tile lo belongs to
+    long long acc = 0;
+    for (int s0 = 0;; s0 += 32) {
+      const long long v = s0 + lane < b.seqs ? tiles_of(s0 + lane) : 0;
+      long long inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, acc + inc > lo);
+      if (past || s0 + 32 >= b.seqs) {
+        const int l = past ? __ffs(past) - 1 : 31;
+        const long long before = acc + __shfl_sync(0xFFFFFFFFu, inc - v, l);
+        if (lane == 0) {
+          sh_seq = s0 + l;
+          sh_acc = before;
+        }
+        break;
+      }
+      acc += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+  }
+  __syncthreads();
+  int seq = sh_seq;
+  long long acc = sh_acc, at = lo;
+  bool headed = false;
+  uint32_t it = 0;  // granules this warp has taken from its ring
+  const uint32_t ring = smem_addr(smem) + C::QBYTES + warp * C::STAGES * C::STAGE;
+  const uint32_t qbase = smem_addr(smem);
+  float* merge = reinterpret_cast<float*>(smem + C::QBYTES);
+
+  while (at < hi && seq < b.seqs) {
+    const Seq sq = load_seq(b, c.page_tokens, seq, ctl.status);
+    const Shape sh = shape_of(sq, G, C::BM, a.window);
+    const long long tot = static_cast<long long>(sh.rb) * sh.nt * c.kv_heads;
+    if (at >= acc + tot) {
+      acc += tot;
+      ++seq;
+      continue;
+    }
+    const int item = static_cast<int>((at - acc) / sh.nt);
+    const int tile = static_cast<int>((at - acc) % sh.nt);
+    const int tend = static_cast<int>(min(static_cast<long long>(sh.nt), tile + (hi - at)));
+    const int head = item / sh.rb, rb = item % sh.rb;
+    const int row0 = rb * C::BM, nrows = sq.n * G, first = sq.len - sq.n;
+    const int rows = min(C::BM, nrows - row0);
+    const int minpos = first + row0 / G, maxpos = first + (row0 + rows - 1) / G;
+
+    // positions of this lane's rows (below every token: a row that does not exist)
+    int pos[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 16 * m + 8 * r + g;
+        pos[m][r] = row < rows ? first + (row0 + row) / G : -1;
+      }
+
+    // queries as A operands
+    uint4 qreg[C::QREG ? MT : 1][C::QREG ? BLK : 1][2];
+    if constexpr (C::QREG) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 16 * m + 8 * r + g;
+          const int tok = sq.start + (row0 + row) / G, hd = head * G + (row0 + row) % G;
+#pragma unroll
+          for (int k = 0; k < BLK; ++k)
+            qreg[m][k][r] =
+                row < rows ? query8<BF>(a, tok, hd, 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
+        }
+    } else {
+      for (int u = warp; u < MT * BLK * 2; u += kWarps) {
+        const int m = u / (BLK * 2), k = u / 2 % BLK, r = u & 1;
+        const int row = 16 * m + 8 * r + g;
+        const int tok = sq.start + (row0 + row) / G, hd = head * G + (row0 + row) % G;
+        reinterpret_cast<uint4*>(smem)[u * 32 + lane] =
+            row < rows ? query8<BF>(a, tok, hd, 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
+      }
+      __syncthreads();
+    }
+
+    float o[MT][D / 8][4], m_ref[MT][2], l_sum[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[m][d][i] = 0.0f;
+      m_ref[m][0] = m_ref[m][1] = kNone;
+      l_sum[m][0] = l_sum[m][1] = 0.0f;
+    }
+
+    // this warp's granules: g0 + 4 k, k < count
+    const int gend = min(4 * (sh.t0 + tend), (min(sq.len, maxpos + 1) + kGranule - 1) / kGranule);
+    const int g0 = 4 * (sh.t0 + tile) + warp;
+    const int count = g0 < gend ? (gend - g0 + kWarps - 1) / kWarps : 0;
+    const int* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
+    auto load_pages = [&](int k) {
+      return k + lane < count ? table[(g0 + kWarps * (k + lane)) * kGranule / c.page_tokens] : -1;
+    };
+    int pages = load_pages(0), pages_next = load_pages(32);
+    // granule k into its stage of the ring (the whole warp)
+    auto issue = [&](int k) {
+      if (k && (k & 31) == 0) {
+        pages = pages_next;
+        pages_next = load_pages(k + 32);
+      }
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, k & 31);
+      if (lane == 0) {
+        const uint32_t st = (it + k) % C::STAGES;
+        const uint32_t bar = smem_addr(&full[warp][st]);
+        const bool ok = page >= 0 && page < c.pages;
+        usable[warp][st] = ok;
+        if (ok) {
+          const uint8_t* src =
+              c.data + granule_offset(c, page, 0, head, (g0 + kWarps * k) * kGranule, C::GB);
+          mbar_arrive_expect_tx(bar, C::STAGE);
+          bulk_load(ring + st * C::STAGE, src, C::GB, bar);
+          bulk_load(ring + st * C::STAGE + C::GB, src + c.kv_heads * c.slab_bytes, C::GB, bar);
+        } else {
+          report_index(ctl.status);
+          mbar_arrive(bar);
+        }
+      }
+    };
+
+    // one granule: scores, probabilities, products with the values
+    auto granule = [&](auto masked_c, int gran, uint32_t kbase) {
+      constexpr bool MASKED = decltype(masked_c)::value;
+      const uint32_t vbase = kbase + C::GB;
+      float s[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[m][n][i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < BLK; ++k) {
+        uint32_t kb[2][4];
+        key_operand<TYPE, D>(kbase, k, lane, kb);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint4 x, y;
+          if constexpr (C::QREG) {
+            x = qreg[m][k][0];
+            y = qreg[m][k][1];
+          } else {
+            x = lds128(qbase + (((m * BLK + k) * 2) * 32 + lane) * 16);
+            y = lds128(qbase + (((m * BLK + k) * 2 + 1) * 32 + lane) * 16);
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            mma16<BF>(s[m][n], x.x, y.x, x.y, y.y, kb[n][0], kb[n][1]);
+            mma16<BF>(s[m][n], x.z, y.z, x.w, y.w, kb[n][2], kb[n][3]);
+          }
+        }
+      }
+      uint32_t p[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float top[2] = {kNone, kNone};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float z = s[m][n][i] * a.scale_log2;
+            if constexpr (MASKED) {
+              const int j = gran * kGranule + 4 * t + 2 * n + (i & 1), ps = pos[m][i >> 1];
+              if (j > ps || (a.window && j <= ps - a.window)) z = -INFINITY;
+            }
+            s[m][n][i] = z;
+            top[i >> 1] = fmaxf(top[i >> 1], z);
+          }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m_ref[m][0] + kSlack || top[1] > m_ref[m][1] + kSlack)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float v = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+            v = fmaxf(v, m_ref[m][r]);
+            const float f = ex2(m_ref[m][r] - v);
+            m_ref[m][r] = v;
+            l_sum[m][r] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              o[m][d][2 * r] *= f;
+              o[m][d][2 * r + 1] *= f;
+            }
+          }
+        }
+        const float base0 = m_ref[m][0] - kHead, base1 = m_ref[m][1] - kHead;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float e0 = ex2(s[m][n][0] - base0), e1 = ex2(s[m][n][1] - base0);
+          const float e2 = ex2(s[m][n][2] - base1), e3 = ex2(s[m][n][3] - base1);
+          l_sum[m][0] += e0 + e1;
+          l_sum[m][1] += e2 + e3;
+          p[m][2 * n] = pack16<BF>(e0, e1);
+          p[m][2 * n + 1] = pack16<BF>(e2, e3);
+        }
+      }
+      bool bad = false;
+#pragma unroll
+      for (int k = 0; k < BLK; ++k) {
+        uint32_t vb[4][2];
+        value_operand<TYPE, D, MASKED>(vbase, k, lane, vb, &bad);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mma16<BF>(o[m][4 * k + q], p[m][0], p[m][1], p[m][2], p[m][3], vb[q][0], vb[q][1]);
+      }
+      if constexpr (MASKED) {
+        // values that are not finite were left out of the product (0 x inf would
+        // reach rows that may not see them): add them to the rows that do
+        if (__any_sync(0xFFFFFFFFu, bad)) {
+          for (int jj = 0; jj < kGranule; ++jj) {
+            const int j = gran * kGranule + jj;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float v = value_not_finite<TYPE, D>(vbase, jj, 8 * d + 2 * t + e);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+                    if (j <= pos[m][r] && !(a.window && j <= pos[m][r] - a.window)) o[m][d][2 * r + e] += v;
+              }
+          }
+        }
+      }
+    };
+
+    bool gave_up = false;
+    for (int k = 0; k < min(count, C::STAGES); ++k) issue(k);
+    for (int k = 0; k < count; ++k) {
+      const uint32_t st = (it + k) % C::STAGES, phase = (it + k) / C::STAGES & 1;
+      if (!mbar_wait(smem_addr(&full[warp][st]), phase, ctl, &sh_abort)) gave_up = true;
+      gave_up = __any_sync(0xFFFFFFFFu, gave_up);
+      if (gave_up) {
+        // copies already under way must land before the CTA's shared memory is given up
+        const uint64_t t0 = globaltimer_ns();
+        for (int u = k; u < min(count, k + C::STAGES); ++u)
+          while (!mbar_try_wait(smem_addr(&full[warp][(it + u) % C::STAGES]), (it + u) / C::STAGES & 1) &&
+                 globaltimer_ns() - t0 < ctl.limit_ns) {
+          }
+        break;
+      }
+      const int gran = g0 + kWarps * k, j0 = gran * kGranule;
+      if (usable[warp][st]) {
+        const bool whole = j0 + kGranule - 1 <= minpos && !(a.window && j0 <= maxpos - a.window);
+        if (whole)
+          granule(std::false_type{}, gran, ring + st * C::STAGE);
+        else
+          granule(std::true_type{}, gran, ring + st * C::STAGE);
+      }
+      __syncwarp();
+      if (k + C::STAGES < count) issue(k + C::STAGES);
+    }
+    if (__syncthreads_or(gave_up)) {
+      if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
+      return;
+    }
+    it += count;
+
+    // join the four warps
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float l = l_sum[m][r];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+        const int row = 16 * m + 8 * r + g;
+        if (t == 0) {
+          sm_m[warp][row] = m_ref[m][r];
+          sm_l[warp][row] = l;
+        }
+        if (row < rows) {
+          float* to = merge + (warp * C::BM + row) * C::MERGE_LD + 2 * t;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d)
+            *reinterpret_cast<float2*>(to + 8 * d) = make_float2(o[m][d][2 * r], o[m][d][2 * r + 1]);
+        }
+      }
+    __syncthreads();
+    const bool starts = tile == 0, ends = tend == sh.nt;
+    float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * part_floats(C::BM, D);
+    for (int u = tid; u < rows * (D / 4); u += 32 * kWarps) {
+      const int row = u / (D / 4), d = u % (D / 4) * 4;
+      float top = sm_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
+      float v[4] = {0, 0, 0, 0}, l = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(sm_m[w][row] - top);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * C::BM + row) * C::MERGE_LD + d);
+        l += f * sm_l[w][row];
+        v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
+      }
+      if (starts && ends) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= inv;
+        store_out(a, sq.start + (row0 + row) / G, head * G + (row0 + row) % G, d, v);
+      } else {
+        *reinterpret_cast<float4*>(part + 2 * C::BM + row * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+        if (d == 0) {
+          part[row] = top;
+          part[C::BM + row] = l;
+        }
+      }
+    }
+    if (starts && !ends) {
+      headed = true;
+      if (tid == 0) {
+        const long long end = acc + static_cast<long long>(item + 1) * sh.nt - 1;
+        desc[blockIdx.x] =
+            Desc{static_cast<int>(end / per), rows, sq.start + row0 / G, row0 % G, head};
+      }
+    }
+    at += tend - tile;
+    fence_proxy_async_smem();  // the ring is refilled over what was just read and written
+    __syncthreads();
+  }
+  if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
+  pdl_launch_dependents();
+}
+
+// Joins the parts of items that several CTAs share: block i those of the item
+// whose first part CTA i has.  Threads take (row, 4 dimensions); where there
+// are more threads than that, several take every n-th part, added in a fixed
+// order at the end.
+constexpr int kJoin = 256;
+__global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc* desc, const float* parts, int bm,
+                                                            int dim) {
+  extern __shared__ float sm[];
+  pdl_wait();
+  const Desc ds = desc[blockIdx.x];
+  if (ds.last < 0) return;
+  const int tid = threadIdx.x;
+  const int n = ds.last - static_cast<int>(blockIdx.x) + 1;
+  const int64_t size = part_floats(bm, dim);
+  auto part = [&](int i) {
+    return parts + (i == 0 ? static_cast<int64_t>(blockIdx.x) * 2 + 1 : (static_cast<int64_t>(blockIdx.x) + i) * 2) * size;
+  };
+  const int quads = dim / 4, items = ds.rows * quads;
+  const int groups = max(1, kJoin / items);
+  for (int u0 = 0; u0 < items; u0 += kJoin) {
+    const int u = groups > 1 ? tid % items : u0 + tid;
+    const int grp = groups > 1 ? tid / items : 0;
+    const bool mine = u < items && grp < groups;
+    const int row = mine ? u / quads : 0, d = mine ? u % quads * 4 : 0;
+    float top = kNone, l = 0, v[4] = {0, 0, 0, 0};
+    if (mine) {
+      for (int i = grp; i < n; i += groups) {
+        const float* p = part(i);
+        const float m = p[row], f0 = fmaxf(top, m);
+        const float keep = ex2(top - f0), f = ex2(m - f0);
+        const float4 x = *reinterpret_cast<const float4*>(p + 2 * bm + row * dim + d);
+        l = l * keep + f * p[bm + row];
+        v[0] = v[0] * keep + f * x.x; v[1] = v[1] * keep + f * x.y;
+        v[2] = v[2] * keep + f * x.z; v[3] = v[3] * keep + f * x.w;
+        top = f0;
+      }
+    }
+    if (groups > 1) {
+      float* mine_at = sm + tid * 6;
+      mine_at[0] = top; mine_at[1] = l;
+      mine_at[2] = v[0]; mine_at[3] = v[1]; mine_at[4] = v[2]; mine_at[5] = v[3];
+      __syncthreads();
+      if (mine && grp == 0)
+        for (int k = 1; k < groups; ++k) {
+          const float* p = sm + (tid + k * items) * 6;
+          const float f0 = fmaxf(top, p[0]), keep = ex2(top - f0), f = ex2(p[0] - f0);
+          l = l * keep + f * p[1];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = v[i] * keep + f * p[2 + i];
+          top = f0;
+        }
+    }
+    if (mine && grp == 0) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= inv;
+      store_out(a, ds.token + (ds.lead + row) / a.group, ds.head * a.group + (ds.lead + row) % a.group, d, v);
+    }
+  }
+}
+
+constexpr int kMaxCtasPerSm = 4;
+
+int rows_mt(const Batch& b, int group, int dim) {
+  return dim < 256 && static_cast<int64_t>(b.max_new) * group > 16 ? 2 : 1;
+}
+
+template <int TYPE, int D, int MT>
+cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev, cudaStream_t stream) {
+  using K = Cfg<TYPE, D, MT>;
+  auto kern = attend_rows_kernel<TYPE, D, MT>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), K::SMEM);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than tiles there can be
+  const int64_t blocks = (static_cast<int64_t>(b.tokens) * a.group + K::BM - 1) / K::BM + b.seqs;
+  const int64_t tiles = static_cast<int64_t>(b.max_pages) * c.page_tokens / kTile + 1;
+  const int64_t most = blocks > kMaxCtasPerSm * 1024 / c.kv_heads ? kMaxCtasPerSm * 1024 : blocks * c.kv_heads * tiles;
+  const int grid = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(dev.num_sms) * K::MINB));
+  Desc* desc = static_cast<Desc*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                          (sizeof(Desc) * kMaxCtasPerSm * dev.num_sms + 255) / 256 * 256);
+  kern<<<grid, 32 * kWarps, K::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});
+  if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kJoin);
+  cfg.dynamicSmemBytes = kJoin * 6 * sizeof(float);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return counted(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, static_cast<const Desc*>(desc),
+                                    static_cast<const float*>(parts), K::BM, D));
+}
+
+template <int TYPE>
+cudaError_t go_dim(const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev, cudaStream_t s) {
+  const int mt = rows_mt(b, a.group, c.dim);
+  if (c.dim == 64) return mt == 2 ? go<TYPE, 64, 2>(c, b, a, ws, dev, s) : go<TYPE, 64, 1>(c, b, a, ws, dev, s);
+  if (c.dim == 128) return mt == 2 ? go<TYPE, 128, 2>(c, b, a, ws, dev, s) : go<TYPE, 128, 1>(c, b, a, ws, dev, s);
+  return go<TYPE, 256, 1>(c, b, a, ws, dev, s);
+}
+
+}  // namespace
+
+size_t attend_workspace(int type, const Cache& c, const Batch& b, int heads, const DevInfo& dev) {
+  const int bm = 16 * rows_mt(b, heads / c.kv_heads, c.dim);
+  const int64_t ctas = static_cast<int64_t>(kMaxCtasPerSm) * dev.num_sms;
+  return static_cast<size_t>((ctas * sizeof(Desc) + 255) / 256 * 256 + ctas * 2 * part_floats(bm, c.dim) * 4);
+}
+
+cudaError_t launch_attend(int type, const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev,
+                          cudaStream_t stream) {
+  switch (type) {
+    case RG_F16: return go_dim<RG_F16>(c, b, a, ws, dev, stream);
+    case RG_BF16: return go_dim<RG_BF16>(c, b, a, ws, dev, stream);
+    case RG_Q8_0: return go_dim<RG_Q8_0>(c, b, a, ws, dev, stream);
+    default: return go_dim<RG_Q4_0>(c, b, a, ws, dev, stream);
+  }
+}
+
+}  // namespace kv
+}  // namespace rg

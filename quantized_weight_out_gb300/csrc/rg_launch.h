@@ -26,6 +26,11 @@ struct DevInfo {
   unsigned long long wait_limit_ns;
 };
 
+// Facts about the current device, queried once per device.
+int current_dev(DevInfo** out);
+// The library's stream-ordered memory pool on device d.
+int pool_for(int d, cudaMemPool_t* out);
+
 // Kernels launched by this library (rg_launch_count); every launcher passes
 // its launch status through counted().
 extern std::atomic<unsigned long long> g_launch_count;
