@@ -64,6 +64,30 @@ int check_rows(const void* p, int64_t st, int64_t sh, int heads, int dim, int at
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? RG_OK : RG_ERR_CUDA; }
 
+// Sequences of more rows than this run as tiles of 256 rows on the tensor
+// cores' accumulators in tensor memory; the others, which would leave most of a
+// tile empty, in the few-row kernel.
+constexpr int kRowsLimit = 64;
+
+// How a batch is run: the few-row kernel for its short sequences, the tile
+// kernel as well when there may be longer ones.
+struct Route {
+  bool tiles;
+  int rows_limit;
+  size_t rows_bytes, tiles_bytes;
+};
+Route route_of(const kv::Cache& c, const kv::Batch& b, int group, const DevInfo& dev) {
+  Route r;
+  r.tiles = kv::tiles_have(c.dim) && static_cast<int64_t>(b.max_new) * group > kRowsLimit;
+  // (one sequence alone: whatever its length turns out to be, one kernel has it)
+  r.rows_limit = !r.tiles ? 2147483647 : b.seqs == 1 ? 0 : kRowsLimit;
+  kv::Batch few = b;
+  if (r.tiles) few.max_new = std::max(1, kRowsLimit / group);
+  r.rows_bytes = (kv::rows_workspace(c, few, group, dev) + 255) / 256 * 256;
+  r.tiles_bytes = r.tiles ? kv::tiles_workspace(c, dev) : 0;
+  return r;
+}
+
 int attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* q, int64_t q_t, int64_t q_h,
            int heads, void* out, int64_t o_t, int64_t o_h, float scale, int window, void* ws, size_t ws_bytes,
            bool own_ws, cudaStream_t stream) {
@@ -99,7 +123,9 @@ int attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const 
   a.atype = atype;
   a.window = window;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const size_t need = kv::attend_workspace(cache->type, c, b, heads, *dev);
+  const Route r = route_of(c, b, a.group, *dev);
+  const size_t need = r.rows_bytes + r.tiles_bytes;
+  a.rows_limit = r.rows_limit;
   void* buf = ws;
   if (own_ws) {
     cudaMemPool_t pool{};
@@ -109,7 +135,11 @@ int attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const 
     if (ws_bytes < need) return RG_ERR_ARG;
     if (!aligned(ws, 256)) return RG_ERR_ALIGN;
   }
-  cudaError_t e = kv::launch_attend(cache->type, c, b, a, buf, *dev, stream);
+  cudaError_t e = cudaSuccess;
+  if (r.tiles)
+    e = kv::launch_tiles(cache->type, c, b, a, static_cast<char*>(buf) + r.rows_bytes, *dev, stream);
+  if (e == cudaSuccess && a.rows_limit > 0)
+    e = kv::launch_rows(cache->type, c, b, a, buf, *dev, stream);
   if (own_ws) {
     const cudaError_t f = cudaFreeAsync(buf, stream);
     if (e == cudaSuccess) e = f;
@@ -170,7 +200,8 @@ size_t rg_kv_attend_workspace_bytes(const rg_kv_cache* cache, const rg_kv_batch*
     return 0;
   DevInfo* dev = nullptr;
   if (current_dev(&dev) != RG_OK) return 0;
-  return kv::attend_workspace(cache->type, c, b, heads, *dev);
+  const Route r = route_of(c, b, heads / c.kv_heads, *dev);
+  return r.rows_bytes + r.tiles_bytes;
 }
 
 int rg_kv_attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* q, int64_t q_t,

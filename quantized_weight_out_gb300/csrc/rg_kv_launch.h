@@ -23,10 +23,22 @@ struct Attend {
   int atype;
   int window;                  // 0: none
   float scale_log2;            // scale * log2(e)
+  int rows_limit;              // sequences of more rows (new tokens x group) are the tile kernel's
 };
-size_t attend_workspace(int type, const Cache& c, const Batch& b, int heads, const DevInfo& dev);
-cudaError_t launch_attend(int type, const Cache& c, const Batch& b, const Attend& a, void* workspace,
-                          const DevInfo& dev, cudaStream_t stream);
+// Few rows a sequence (rg_kv_rows.cu): those of at most a.rows_limit rows.
+size_t rows_workspace(const Cache& c, const Batch& b, int group, const DevInfo& dev);
+cudaError_t launch_rows(int type, const Cache& c, const Batch& b, const Attend& a, void* workspace,
+                        const DevInfo& dev, cudaStream_t stream);
+// Tiles of rows on the 5th-generation tensor cores (rg_kv_tiles.cu): the others.
+bool tiles_have(int dim);
+size_t tiles_workspace(const Cache& c, const DevInfo& dev);
+cudaError_t launch_tiles(int type, const Cache& c, const Batch& b, const Attend& a, void* workspace,
+                         const DevInfo& dev, cudaStream_t stream);
+
+// Joins the parts of items that several CTAs share (rg_kv_rows.cu).
+struct Desc;
+cudaError_t launch_join(const Attend& a, const Desc* desc, const float* parts, int bm, int dim, int ctas,
+                        cudaStream_t stream);
 
 }  // namespace kv
 }  // namespace rg

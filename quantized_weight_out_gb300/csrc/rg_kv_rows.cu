@@ -19,7 +19,7 @@
 // Scores, statistics and accumulators are F32; queries (F32 ones), decoded
 // values and probabilities are rounded once to fp16 (a BF16 cache: bf16).
 #include "rg_kv_launch.h"
-#include "rg_kv_rows.cuh"
+#include "rg_kv_attend.cuh"
 
 namespace rg {
 namespace kv {
@@ -27,10 +27,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 64;            // tokens: a granule a warp
-constexpr float kNone = -3.0e38f;    // the reference before any visible score
-constexpr float kHead = 7.0f;        // probabilities are scaled by 2^7
-constexpr float kSlack = 8.0f;       // scores may pass the reference by this
-
 template <int TYPE, int D, int MT>
 struct Cfg {
   static constexpr int BM = 16 * MT;
@@ -50,67 +46,18 @@ struct Cfg {
   static_assert(STAGES >= 2, "a ring needs two stages");
 };
 
-// One partial result: m[BM], l[BM], O[BM][D] (unnormalised, relative to 2^m).
-__host__ __device__ constexpr int64_t part_floats(int bm, int dim) { return static_cast<int64_t>(bm) * (dim + 2); }
-
-// The first part of an item that several CTAs share, for the joining kernel.
-struct Desc {
-  int last;    // last CTA with a part of it; -1: none starts here
-  int rows;    // valid rows
-  int token;   // row 0's packed token ...
-  int lead;    // ... and the row's index in the kv head's group
-  int head;    // kv head
-};
-
 struct Shape {
   int rb, t0, nt;  // row blocks; first tile; tiles
 };
-__device__ __forceinline__ Shape shape_of(const Seq& q, int group, int bm, int window) {
+__device__ __forceinline__ Shape shape_of(const Seq& q, int group, int bm, int window, int max_rows) {
   Shape s{0, 0, 0};
-  if (q.n == 0) return s;
+  if (q.n == 0 || q.n * group > max_rows) return s;  // (the tile kernel's)
   s.rb = (q.n * group + bm - 1) / bm;
   const int first = max(q.len - q.n, 0);
   s.t0 = window ? max(0, first - window + 1) / kTile : 0;
   // a sequence that sees nothing still has its rows to write: one tile
   s.nt = max(1, (q.len + kTile - 1) / kTile - s.t0);
   return s;
-}
-
-__device__ __forceinline__ void store_out(const Attend& a, int token, int head, int d, const float (&v)[4]) {
-  const int64_t at = token * a.o_t + head * a.o_h + d;
-  if (a.atype == RG_F32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-  else if (a.atype == RG_F16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-        make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-}
-
-// Eight query values as four operand words; finite values beyond fp16 are reported.
-template <bool BF>
-__device__ __forceinline__ uint4 query8(const Attend& a, int token, int head, int d, int* status) {
-  const int64_t at = token * a.q_t + head * a.q_h + d;
-  float x[8];
-  if (a.atype == RG_F32) {
-    load8<RG_F32>(a.q, at, x);
-  } else if (BF == (a.atype == RG_BF16)) {
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));  // already the operand type
-  } else if (a.atype == RG_F16) {
-    load8<RG_F16>(a.q, at, x);
-  } else {
-    load8<RG_BF16>(a.q, at, x);
-  }
-  uint32_t w[4];
-  bool over = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = pack16<BF>(x[2 * i], x[2 * i + 1]);
-    over |= overflowed16<BF>(x[2 * i], w[i]) || overflowed16<BF>(x[2 * i + 1], w[i] >> 16);
-  }
-  if (over) report_range(status);
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int TYPE, int D, int MT>
@@ -136,7 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
   // this CTA's share [lo, hi) of the line of tiles
   auto tiles_of = [&](int s) -> long long {
     const Seq q = load_seq(b, c.page_tokens, s, ctl.status);
-    const Shape sh = shape_of(q, G, C::BM, a.window);
+    const Shape sh = shape_of(q, G, C::BM, a.window, a.rows_limit);
     return static_cast<long long>(sh.rb) * sh.nt * c.kv_heads;
   };
   long long sum = 0;
@@ -188,7 +135,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
 
   while (at < hi && seq < b.seqs) {
     const Seq sq = load_seq(b, c.page_tokens, seq, ctl.status);
-    const Shape sh = shape_of(sq, G, C::BM, a.window);
+    const Shape sh = shape_of(sq, G, C::BM, a.window, a.rows_limit);
     const long long tot = static_cast<long long>(sh.rb) * sh.nt * c.kv_heads;
     if (at >= acc + tot) {
       acc += tot;
@@ -296,8 +243,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
           for (int i = 0; i < 4; ++i) s[m][n][i] = 0.0f;
 #pragma unroll
       for (int k = 0; k < BLK; ++k) {
+        KeyWords<TYPE> kw;
+        load_words<TYPE, D>(kw, kbase, k, lane);
         uint32_t kb[2][4];
-        key_operand<TYPE, D>(kbase, k, lane, kb);
+        key_operand(kw, kb);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           uint4 x, y;
@@ -361,8 +310,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
       bool bad = false;
 #pragma unroll
       for (int k = 0; k < BLK; ++k) {
+        ValueWords<TYPE> vw;
+        load_words<TYPE, D>(vw, vbase, k, lane);
         uint32_t vb[4][2];
-        value_operand<TYPE, D, MASKED>(vbase, k, lane, vb, &bad);
+        value_operand<TYPE, MASKED>(vw, vb, &bad);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -507,7 +458,8 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
   };
   const int quads = dim / 4, items = ds.rows * quads;
   const int groups = max(1, kJoin / items);
-  for (int u0 = 0; u0 < items; u0 += kJoin) {
+  // (grid.y blocks take turns at stretches of kJoin items)
+  for (int u0 = blockIdx.y * kJoin; u0 < items; u0 += gridDim.y * kJoin) {
     const int u = groups > 1 ? tid % items : u0 + tid;
     const int grp = groups > 1 ? tid / items : 0;
     const bool mine = u < items && grp < groups;
@@ -571,18 +523,7 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
                                           (sizeof(Desc) * kMaxCtasPerSm * dev.num_sms + 255) / 256 * 256);
   kern<<<grid, 32 * kWarps, K::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});
   if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kJoin);
-  cfg.dynamicSmemBytes = kJoin * 6 * sizeof(float);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return counted(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, static_cast<const Desc*>(desc),
-                                    static_cast<const float*>(parts), K::BM, D));
+  return launch_join(a, desc, parts, K::BM, D, grid, stream);
 }
 
 template <int TYPE>
@@ -595,13 +536,28 @@ cudaError_t go_dim(const Cache& c, const Batch& b, const Attend& a, void* ws, co
 
 }  // namespace
 
-size_t attend_workspace(int type, const Cache& c, const Batch& b, int heads, const DevInfo& dev) {
-  const int bm = 16 * rows_mt(b, heads / c.kv_heads, c.dim);
+cudaError_t launch_join(const Attend& a, const Desc* desc, const float* parts, int bm, int dim, int ctas,
+                        cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, bm * dim / 4 > 16 * kJoin ? 8 : 1);
+  cfg.blockDim = dim3(kJoin);
+  cfg.dynamicSmemBytes = kJoin * 6 * sizeof(float);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return counted(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, desc, parts, bm, dim));
+}
+
+size_t rows_workspace(const Cache& c, const Batch& b, int group, const DevInfo& dev) {
+  const int bm = 16 * rows_mt(b, group, c.dim);
   const int64_t ctas = static_cast<int64_t>(kMaxCtasPerSm) * dev.num_sms;
   return static_cast<size_t>((ctas * sizeof(Desc) + 255) / 256 * 256 + ctas * 2 * part_floats(bm, c.dim) * 4);
 }
 
-cudaError_t launch_attend(int type, const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev,
+cudaError_t launch_rows(int type, const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev,
                           cudaStream_t stream) {
   switch (type) {
     case RG_F16: return go_dim<RG_F16>(c, b, a, ws, dev, stream);
