@@ -29,6 +29,14 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// mbar_wait (rg_internal.cuh), the clock first read after some thousand tries.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
+                                         volatile int* abort_flag) {
+  for (uint32_t it = 0; it < 4096; ++it)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, ctl, abort_flag);
+}
+
 // Contiguous bytes (a multiple of 16, both addresses 16-byte aligned) from
 // global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -189,19 +197,31 @@ __device__ __forceinline__ void key_operand(const KeyWords<TYPE>& k, uint32_t (&
   }
 }
 
-// Value operands of block c: b[q][i], n8 block q (dimensions 32c + 8q + g),
-// tokens 4t + 2i, 4t + 2i + 1.  CLEAN: scales (or 16-bit values) that are not
-// finite become zero and *bad is set.
-template <int TYPE, bool CLEAN>
-__device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_t (&b)[4][2], bool* bad) {
+// Scales (or 16-bit values) that are not finite become zero; true if there was one.
+template <int TYPE>
+__device__ __forceinline__ bool clean_words(ValueWords<TYPE>& v) {
   constexpr uint32_t INF = TYPE == RG_BF16 ? 0x7F80u : 0x7C00u;
-  auto clean = [&](uint32_t x) {
+  bool bad = false;
+  auto clean = [&](uint32_t& x) {
     const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
-    *bad = *bad || lo || hi;
-    return x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
+    bad = bad || lo || hi;
+    x &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
   };
   if constexpr (has_scales(TYPE)) {
-    const uint32_t s0 = CLEAN ? clean(v.s[0]) : v.s[0], s1 = CLEAN ? clean(v.s[1]) : v.s[1];
+    clean(v.s[0]);
+    clean(v.s[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) clean(v.w[i]);
+  }
+  return bad;
+}
+
+// Value operands of block c: b[q][i], n8 block q (dimensions 32c + 8q + g),
+// tokens 4t + 2i, 4t + 2i + 1.
+template <int TYPE>
+__device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_t (&b)[4][2]) {
+  if constexpr (has_scales(TYPE)) {
     if constexpr (TYPE == RG_Q8_0) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) q8_pairs(v.w[q], b[q][0], b[q][1]);
@@ -214,18 +234,18 @@ __device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      b[q][0] = scale2(b[q][0], s0);
-      b[q][1] = scale2(b[q][1], s1);
+      b[q][0] = scale2(b[q][0], v.s[0]);
+      b[q][1] = scale2(b[q][1], v.s[1]);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) b[q][i] = CLEAN ? clean(v.w[2 * q + i]) : v.w[2 * q + i];
+      for (int i = 0; i < 2; ++i) b[q][i] = v.w[2 * q + i];
   }
 }
 
-// What value_operand cleaned away, of token j and dimension d of a granule:
+// What clean_words took out, of token j and dimension d of a granule:
 // 0 where the value is finite.
 __device__ __forceinline__ uint32_t ld32(uint32_t a) { return lds32(a); }
 __device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }

@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
         ValueWords<TYPE> vw;
         load_words<TYPE, D>(vw, vbase, k, lane);
         uint32_t vb[4][2];
-        value_operand<TYPE, MASKED>(vw, vb, &bad);
+        if constexpr (MASKED) bad |= clean_words(vw);
+        value_operand(vw, vb);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
     for (int k = 0; k < min(count, C::STAGES); ++k) issue(k);
     for (int k = 0; k < count; ++k) {
       const uint32_t st = (it + k) % C::STAGES, phase = (it + k) / C::STAGES & 1;
-      if (!mbar_wait(smem_addr(&full[warp][st]), phase, ctl, &sh_abort)) gave_up = true;
+      if (!wait_bar(smem_addr(&full[warp][st]), phase, ctl, &sh_abort)) gave_up = true;
       gave_up = __any_sync(0xFFFFFFFFu, gave_up);
       if (gave_up) {
         // copies already under way must land before the CTA's shared memory is given up

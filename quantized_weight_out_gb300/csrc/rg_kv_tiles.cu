@@ -8,9 +8,11 @@
 //   O += P V            tcgen05.mma, P read from TMEM, V^T from shared memory
 // While one stream's softmax runs, the tensor core works for the other.  Warps:
 //   0 - 7    softmax, a warpgroup a stream; they also load Q and write the result
-//   8 - 15   decoders: a granule (16 tokens) of each tile a warp, global memory ->
-//            registers -> operand tiles (128-byte swizzle), a tile ahead
-//   16       the thread that issues the matrix instructions
+//   8 - 11   key decoders, 12 - 15 value decoders: two granules (16 tokens) of each
+//            tile a warp, global memory -> registers -> operand tiles (128-byte
+//            swizzle), loaded a tile ahead
+//   16       the thread that issues the matrix instructions (17 - 19 idle: registers
+//            are handed out by warpgroups)
 // The running maximum is a reference that moves only when a score passes it by
 // 2^8 (as in rg_kv_rows.cu), so O is rescaled, which needs the tensor core's
 // previous product finished, a few times an item.
@@ -18,6 +20,8 @@
 // causal items of different lengths and ragged sequences balance, and a short
 // prompt over a long cache uses every SM.  An item cut by a border leaves F32
 // parts that a second kernel joins in a fixed order.
+#include <type_traits>
+
 #include "rg_kv_attend.cuh"
 
 namespace rg {
@@ -27,7 +31,15 @@ namespace {
 constexpr int BN = 128;          // tokens of a key tile
 constexpr int BM = 256;          // rows of an item
 constexpr int kSoftWarps = 8, kDecWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 1);
+constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
+constexpr int kMmaWarp = kSoftWarps + kDecWarps;
+// Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 136 for
+// the softmax, 256 x 80 for the decoders and 128 x 40 for the rest, 60416.
+constexpr int kRegsSoft = 136, kRegsDec = 80, kRegsMma = 40;
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 
 template <int D>
@@ -106,22 +118,49 @@ __device__ __forceinline__ bool tile_masked(const Block& b, int window, int t) {
 
 // --- tensor memory --------------------------------------------------------------
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// The matrix instructions and commits are executed by the whole warp with one
+// lane's predicate set, not in a branch of that lane: in converged code their
+// operands stay in uniform registers.  (In a branch each instruction took about
+// 150 cycles to issue, against the 64 that the tensor core needs for it.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc,
+                                       uint32_t one) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
-      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc,
+                                       uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
@@ -133,7 +172,51 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// The load without its wait, and the wait, after which r may be used.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  // (an asm statement takes 30 operands at most)
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two F32 at once
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -142,12 +225,117 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
+// One kind's decoders: warp w of four fills granules 2w and 2w + 1 of every tile
+// of the CTA's share into the two slots at `tiles`, one granule after another,
+// the next one's words on their way meanwhile.
+template <int TYPE, int D, int KIND>
+__device__ __forceinline__ void decode_loop(const Cache& c, const Batch& b, const Attend& a, Walk walk, uint32_t tiles,
+                                            uint32_t full, uint32_t freed, uint8_t (*valid)[kDecWarps], int* poison,
+                                            const WaitCtl& ctl, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  using Words = typename std::conditional<KIND == 0, KeyWords<TYPE>, ValueWords<TYPE>>::type;
+  constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
+  const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int key0 = 4 * (g >> 1) + (g & 1);
+  Segment sg;
+  bool more = walk.next(c, b, a, sg);
+  int ord = 0, i = more ? sg.begin : 0, half = 0;
+  struct Gran {
+    int page, pos, head, ord;
+    bool there;    // inside the item's tokens (past them it is hidden by position)
+    bool masked;   // hidden from some row
+  };
+  auto next_granule = [&](Gran& x) {
+    if (!more) return false;
+    const int t = sg.b.t0 + i;
+    x.pos = t * BN + (2 * w + half) * kGranule;
+    x.head = sg.head;
+    x.ord = ord;
+    x.masked = tile_masked(sg.b, a.window, t);
+    x.there = x.pos < min(sg.sq.len, sg.b.maxpos + 1);
+    x.page = x.there ? __ldg(b.table + static_cast<int64_t>(sg.seq) * b.max_pages + x.pos / c.page_tokens) : -1;
+    half ^= 1;
+    if (half == 0 && ++i == sg.end) {
+      more = walk.next(c, b, a, sg);
+      ++ord;
+      i = sg.begin;
+    }
+    return true;
+  };
+  Words words[BLK] = {};
+  // Without a page of its own a granule loads page 0's: its scores are hidden, so
+  // its keys do not matter, and its values only have to be finite (cleaned).  No
+  // branch: the loads stay in flight until the words are used.
+  auto load = [&](const Gran& x) {
+    if (c.pages == 0) return;
+    const int page = x.page >= 0 && x.page < c.pages ? x.page : 0;
+    const uint8_t* src = c.data + granule_offset(c, page, KIND, x.head, x.pos, GB);
+#pragma unroll
+    for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(words[k], src, k, lane);
+  };
+  Gran cur, nxt;
+  bool have = next_granule(cur);
+  if (have) load(cur);
+  for (uint32_t n2 = 0; have; ++n2) {
+    const uint32_t n = n2 >> 1, slot = n & 1, ph = (n >> 1) & 1;
+    const int gr = 2 * w + (n2 & 1);
+    const bool have_next = next_granule(nxt);
+    const bool paged = cur.page >= 0 && cur.page < c.pages;
+    if ((n2 & 1) == 0 && !__all_sync(0xFFFFFFFFu, wait_bar(freed + 8 * slot, ph ^ 1, ctl, abort_flag))) break;
+    if constexpr (KIND == 0) {
+      const uint32_t to = tiles + slot * C::KV;
+#pragma unroll
+      for (int k = 0; k < BLK; ++k) {
+        uint32_t kb[2][4];
+        key_operand(words[k], kb);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 16 * gr + key0 + 2 * q, chunk = (k & 1) * 4 + t4;
+          sts128(to + (k >> 1) * C::CHUNK + row * 128 + ((chunk ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2],
+                 kb[q][3]);
+        }
+      }
+      if (lane == 0) {
+        *reinterpret_cast<volatile uint8_t*>(&valid[n & 7][gr]) = paged || !cur.there;
+        if (!paged && cur.there) report_index(ctl.status);
+      }
+    } else {
+      if (cur.masked || !paged) {
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) bad |= clean_words(words[k]);
+        if (bad) *reinterpret_cast<volatile int*>(&poison[cur.ord & 3]) = cur.ord;
+      }
+      const uint32_t to = tiles + slot * C::KV + (gr >> 2) * C::VCHUNK + (t4 & 1) * 8;
+      const int chunk = (gr & 3) * 2 + (t4 >> 1);
+#pragma unroll
+      for (int k = 0; k < BLK; ++k) {
+        uint32_t vb[4][2];
+        value_operand(words[k], vb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 32 * k + 8 * q + g;
+          sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
+        }
+      }
+    }
+    if (have_next) load(nxt);
+    if (n2 & 1) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * slot);
+    }
+    cur = nxt;
+    have = have_next;
+  }
+}
+
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tiles_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
   using C = Cfg<D>;
   constexpr bool BF = TYPE == RG_BF16;
-  constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
+  constexpr int GB = granule_bytes(TYPE, D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[17];
   __shared__ __align__(8) uint8_t valid[8][kDecWarps];  // by tile ordinal: the granule's page exists
@@ -165,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(KFULL + i), kDecWarps);
+      mbar_init(bar(KFULL + i), kDecWarps / 2);
       mbar_init(bar(KFREE + i), 1);
-      mbar_init(bar(VFULL + i), kDecWarps);
+      mbar_init(bar(VFULL + i), kDecWarps / 2);
       mbar_init(bar(VFREE + i), 1);
       mbar_init(bar(SFULL + i), 1);
       mbar_init(bar(PFULL + i), 4);
@@ -179,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) poison[i] = -1;
     fence_mbar_init();
   }
-  if (warp == kSoftWarps + kDecWarps) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -252,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment sg;
     if (warp < kSoftWarps) {
       // ---------------- softmax: a row a thread ----------------
+      more_regs<kRegsSoft>();
       const int h = warp >> 2, r = (warp & 3) * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + lanes + h * 128, tO = tmem + lanes + kColO + h * 128;
@@ -287,63 +476,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_ref = kNone, l = 0.0f;
         for (int i = sg.begin; i < sg.end; ++i, ++tile_no, ++n_s) {
           const int t = sg.b.t0 + i;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(SFULL + h), n_s & 1, ctl, &abort_flag));
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(SFULL + h), n_s & 1, ctl, &abort_flag));
           if (!ok) break;
           tc_fence_after();
           const uint64_t granules = *reinterpret_cast<const volatile uint64_t*>(valid[tile_no & 7]);
           const bool masked = tile_masked(sg.b, a.window, t) || granules != 0x0101010101010101ull;
           // columns (lim_lo, lim_hi] of the tile are visible to this row
           const int lim_hi = pos - t * BN, lim_lo = a.window ? pos - a.window - t * BN : -1;
-          auto hide = [&](uint32_t (&s)[32], int c0) {
-            const bool g0 = (granules >> (c0 / 16 * 8)) & 1, g1 = (granules >> (c0 / 16 * 8 + 8)) & 1;
+          if (masked) {
+            // hidden scores become -inf in tensor memory: the passes below have no mask
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 32) {
+              const bool g0 = (granules >> (c0 / 16 * 8)) & 1, g1 = (granules >> (c0 / 16 * 8 + 8)) & 1;
+              const int to = lim_hi - c0, from = lim_lo - c0;
+              uint32_t s[32];
+              tmem_ld_32x32b_x32(tS + c0, s);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c0 + k > lim_hi || c0 + k <= lim_lo || !(k < 16 ? g0 : g1)) s[k] = 0xFF800000u;
-          };
-          float top = kNone;
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            uint32_t s[32];
-            tmem_ld_32x32b_x32(tS + 32 * k4, s);
-            if (masked) hide(s, 32 * k4);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[k]));
+              for (int k = 0; k < 32; ++k)
+                if (k > to || k <= from || !(k < 16 ? g0 : g1)) s[k] = 0xFF800000u;
+              tmem_st32(tS + c0, s);
+            }
+            tmem_wait_st();
           }
-          top = top <= kNone ? kNone : top * cz;
-          if (i == sg.begin) {
-            m_ref = fmaxf(top, kNone);
-          } else if (__any_sync(0xFFFFFFFFu, top > m_ref + kSlack)) {
-            // rescale what has been accumulated, once the last product is in
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
-            if (!ok) break;
-            tc_fence_after();
+          // Probabilities relative to the reference so far, and the tile's maximum on the
+          // way; where it passes the reference by too much, once more with a new one.
+          uint32_t p[BN / 2];
+          float sum;
+          for (;;) {
+            const float off = kHead - m_ref;
+            const uint64_t cz2 = pack_f2(cz, cz), off2 = pack_f2(off, off);
+            float top = kNone;
+            uint64_t sum2 = 0;
+            uint32_t s[2][32];
+            tmem_ld32(tS, s[0]);
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+              uint32_t(&x)[32] = s[k4 & 1];
+              tmem_wait_ld(x);
+              if (k4 < 3) tmem_ld32(tS + 32 * (k4 + 1), s[(k4 + 1) & 1]);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float s0 = __uint_as_float(x[2 * k]), s1 = __uint_as_float(x[2 * k + 1]);
+                top = fmaxf(top, fmaxf(s0, s1));
+                float e0, e1;
+                unpack_f2(fma_f2(pack_f2(s0, s1), cz2, off2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum2 = add_f2(sum2, pack_f2(e0, e1));
+                p[16 * k4 + k] = pack16<BF>(e0, e1);
+              }
+            }
+            float sx, sy;
+            unpack_f2(sum2, sx, sy);
+            sum = sx + sy;
+            top = top <= kNone ? kNone : top * cz;
+            if (!__any_sync(0xFFFFFFFFu, top > m_ref + kSlack)) break;
             const float v = fmaxf(top, m_ref), f = ex2(m_ref - v);
             m_ref = v;
-            l *= f;
+            if (i > sg.begin) {
+              // rescale what has been accumulated, once the last product is in
+              ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
+              if (!ok) break;
+              tc_fence_after();
+              l *= f;
+#pragma unroll 1
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(tO + 32 * k, o);
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO + 32 * k, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(tO + 32 * k, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(tO + 32 * k, o);
+              }
             }
+            if (m_ref == INFINITY) break;  // (a score of +inf: the row is NaN)
           }
-          const float off = kHead - m_ref;
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            uint32_t s[32], p[16];
-            tmem_ld_32x32b_x32(tS + 32 * k4, s);
-            if (masked) hide(s, 32 * k4);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float e0 = ex2(fmaf(__uint_as_float(s[2 * k]), cz, off));
-              const float e1 = ex2(fmaf(__uint_as_float(s[2 * k + 1]), cz, off));
-              l += e0 + e1;
-              p[k] = pack16<BF>(e0, e1);
-            }
-            tmem_st16(tS + 16 * k4, p);
-          }
+          if (!ok) break;
+          l += sum;
+          tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(p));
+          tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -351,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // the result, or this CTA's part of it
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
         if (!ok) break;
         tc_fence_after();
         const bool starts = sg.begin == 0, ends = sg.end == sg.b.nt;
@@ -406,163 +616,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
     } else if (warp < kSoftWarps + kDecWarps) {
-      // ---------------- decoders: a granule of each tile a warp ----------------
-      const int w = warp - kSoftWarps, g = lane >> 2, t4 = lane & 3;
-      const int key0 = 4 * (g >> 1) + (g & 1);
-      struct Tile {
-        int page, pos, head, ord;
-        bool there, masked;   // inside the sequence; hidden from some row
-      };
-      // the tile after the one before, its page number on the way
-      bool more = walk.next(c, b, a, sg);
-      int ord = 0, i = more ? sg.begin : 0;
-      auto next_tile = [&](Tile& x) {
-        if (!more) return false;
-        const int t = sg.b.t0 + i;
-        x.pos = t * BN + w * kGranule;
-        x.head = sg.head;
-        x.ord = ord;
-        x.there = x.pos < min(sg.sq.len, sg.b.maxpos + 1);
-        x.masked = tile_masked(sg.b, a.window, t);
-        x.page = x.there ? __ldg(b.table + static_cast<int64_t>(sg.seq) * b.max_pages + x.pos / c.page_tokens) : -1;
-        if (++i == sg.end) {
-          more = walk.next(c, b, a, sg);
-          ++ord;
-          i = sg.begin;
-        }
-        return true;
-      };
-      KeyWords<TYPE> kw[BLK];
-      ValueWords<TYPE> vw[BLK];
-      auto load_keys = [&](const Tile& x) {
-        if (x.page >= 0 && x.page < c.pages) {
-          const uint8_t* src = c.data + granule_offset(c, x.page, 0, x.head, x.pos, GB);
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
-        } else {
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) kw[k] = KeyWords<TYPE>{};
-        }
-      };
-      auto load_values = [&](const Tile& x) {
-        if (x.page >= 0 && x.page < c.pages) {
-          const uint8_t* src = c.data + granule_offset(c, x.page, 1, x.head, x.pos, GB);
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src, k, lane);
-        } else {
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) vw[k] = ValueWords<TYPE>{};
-        }
-      };
-      Tile cur, nxt;
-      bool have = next_tile(cur);
-      if (have) {
-        load_keys(cur);
-        load_values(cur);
-      }
-      for (uint32_t n = 0; have; ++n) {
-        const bool have_next = next_tile(nxt);
-        const uint32_t slot = n & 1, ph = (n >> 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(KFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
-        {
-          const uint32_t to = sK + slot * C::KV;
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) {
-            uint32_t kb[2][4];
-            key_operand(kw[k], kb);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int row = 16 * w + key0 + 2 * q, chunk = (k & 1) * 4 + t4;
-              sts128(to + (k >> 1) * C::CHUNK + row * 128 + ((chunk ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2],
-                     kb[q][3]);
-            }
-          }
-          if (lane == 0) {
-            const bool ok = !cur.there || (cur.page >= 0 && cur.page < c.pages);
-            *reinterpret_cast<volatile uint8_t*>(&valid[n & 7][w]) = ok;
-            if (!ok) report_index(ctl.status);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(KFULL + slot));
-        }
-        if (have_next) load_keys(nxt);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(VFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
-        {
-          const uint32_t to = sV + slot * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
-          const int chunk = (w & 3) * 2 + (t4 >> 1);
-          bool bad = false;
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) {
-            uint32_t vb[4][2];
-            if (cur.masked)
-              value_operand<TYPE, true>(vw[k], vb, &bad);
-            else
-              value_operand<TYPE, false>(vw[k], vb, &bad);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int row = 32 * k + 8 * q + g;
-              sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
-            }
-          }
-          if (bad) *reinterpret_cast<volatile int*>(&poison[cur.ord & 3]) = cur.ord;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(VFULL + slot));
-        }
-        if (have_next) load_values(nxt);
-        cur = nxt;
-        have = have_next;
-      }
-    } else if (lane == 0) {
+      // ---------------- decoders ----------------
+      fewer_regs<kRegsDec>();
+      if (warp < kSoftWarps + kDecWarps / 2)
+        decode_loop<TYPE, D, 0>(c, b, a, walk, sK, bar(KFULL), bar(KFREE), valid, poison, ctl, &abort_flag);
+      else
+        decode_loop<TYPE, D, 1>(c, b, a, walk, sV, bar(VFULL), bar(VFREE), valid, poison, ctl, &abort_flag);
+    } else {
+      fewer_regs<kRegsMma>();
+    }
+    if (warp == kMmaWarp) {
       // ---------------- the matrix instructions ----------------
+      // (the whole warp walks and waits, so that operands stay warp-uniform; one lane issues)
       constexpr uint32_t idS = idesc_f16(BF, 128, BN, false, false);
       constexpr uint32_t idO = idesc_f16(BF, 128, D, false, false);
-      uint32_t n = 0, ns[2] = {0, 0}, nq[2] = {0, 0};
+      const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024);
+      uint32_t n = 0, n0 = 0, n1 = 0, q0 = 0, q1 = 0;  // tiles; tiles and segments of each stream
       bool ok = true;
       auto wait = [&](int i, uint32_t parity) {
-        if (ok) ok = mbar_wait(bar(i), parity, ctl, &abort_flag);
-        if (ok) tc_fence_after();
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity, ctl, &abort_flag));
+        tc_fence_after();
         return ok;
       };
+      const uint32_t one = elect_one();
+      const uint32_t tm = uniform(tmem);
       auto scores = [&](int h, uint32_t slot) {
+        const uint64_t q = dQ + h * (C::Q >> 4), k = dK + slot * (C::KV >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(tmem + h * 128, sdesc_sw128(sQ + h * C::Q + (k >> 2) * C::CHUNK + (k & 3) * 32, 16, 1024),
-                     sdesc_sw128(sK + slot * C::KV + (k >> 2) * C::CHUNK + (k & 3) * 32, 16, 1024), idS, k != 0);
-        tc_commit(bar(SFULL + h));
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t o = ((i >> 2) * C::CHUNK + (i & 3) * 32) >> 4;
+          mma_ss(tm + h * 128, q + o, k + o, idS, i != 0, one);
+        }
+        commit_one(bar(SFULL + h), one);
+      };
+      auto product = [&](int h, uint32_t slot, bool first, bool frees) {
+        const uint64_t v = dV + slot * (C::KV >> 4);
+#pragma unroll
+        for (int i = 0; i < BN / 16; ++i)
+          mma_ts(tm + kColO + h * 128, tm + h * 128 + 8 * i, v + (((i >> 2) * C::VCHUNK + (i & 3) * 32) >> 4), idO,
+                 i != 0 || !first, one);
+        commit_one(bar(ODONE + h), one);
+        if (frees) commit_one(bar(VFREE + slot), one);
       };
       while (ok && walk.next(c, b, a, sg)) {
-        const int streams = sg.b.rows > 128 ? 2 : 1, count = sg.end - sg.begin;
-        for (int h = 0; h < streams; ++h) wait(QFULL + h, nq[h]++ & 1);
+        const bool two = uniform(sg.b.rows) > 128;
+        const int count = uniform(sg.end - sg.begin);
+        if (!wait(QFULL, q0++ & 1)) break;
+        if (two && !wait(QFULL + 1, q1++ & 1)) break;
         if (!wait(KFULL + (n & 1), (n >> 1) & 1)) break;
-        for (int h = 0; h < streams; ++h) scores(h, n & 1);
-        tc_commit(bar(KFREE + (n & 1)));
-        for (int i = 0; i < count && ok; ++i, ++n) {
+        scores(0, n & 1);
+        if (two) scores(1, n & 1);
+        commit_one(bar(KFREE + (n & 1)), one);
+        for (int i = 0; i < count; ++i, ++n) {
           const uint32_t slot = n & 1, next = (n + 1) & 1;
+          const bool more = i + 1 < count;
           if (!wait(VFULL + slot, (n >> 1) & 1)) break;
-          for (int h = 0; h < streams; ++h) {
-            if (!wait(PFULL + h, ns[h] & 1)) break;
-            ++ns[h];
-#pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              mma_ts(tmem + kColO + h * 128, tmem + h * 128 + 8 * k,
-                     sdesc_sw128(sV + slot * C::KV + (k >> 2) * C::VCHUNK + (k & 3) * 32, 16, 1024), idO,
-                     i != 0 || k != 0);
-            tc_commit(bar(ODONE + h));
-            if (h == streams - 1) tc_commit(bar(VFREE + slot));
-            if (i + 1 < count) {
-              if (h == 0 && !wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
-              scores(h, next);
-              if (h == streams - 1) tc_commit(bar(KFREE + next));
-            }
+          if (!wait(PFULL, n0++ & 1)) break;
+          product(0, slot, i == 0, !two);
+          if (more) {
+            if (!wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
+            scores(0, next);
           }
+          if (two) {
+            if (!wait(PFULL + 1, n1++ & 1)) break;
+            product(1, slot, i == 0, true);
+            if (more) scores(1, next);
+          }
+          if (more) commit_one(bar(KFREE + next), one);
         }
       }
       if (!ok) {  // every product issued ends before tensor memory is freed
-        tc_commit(bar(DRAIN));
-        volatile int no_abort = 0;
-        (void)mbar_wait(bar(DRAIN), 0, ctl, &no_abort);
+        if (lane == 0) {
+          tc_commit(bar(DRAIN));
+          volatile int no_abort = 0;
+          (void)mbar_wait(bar(DRAIN), 0, ctl, &no_abort);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();
@@ -571,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kDecWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
