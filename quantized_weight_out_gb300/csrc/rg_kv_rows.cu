@@ -440,61 +440,70 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
   pdl_launch_dependents();
 }
 
-// Joins the parts of items that several CTAs share: block i those of the item
-// whose first part CTA i has.  Threads take (row, 4 dimensions); where there
-// are more threads than that, several take every n-th part, added in a fixed
-// order at the end.
-constexpr int kJoin = 256;
+// Joins the parts of items that several CTAs share: block (i, y) has `stretch`
+// rows of the item whose first part CTA i has.  A warp a row first finds the
+// row's reference and sum; then threads take (row, 4 dimensions), and where there
+// are more threads than that, several share the parts, added in a fixed order.
+// Each part's loads stand alone, so that many are in flight.
+constexpr int kJoin = 512;
 __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc* desc, const float* parts, int bm,
-                                                            int dim) {
-  extern __shared__ float sm[];
+                                                            int dim, int stretch) {
+  __shared__ float sm_top[32], sm_inv[32];
+  __shared__ float sm_v[kJoin * 4];
   pdl_wait();
   const Desc ds = desc[blockIdx.x];
-  if (ds.last < 0) return;
-  const int tid = threadIdx.x;
+  const int first = blockIdx.y * stretch, rows = min(stretch, ds.rows - first);
+  if (ds.last < 0 || rows <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int n = ds.last - static_cast<int>(blockIdx.x) + 1;
   const int64_t size = part_floats(bm, dim);
-  auto part = [&](int i) {
-    return parts + (i == 0 ? static_cast<int64_t>(blockIdx.x) * 2 + 1 : (static_cast<int64_t>(blockIdx.x) + i) * 2) * size;
-  };
-  const int quads = dim / 4, items = ds.rows * quads;
-  const int groups = max(1, kJoin / items);
-  // (grid.y blocks take turns at stretches of kJoin items)
-  for (int u0 = blockIdx.y * kJoin; u0 < items; u0 += gridDim.y * kJoin) {
-    const int u = groups > 1 ? tid % items : u0 + tid;
-    const int grp = groups > 1 ? tid / items : 0;
+  const float* head = parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * size;
+  const float* rest = parts + static_cast<int64_t>(blockIdx.x) * 2 * size;  // part i >= 1: rest + 2 i size
+  auto part = [&](int i) { return i == 0 ? head : rest + 2 * i * size; };
+  for (int r = tid >> 5; r < rows; r += kJoin / 32) {
+    const int row = first + r;
+    float top = kNone;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float l = 0.0f;
+    for (int i = lane; i < n; i += 32) l += ex2(part(i)[row] - top) * part(i)[bm + row];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (lane == 0) {
+      sm_top[r] = top;
+      sm_inv[r] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+  }
+  __syncthreads();
+  const int quads = dim / 4, items = rows * quads;
+  const int groups = items < kJoin ? kJoin / items : 1;
+  for (int u0 = 0; u0 < items; u0 += kJoin) {
+    const int u = groups > 1 ? tid % items : u0 + tid, grp = groups > 1 ? tid / items : 0;
     const bool mine = u < items && grp < groups;
-    const int row = mine ? u / quads : 0, d = mine ? u % quads * 4 : 0;
-    float top = kNone, l = 0, v[4] = {0, 0, 0, 0};
+    const int r = mine ? u / quads : 0, row = first + r, d = mine ? u % quads * 4 : 0;
+    float v[4] = {0, 0, 0, 0};
     if (mine) {
+      const float top = sm_top[r];
+#pragma unroll 8
       for (int i = grp; i < n; i += groups) {
         const float* p = part(i);
-        const float m = p[row], f0 = fmaxf(top, m);
-        const float keep = ex2(top - f0), f = ex2(m - f0);
+        const float f = ex2(p[row] - top);
         const float4 x = *reinterpret_cast<const float4*>(p + 2 * bm + row * dim + d);
-        l = l * keep + f * p[bm + row];
-        v[0] = v[0] * keep + f * x.x; v[1] = v[1] * keep + f * x.y;
-        v[2] = v[2] * keep + f * x.z; v[3] = v[3] * keep + f * x.w;
-        top = f0;
+        v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
       }
     }
     if (groups > 1) {
-      float* mine_at = sm + tid * 6;
-      mine_at[0] = top; mine_at[1] = l;
-      mine_at[2] = v[0]; mine_at[3] = v[1]; mine_at[4] = v[2]; mine_at[5] = v[3];
+      *reinterpret_cast<float4*>(sm_v + 4 * tid) = make_float4(v[0], v[1], v[2], v[3]);
       __syncthreads();
       if (mine && grp == 0)
         for (int k = 1; k < groups; ++k) {
-          const float* p = sm + (tid + k * items) * 6;
-          const float f0 = fmaxf(top, p[0]), keep = ex2(top - f0), f = ex2(p[0] - f0);
-          l = l * keep + f * p[1];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = v[i] * keep + f * p[2 + i];
-          top = f0;
+          const float4 x = *reinterpret_cast<const float4*>(sm_v + 4 * (tid + k * items));
+          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         }
     }
     if (mine && grp == 0) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = sm_inv[r];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] *= inv;
       store_out(a, ds.token + (ds.lead + row) / a.group, ds.head * a.group + (ds.lead + row) % a.group, d, v);
@@ -539,17 +548,17 @@ cudaError_t go_dim(const Cache& c, const Batch& b, const Attend& a, void* ws, co
 
 cudaError_t launch_join(const Attend& a, const Desc* desc, const float* parts, int bm, int dim, int ctas,
                         cudaStream_t stream) {
+  const int stretch = std::min(bm, std::min(32, kJoin * 4 / dim));  // rows a block: one (row, 4 dimensions) a thread
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, bm * dim / 4 > 16 * kJoin ? 8 : 1);
+  cfg.gridDim = dim3(ctas, (bm + stretch - 1) / stretch);
   cfg.blockDim = dim3(kJoin);
-  cfg.dynamicSmemBytes = kJoin * 6 * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return counted(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, desc, parts, bm, dim));
+  return counted(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, desc, parts, bm, dim, stretch));
 }
 
 size_t rows_workspace(const Cache& c, const Batch& b, int group, const DevInfo& dev) {

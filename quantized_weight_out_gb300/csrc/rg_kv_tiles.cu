@@ -8,11 +8,11 @@
 //   O += P V            tcgen05.mma, P read from TMEM, V^T from shared memory
 // While one stream's softmax runs, the tensor core works for the other.  Warps:
 //   0 - 7    softmax, a warpgroup a stream; they also load Q and write the result
-//   8 - 11   key decoders, 12 - 15 value decoders: two granules (16 tokens) of each
-//            tile a warp, global memory -> registers -> operand tiles (128-byte
-//            swizzle), loaded a tile ahead
-//   16       the thread that issues the matrix instructions (17 - 19 idle: registers
-//            are handed out by warpgroups)
+//   8 - 15   decoders: a granule (16 tokens) of each tile a warp, global memory ->
+//            registers -> operand tiles (128-byte swizzle), loaded a tile ahead
+//   16       issues the matrix instructions
+//   17       scheduler: page numbers and masks of the next tiles (18, 19 idle:
+//            registers are handed out by warpgroups)
 // The running maximum is a reference that moves only when a score passes it by
 // 2^8 (as in rg_kv_rows.cu), so O is rescaled, which needs the tensor core's
 // previous product finished, a few times an item.
@@ -34,13 +34,14 @@ constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
 // Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 136 for
-// the softmax, 256 x 80 for the decoders and 128 x 40 for the rest, 60416.
-constexpr int kRegsSoft = 136, kRegsDec = 80, kRegsMma = 40;
+// the softmax, 256 x 88 for the decoders and 128 x 32 for the rest, the same.
+constexpr int kRegsSoft = 136, kRegsDec = 88, kRegsMma = 32;
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr int kScan = 256;       // sequences counted at a time
 
 template <int D>
 struct Cfg {
@@ -225,137 +226,44 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
-// One kind's decoders: warp w of four fills granules 2w and 2w + 1 of every tile
-// of the CTA's share into the two slots at `tiles`, one granule after another,
-// the next one's words on their way meanwhile.
-template <int TYPE, int D, int KIND>
-__device__ __forceinline__ void decode_loop(const Cache& c, const Batch& b, const Attend& a, Walk walk, uint32_t tiles,
-                                            uint32_t full, uint32_t freed, uint8_t (*valid)[kDecWarps], int* poison,
-                                            const WaitCtl& ctl, volatile int* abort_flag) {
-  using C = Cfg<D>;
-  using Words = typename std::conditional<KIND == 0, KeyWords<TYPE>, ValueWords<TYPE>>::type;
-  constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
-  const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int key0 = 4 * (g >> 1) + (g & 1);
-  Segment sg;
-  bool more = walk.next(c, b, a, sg);
-  int ord = 0, i = more ? sg.begin : 0, half = 0;
-  struct Gran {
-    int page, pos, head, ord;
-    bool there;    // inside the item's tokens (past them it is hidden by position)
-    bool masked;   // hidden from some row
-  };
-  auto next_granule = [&](Gran& x) {
-    if (!more) return false;
-    const int t = sg.b.t0 + i;
-    x.pos = t * BN + (2 * w + half) * kGranule;
-    x.head = sg.head;
-    x.ord = ord;
-    x.masked = tile_masked(sg.b, a.window, t);
-    x.there = x.pos < min(sg.sq.len, sg.b.maxpos + 1);
-    x.page = x.there ? __ldg(b.table + static_cast<int64_t>(sg.seq) * b.max_pages + x.pos / c.page_tokens) : -1;
-    half ^= 1;
-    if (half == 0 && ++i == sg.end) {
-      more = walk.next(c, b, a, sg);
-      ++ord;
-      i = sg.begin;
-    }
-    return true;
-  };
-  Words words[BLK] = {};
-  // Without a page of its own a granule loads page 0's: its scores are hidden, so
-  // its keys do not matter, and its values only have to be finite (cleaned).  No
-  // branch: the loads stay in flight until the words are used.
-  auto load = [&](const Gran& x) {
-    if (c.pages == 0) return;
-    const int page = x.page >= 0 && x.page < c.pages ? x.page : 0;
-    const uint8_t* src = c.data + granule_offset(c, page, KIND, x.head, x.pos, GB);
-#pragma unroll
-    for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(words[k], src, k, lane);
-  };
-  Gran cur, nxt;
-  bool have = next_granule(cur);
-  if (have) load(cur);
-  for (uint32_t n2 = 0; have; ++n2) {
-    const uint32_t n = n2 >> 1, slot = n & 1, ph = (n >> 1) & 1;
-    const int gr = 2 * w + (n2 & 1);
-    const bool have_next = next_granule(nxt);
-    const bool paged = cur.page >= 0 && cur.page < c.pages;
-    if ((n2 & 1) == 0 && !__all_sync(0xFFFFFFFFu, wait_bar(freed + 8 * slot, ph ^ 1, ctl, abort_flag))) break;
-    if constexpr (KIND == 0) {
-      const uint32_t to = tiles + slot * C::KV;
-#pragma unroll
-      for (int k = 0; k < BLK; ++k) {
-        uint32_t kb[2][4];
-        key_operand(words[k], kb);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int row = 16 * gr + key0 + 2 * q, chunk = (k & 1) * 4 + t4;
-          sts128(to + (k >> 1) * C::CHUNK + row * 128 + ((chunk ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2],
-                 kb[q][3]);
-        }
-      }
-      if (lane == 0) {
-        *reinterpret_cast<volatile uint8_t*>(&valid[n & 7][gr]) = paged || !cur.there;
-        if (!paged && cur.there) report_index(ctl.status);
-      }
-    } else {
-      if (cur.masked || !paged) {
-        bool bad = false;
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) bad |= clean_words(words[k]);
-        if (bad) *reinterpret_cast<volatile int*>(&poison[cur.ord & 3]) = cur.ord;
-      }
-      const uint32_t to = tiles + slot * C::KV + (gr >> 2) * C::VCHUNK + (t4 & 1) * 8;
-      const int chunk = (gr & 3) * 2 + (t4 >> 1);
-#pragma unroll
-      for (int k = 0; k < BLK; ++k) {
-        uint32_t vb[4][2];
-        value_operand(words[k], vb);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = 32 * k + 8 * q + g;
-          sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
-        }
-      }
-    }
-    if (have_next) load(nxt);
-    if (n2 & 1) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + 8 * slot);
-    }
-    cur = nxt;
-    have = have_next;
-  }
-}
+// What the decoders need to know of a tile, written by the scheduler a few tiles
+// ahead, so that they wait for no page number and walk nothing.
+struct TileInfo {
+  long long off[8];   // byte offset of each granule's keys
+  int ord;            // segment; -1: no more tiles
+  uint8_t clean;      // values are checked: some row may not see them all
+  uint8_t valid;      // bit g: granule g's tokens are there, or hidden by position
+};
+constexpr int kRing = 8;
 
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tiles_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
   using C = Cfg<D>;
   constexpr bool BF = TYPE == RG_BF16;
-  constexpr int GB = granule_bytes(TYPE, D);
+  constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[17];
-  __shared__ __align__(8) uint8_t valid[8][kDecWarps];  // by tile ordinal: the granule's page exists
+  __shared__ __align__(8) uint64_t bars[17 + 2 * kRing];
+  __shared__ TileInfo ring[kRing];
+  __shared__ uint8_t valid[8];                          // by tile ordinal: TileInfo's valid
   __shared__ int poison[4];                             // by segment ordinal: values left out of the product
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ Walk sh_walk;
-  __shared__ long long sh_sum[kThreads / 32];
+  __shared__ long long sh_tiles[kScan];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sK = base + 2 * C::Q, sV = sK + 2 * C::KV;
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
   // barriers: two of each kind
-  constexpr int KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, ODONE = 12, QFULL = 14, DRAIN = 16;
+  constexpr int KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, ODONE = 12, QFULL = 14, DRAIN = 16,
+                RFULL = 17, RFREE = RFULL + kRing;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(KFULL + i), kDecWarps / 2);
+      mbar_init(bar(KFULL + i), kDecWarps);
       mbar_init(bar(KFREE + i), 1);
-      mbar_init(bar(VFULL + i), kDecWarps / 2);
+      mbar_init(bar(VFULL + i), kDecWarps);
       mbar_init(bar(VFREE + i), 1);
       mbar_init(bar(SFULL + i), 1);
       mbar_init(bar(PFULL + i), 4);
@@ -363,6 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(QFULL + i), 4);
     }
     mbar_init(bar(DRAIN), 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(RFULL + i), 1);
+      mbar_init(bar(RFREE + i), kDecWarps);
+    }
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) poison[i] = -1;
     fence_mbar_init();
@@ -372,65 +284,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
 
-  // this CTA's share of the line
-  auto tiles_of = [&](int s, int* status) -> long long {
-    const Seq q = load_seq(b, c.page_tokens, s, status);
-    const int nrb = blocks_of(q, a.group, a.rows_limit);
-    long long n = 0;
-    for (int rb = 0; rb < nrb; ++rb) n += block_of(q, a.group, a.window, rb).nt;
-    return n * c.kv_heads;
-  };
-  long long sum = 0;
-  for (int s = tid; s < b.seqs; s += kThreads) sum += tiles_of(s, ctl.status);
+  // This CTA's share of the line: every sequence's tiles are counted by a warp
+  // (lanes over its blocks), kScan sequences at a time.
+  auto count_tiles = [&](int s0, int* status) {
+    for (int s = s0 + warp; s < min(b.seqs, s0 + kScan); s += kThreads / 32) {
+      const Seq q = load_seq(b, c.page_tokens, s, status);
+      const int nrb = blocks_of(q, a.group, a.rows_limit);
+      int n = 0;
+      for (int rb = lane; rb < nrb; rb += 32) n += block_of(q, a.group, a.window, rb).nt;
+      long long all = n;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) sh_sum[warp] = sum;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+      if (lane == 0) sh_tiles[s - s0] = all * c.kv_heads;
+    }
+  };
   long long total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) total += sh_sum[w];
+  for (int s0 = 0; s0 < b.seqs; s0 += kScan) {
+    if (s0) __syncthreads();
+    count_tiles(s0, ctl.status);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long sum = 0;
+    for (int s = lane; s < min(b.seqs - s0, kScan); s += 32) sum += sh_tiles[s];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    total += sum;
+  }
+  const uint32_t tmem = tmem_slot;
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long lo = per * blockIdx.x, hi = min(total, lo + per);
-  if (warp == 0 && lo < hi) {  // where it begins
-    long long acc = 0;
-    for (int s0 = 0;; s0 += 32) {
-      const long long v = s0 + lane < b.seqs ? tiles_of(s0 + lane, nullptr) : 0;
+  // where it begins
+  long long before = 0;
+  bool found = lo >= hi;
+  for (int s0 = 0; s0 < b.seqs && !found; s0 += kScan) {
+    if (b.seqs > kScan) {
+      __syncthreads();
+      count_tiles(s0, nullptr);
+      __syncthreads();
+    }
+    const int here = min(b.seqs - s0, kScan);
+    for (int s1 = 0; s1 < here && !found; s1 += 32) {
+      const long long v = s1 + lane < here ? sh_tiles[s1 + lane] : 0;
       long long inc = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += u;
       }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, acc + inc > lo);
-      if (past || s0 + 32 >= b.seqs) {
-        const int l = past ? __ffs(past) - 1 : 31;
-        const long long before = acc + __shfl_sync(0xFFFFFFFFu, inc - v, l);
-        if (lane == 0) {
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + inc > lo);
+      if (past) {
+        found = true;
+        if (warp == 0) {
+          const int l = __ffs(past) - 1;
+          const long long one = __shfl_sync(0xFFFFFFFFu, v, l) / c.kv_heads;
+          long long rel = lo - before - __shfl_sync(0xFFFFFFFFu, inc - v, l);
           Walk w;
           w.at = lo;
-          w.hi = past ? hi : lo;
-          w.seq = s0 + l;
-          w.sq = load_seq(b, c.page_tokens, min(w.seq, b.seqs - 1), nullptr);
+          w.hi = hi;
+          w.seq = s0 + s1 + l;
+          w.sq = load_seq(b, c.page_tokens, w.seq, nullptr);
           w.nrb = blocks_of(w.sq, a.group, a.rows_limit);
-          long long one = 0;
-          for (int rb = 0; rb < w.nrb; ++rb) one += block_of(w.sq, a.group, a.window, rb).nt;
-          long long rel = lo - before;
-          w.head = one ? static_cast<int>(rel / one) : 0;
+          w.head = static_cast<int>(rel / one);
           rel -= w.head * one;
-          w.rb = 0;
-          for (; w.rb < w.nrb - 1; ++w.rb) {
-            const int nt = block_of(w.sq, a.group, a.window, w.rb).nt;
-            if (rel < nt) break;
-            rel -= nt;
+          for (int rb0 = 0;; rb0 += 32) {  // the block, 32 at a time
+            const int nt = rb0 + lane < w.nrb ? block_of(w.sq, a.group, a.window, rb0 + lane).nt : 0;
+            int sum = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+              if (lane >= o) sum += u;
+            }
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, sum > rel);
+            if (in || rb0 + 32 >= w.nrb) {
+              const int k = in ? __ffs(in) - 1 : 0;
+              w.rb = rb0 + k;
+              w.tile = static_cast<int>(rel) - __shfl_sync(0xFFFFFFFFu, sum - nt, k);
+              break;
+            }
+            rel -= __shfl_sync(0xFFFFFFFFu, sum, 31);
           }
-          w.tile = static_cast<int>(rel);
-          sh_walk = w;
+          if (lane == 0) sh_walk = w;
         }
-        break;
       }
-      acc += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      before += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
   __syncthreads();
@@ -479,15 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(SFULL + h), n_s & 1, ctl, &abort_flag));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t granules = *reinterpret_cast<const volatile uint64_t*>(valid[tile_no & 7]);
-          const bool masked = tile_masked(sg.b, a.window, t) || granules != 0x0101010101010101ull;
+          const uint32_t granules = *reinterpret_cast<const volatile uint8_t*>(&valid[tile_no & 7]);
+          const bool masked = tile_masked(sg.b, a.window, t) || granules != 0xFFu;
           // columns (lim_lo, lim_hi] of the tile are visible to this row
           const int lim_hi = pos - t * BN, lim_lo = a.window ? pos - a.window - t * BN : -1;
           if (masked) {
             // hidden scores become -inf in tensor memory: the passes below have no mask
 #pragma unroll 1
             for (int c0 = 0; c0 < BN; c0 += 32) {
-              const bool g0 = (granules >> (c0 / 16 * 8)) & 1, g1 = (granules >> (c0 / 16 * 8 + 8)) & 1;
+              const bool g0 = (granules >> (c0 / 16)) & 1, g1 = (granules >> (c0 / 16 + 1)) & 1;
               const int to = lim_hi - c0, from = lim_lo - c0;
               uint32_t s[32];
               tmem_ld_32x32b_x32(tS + c0, s);
@@ -616,14 +553,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
     } else if (warp < kSoftWarps + kDecWarps) {
-      // ---------------- decoders ----------------
+      // ---------------- decoders: granule w of every tile ----------------
       fewer_regs<kRegsDec>();
-      if (warp < kSoftWarps + kDecWarps / 2)
-        decode_loop<TYPE, D, 0>(c, b, a, walk, sK, bar(KFULL), bar(KFREE), valid, poison, ctl, &abort_flag);
-      else
-        decode_loop<TYPE, D, 1>(c, b, a, walk, sV, bar(VFULL), bar(VFREE), valid, poison, ctl, &abort_flag);
+      const int w = warp - kSoftWarps, g = lane >> 2, t4 = lane & 3;
+      const int key0 = 16 * w + 4 * (g >> 1) + (g & 1);
+      const long long to_values = c.kv_heads * c.slab_bytes;
+      KeyWords<TYPE> kw[BLK] = {};
+      ValueWords<TYPE> vw[BLK] = {};
+      auto info = [&](uint32_t n) -> const TileInfo& { return ring[n % kRing]; };
+      bool ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL), 0, ctl, &abort_flag));
+      bool any = ok && info(0).ord >= 0;
+      if (any && c.pages > 0) {
+        const uint8_t* src = c.data + info(0).off[w];
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src + to_values, k, lane);
+      }
+      for (uint32_t n = 0; any; ++n) {
+        const uint32_t slot = n & 1, ph = (n >> 1) & 1;
+        const int ord = info(n).ord;
+        const bool clean = info(n).clean;
+        const uint8_t valid_bits = info(n).valid;
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL + (n + 1) % kRing), ((n + 1) / kRing) & 1, ctl, &abort_flag)))
+          break;
+        any = info(n + 1).ord >= 0;
+        // (the words' loads have no branch of their own kind's: they stay in flight until used)
+        const uint8_t* src = c.data + info(n + 1).off[w];
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(KFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
+        {
+          const uint32_t to = sK + slot * C::KV;
+#pragma unroll
+          for (int k = 0; k < BLK; ++k) {
+            uint32_t kb[2][4];
+            key_operand(kw[k], kb);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int row = key0 + 2 * q, chunk = (k & 1) * 4 + t4;
+              sts128(to + (k >> 1) * C::CHUNK + row * 128 + ((chunk ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2],
+                     kb[q][3]);
+            }
+          }
+          if (lane == 0 && w == 0) *reinterpret_cast<volatile uint8_t*>(&valid[n & 7]) = valid_bits;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(KFULL + slot));
+        }
+        if (any && c.pages > 0) {
+#pragma unroll
+          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(VFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
+        {
+          if (clean) {
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < BLK; ++k) bad |= clean_words(vw[k]);
+            if (bad) *reinterpret_cast<volatile int*>(&poison[ord & 3]) = ord;
+          }
+          const uint32_t to = sV + slot * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
+          const int chunk = (w & 3) * 2 + (t4 >> 1);
+#pragma unroll
+          for (int k = 0; k < BLK; ++k) {
+            uint32_t vb[4][2];
+            value_operand(vw[k], vb);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row = 32 * k + 8 * q + g;
+              sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(VFULL + slot));
+            mbar_arrive(bar(RFREE + n % kRing));
+          }
+        }
+        if (any && c.pages > 0) {
+#pragma unroll
+          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src + to_values, k, lane);
+        }
+      }
     } else {
       fewer_regs<kRegsMma>();
+    }
+    if (warp == kMmaWarp + 1) {
+      // ---------------- the scheduler: a granule of each tile a lane ----------------
+      uint32_t n = 0;
+      bool ok = true;
+      auto slot_free = [&] {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFREE + n % kRing), ((n / kRing) & 1) ^ 1, ctl, &abort_flag));
+        return ok;
+      };
+      for (int ord = 0; ok && walk.next(c, b, a, sg); ++ord) {
+        const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
+        const int end = min(sg.sq.len, sg.b.maxpos + 1);
+        for (int i = sg.begin; i < sg.end; ++i, ++n) {
+          const int t = sg.b.t0 + i, pos = t * BN + (lane & 7) * kGranule;
+          const bool there = pos < end;
+          const int page = there ? __ldg(table + pos / c.page_tokens) : -1;
+          const bool paged = page >= 0 && page < c.pages;
+          if (there && !paged) report_index(ctl.status);
+          // A granule without a page of its own loads page 0's: its scores are hidden, so
+          // its keys do not matter, and its values only have to be finite (cleaned).
+          const long long off = granule_offset(c, paged ? page : 0, 0, sg.head, pos, GB);
+          const uint32_t valid_bits = __ballot_sync(0xFFFFFFFFu, paged || !there) & 0xFFu;
+          if (!slot_free()) break;
+          TileInfo& x = ring[n % kRing];
+          if (lane < 8) x.off[lane] = off;
+          if (lane == 0) {
+            x.ord = ord;
+            x.clean = tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu;
+            x.valid = static_cast<uint8_t>(valid_bits);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(RFULL + n % kRing));
+        }
+      }
+      if (ok && slot_free()) {
+        if (lane < 8) ring[n % kRing].off[lane] = 0;
+        if (lane == 0) {
+          ring[n % kRing].ord = -1;
+          mbar_arrive(bar(RFULL + n % kRing));
+        }
+      }
+      __syncwarp();
     }
     if (warp == kMmaWarp) {
       // ---------------- the matrix instructions ----------------
@@ -686,11 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) {  // every product issued ends before tensor memory is freed
-        if (lane == 0) {
-          tc_commit(bar(DRAIN));
-          volatile int no_abort = 0;
-          (void)mbar_wait(bar(DRAIN), 0, ctl, &no_abort);
-        }
+        commit_one(bar(DRAIN), one);
+        volatile int no_abort = 0;
+        (void)mbar_wait(bar(DRAIN), 0, ctl, &no_abort);
         __syncwarp();
       }
     }
