@@ -32,6 +32,7 @@ __device__ __forceinline__ float ex2(float x) {
 // mbar_wait (rg_internal.cuh), the clock first read after some thousand tries.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
                                          volatile int* abort_flag) {
+#pragma unroll 1
   for (uint32_t it = 0; it < 4096; ++it)
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, ctl, abort_flag);

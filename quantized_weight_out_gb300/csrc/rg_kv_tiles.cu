@@ -34,8 +34,8 @@ constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
 // Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 136 for
-// the softmax, 256 x 88 for the decoders and 128 x 32 for the rest, the same.
-constexpr int kRegsSoft = 136, kRegsDec = 88, kRegsMma = 32;
+// the softmax, 256 x 80 for the decoders and 128 x 40 for the rest, 60416.
+constexpr int kRegsSoft = 136, kRegsDec = 80, kRegsMma = 40;
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -80,7 +80,7 @@ struct Segment {
   int seq, head, rb, begin, end;
   long long last;  // the line's index of the item's last tile
 };
-// Walks a CTA's share; every role walks it for itself.
+// Walks a CTA's share (the scheduler warp).
 struct Walk {
   long long at, hi;
   int seq, head, rb, tile, nrb;
@@ -233,8 +233,10 @@ struct TileInfo {
   int ord;            // segment; -1: no more tiles
   uint8_t clean;      // values are checked: some row may not see them all
   uint8_t valid;      // bit g: granule g's tokens are there, or hidden by position
+  uint8_t two;        // both streams have rows
+  uint8_t edge;       // 1: the segment's first tile, 2: its last
 };
-constexpr int kRing = 8;
+constexpr int kRing = 8, kSegs = 4;
 
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -243,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool BF = TYPE == RG_BF16;
   constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[17 + 2 * kRing];
+  __shared__ __align__(8) uint64_t bars[17 + 2 * kRing + 2 * kSegs];
   __shared__ TileInfo ring[kRing];
+  __shared__ Segment segs[kSegs];                       // begin -1: no more
   __shared__ uint8_t valid[8];                          // by tile ordinal: TileInfo's valid
   __shared__ int poison[4];                             // by segment ordinal: values left out of the product
   __shared__ uint32_t tmem_slot;
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
   // barriers: two of each kind
   constexpr int KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, ODONE = 12, QFULL = 14, DRAIN = 16,
-                RFULL = 17, RFREE = RFULL + kRing;
+                RFULL = 17, RFREE = RFULL + kRing, GFULL = RFREE + kRing, GFREE = GFULL + kSegs;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -273,7 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(DRAIN), 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(RFULL + i), 1);
-      mbar_init(bar(RFREE + i), kDecWarps);
+      mbar_init(bar(RFREE + i), kDecWarps + 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(bar(GFULL + i), 1);
+      mbar_init(bar(GFREE + i), kSoftWarps);
     }
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) poison[i] = -1;
@@ -373,8 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   if (lo < hi) {
-    Walk walk = sh_walk;
-    Segment sg;
     if (warp < kSoftWarps) {
       // ---------------- softmax: a row a thread ----------------
       more_regs<kRegsSoft>();
@@ -387,10 +392,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_s = 0;      // tiles this stream has had
       uint32_t tile_no = 0;  // tiles of the CTA
       bool ok = true, headed = false;
-      for (int ord = 0; ok && walk.next(c, b, a, sg); ++ord) {
+      for (int ord = 0;; ++ord) {
+        const uint32_t gfree = bar(GFREE + ord % kSegs);
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(GFULL + ord % kSegs), (ord / kSegs) & 1, ctl, &abort_flag));
+        const Segment& sg = segs[ord % kSegs];
+        if (!ok || sg.begin < 0) break;
         const int row = h * 128 + r;
         if (h == 1 && sg.b.rows <= 128) {
           tile_no += sg.end - sg.begin;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(gfree);
           continue;
         }
         const bool real = row < sg.b.rows;
@@ -509,28 +520,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[row] = m_ref;
           part[BM + row] = l;
         }
+        if (__any_sync(0xFFFFFFFFu, left_out)) {
+          // values that are not finite, to the rows that see them (a column at a time: rare)
+          const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
+#pragma unroll 1
+          for (int d = 0; d < D; ++d) {
+            float add = 0.0f;
+#pragma unroll 1
+            for (int j = (sg.b.t0 + sg.begin) * BN; j < (sg.b.t0 + sg.end) * BN && j <= pos; ++j) {
+              if ((a.window && j <= pos - a.window) || !tile_masked(sg.b, a.window, j / BN)) continue;
+              const int page = table[j / c.page_tokens];
+              if (page < 0 || page >= c.pages) continue;
+              add += value_not_finite<TYPE, D>(c.data + granule_offset(c, page, 1, sg.head, j, GB), j % kGranule, d);
+            }
+            __syncwarp();
+            uint32_t o;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                         : "=r"(o) : "r"(tO + d) : "memory");
+            o = __float_as_uint(__uint_as_float(o) + add);
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tO + d), "r"(o) : "memory");
+            tmem_wait_st();
+          }
+        }
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(tO + 32 * k, o);
-          if (left_out && real) {
-            // values that are not finite, to the rows that see them
-            const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
-            for (int i = sg.begin; i < sg.end; ++i) {
-              const int t = sg.b.t0 + i;
-              if (!tile_masked(sg.b, a.window, t)) continue;
-              for (int j = t * BN; j < t * BN + BN && j <= pos; ++j) {
-                if (a.window && j <= pos - a.window) continue;
-                const int page = table[j / c.page_tokens];
-                if (page < 0 || page >= c.pages) continue;
-                const uint8_t* src = c.data + granule_offset(c, page, 1, sg.head, j, GB);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) +
-                                         value_not_finite<TYPE, D>(src, j % kGranule, 32 * k + e));
-              }
-            }
-          }
           if (real) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -550,6 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           desc[blockIdx.x] = Desc{static_cast<int>(sg.last / per), sg.b.rows, sg.sq.start + sg.rb * BM / a.group,
                                   sg.rb * BM % a.group, sg.head};
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(gfree);
       }
       if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
     } else if (warp < kSoftWarps + kDecWarps) {
@@ -640,13 +657,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kMmaWarp + 1) {
       // ---------------- the scheduler: a granule of each tile a lane ----------------
+      Walk walk = sh_walk;
+      Segment sg;
       uint32_t n = 0;
+      int ord = 0;
       bool ok = true;
       auto slot_free = [&] {
         ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFREE + n % kRing), ((n / kRing) & 1) ^ 1, ctl, &abort_flag));
         return ok;
       };
-      for (int ord = 0; ok && walk.next(c, b, a, sg); ++ord) {
+      auto segment_free = [&] {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(GFREE + ord % kSegs), ((ord / kSegs) & 1) ^ 1, ctl, &abort_flag));
+        return ok;
+      };
+      for (; ok && walk.next(c, b, a, sg); ++ord) {
+        if (!segment_free()) break;
+        if (lane == 0) {
+          segs[ord % kSegs] = sg;
+          mbar_arrive(bar(GFULL + ord % kSegs));
+        }
+        __syncwarp();
         const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
         const int end = min(sg.sq.len, sg.b.maxpos + 1);
         for (int i = sg.begin; i < sg.end; ++i, ++n) {
@@ -666,6 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.ord = ord;
             x.clean = tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu;
             x.valid = static_cast<uint8_t>(valid_bits);
+            x.two = sg.b.rows > 128;
+            x.edge = (i == sg.begin ? 1 : 0) | (i + 1 == sg.end ? 2 : 0);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(RFULL + n % kRing));
@@ -676,6 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ring[n % kRing].ord = -1;
           mbar_arrive(bar(RFULL + n % kRing));
+        }
+        if (segment_free() && lane == 0) {
+          segs[ord % kSegs].begin = -1;
+          mbar_arrive(bar(GFULL + ord % kSegs));
         }
       }
       __syncwarp();
@@ -713,32 +749,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_one(bar(ODONE + h), one);
         if (frees) commit_one(bar(VFREE + slot), one);
       };
-      while (ok && walk.next(c, b, a, sg)) {
-        const bool two = uniform(sg.b.rows) > 128;
-        const int count = uniform(sg.end - sg.begin);
-        if (!wait(QFULL, q0++ & 1)) break;
-        if (two && !wait(QFULL + 1, q1++ & 1)) break;
-        if (!wait(KFULL + (n & 1), (n >> 1) & 1)) break;
-        scores(0, n & 1);
-        if (two) scores(1, n & 1);
-        commit_one(bar(KFREE + (n & 1)), one);
-        for (int i = 0; i < count; ++i, ++n) {
-          const uint32_t slot = n & 1, next = (n + 1) & 1;
-          const bool more = i + 1 < count;
-          if (!wait(VFULL + slot, (n >> 1) & 1)) break;
-          if (!wait(PFULL, n0++ & 1)) break;
-          product(0, slot, i == 0, !two);
-          if (more) {
-            if (!wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
-            scores(0, next);
-          }
-          if (two) {
-            if (!wait(PFULL + 1, n1++ & 1)) break;
-            product(1, slot, i == 0, true);
-            if (more) scores(1, next);
-          }
-          if (more) commit_one(bar(KFREE + next), one);
+      while (ok) {
+        // (a tile's products, with the next tile's scores issued in between)
+        if (!wait(RFULL + n % kRing, (n / kRing) & 1)) break;
+        if (uniform(ring[n % kRing].ord) < 0) break;
+        const bool two = uniform(ring[n % kRing].two) != 0;
+        const int edge = uniform(ring[n % kRing].edge);
+        const bool first = edge & 1, more = !(edge & 2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(RFREE + n % kRing));
+        const uint32_t slot = n & 1, next = (n + 1) & 1;
+        if (first) {
+          if (!wait(QFULL, q0++ & 1)) break;
+          if (two && !wait(QFULL + 1, q1++ & 1)) break;
+          if (!wait(KFULL + slot, (n >> 1) & 1)) break;
+          scores(0, slot);
+          if (two) scores(1, slot);
+          commit_one(bar(KFREE + slot), one);
         }
+        if (!wait(VFULL + slot, (n >> 1) & 1)) break;
+        if (!wait(PFULL, n0++ & 1)) break;
+        product(0, slot, first, !two);
+        if (more) {
+          if (!wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
+          scores(0, next);
+        }
+        if (two) {
+          if (!wait(PFULL + 1, n1++ & 1)) break;
+          product(1, slot, first, true);
+          if (more) scores(1, next);
+        }
+        if (more) commit_one(bar(KFREE + next), one);
+        ++n;
       }
       if (!ok) {  // every product issued ends before tensor memory is freed
         commit_one(bar(DRAIN), one);
