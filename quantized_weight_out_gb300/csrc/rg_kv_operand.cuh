@@ -29,13 +29,26 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// mbar_wait (rg_internal.cuh), the clock first read after some thousand tries.
+// mbar_wait (rg_internal.cuh) as a few instructions: the abort flag and the
+// clock are looked at every 4096 tries, in code that stands apart.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
                                          volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  uint32_t it = 0;
 #pragma unroll 1
-  for (uint32_t it = 0; it < 4096; ++it)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, ctl, abort_flag);
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++it & 4095u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag) return false;
+      if (now - t0 > ctl.limit_ns) {
+        *abort_flag = 1;
+        report_timeout(ctl.status);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 // Contiguous bytes (a multiple of 16, both addresses 16-byte aligned) from

@@ -197,6 +197,30 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
   // (an asm statement takes 30 operands at most)
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two F32 at once
@@ -230,12 +254,12 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
 // ahead, so that they wait for no page number and walk nothing.
 struct TileInfo {
   long long off[8];   // byte offset of each granule's keys
-  int ord;            // segment; -1: no more tiles
-  uint8_t clean;      // values are checked: some row may not see them all
-  uint8_t valid;      // bit g: granule g's tokens are there, or hidden by position
-  uint8_t two;        // both streams have rows
-  uint8_t edge;       // 1: the segment's first tile, 2: its last
+  int flags;          // kEnd: no more tiles; kFirst, kLast: of its segment; kTwo: both streams have
+                      // rows; kClean: values are checked, some row may not see them all
+  int ord;            // segment
+  int valid;          // bit g: granule g's tokens are there, or hidden by position
 };
+constexpr int kEnd = 1, kFirst = 2, kLast = 4, kTwo = 8, kClean = 16;
 constexpr int kRing = 8, kSegs = 4;
 
 template <int TYPE, int D>
@@ -273,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(ODONE + i), 1);
       mbar_init(bar(QFULL + i), 4);
     }
-    mbar_init(bar(DRAIN), 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(RFULL + i), 1);
       mbar_init(bar(RFREE + i), kDecWarps + 1);
@@ -282,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(GFULL + i), 1);
       mbar_init(bar(GFREE + i), kSoftWarps);
     }
+    mbar_init(bar(DRAIN), 1);
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) poison[i] = -1;
     fence_mbar_init();
@@ -389,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a scale of zero stands for a tiny one: hidden scores are -inf, and -inf x 0 is NaN)
       const float cz = fmaxf(fabsf(a.scale_log2), 1e-37f);
       const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-      uint32_t n_s = 0;      // tiles this stream has had
+      uint32_t n_s = 0, n_seg = 0;  // tiles and segments this stream has had
       uint32_t tile_no = 0;  // tiles of the CTA
       bool ok = true, headed = false;
       for (int ord = 0;; ++ord) {
@@ -455,15 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t cz2 = pack_f2(cz, cz), off2 = pack_f2(off, off);
             float top = kNone;
             uint64_t sum2 = 0;
-            uint32_t s[2][32];
-            tmem_ld32(tS, s[0]);
+            uint32_t s[2][16];
+            tmem_ld16(tS, s[0]);
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              uint32_t(&x)[32] = s[k4 & 1];
+            for (int k4 = 0; k4 < 8; ++k4) {
+              uint32_t(&x)[16] = s[k4 & 1];
               tmem_wait_ld(x);
-              if (k4 < 3) tmem_ld32(tS + 32 * (k4 + 1), s[(k4 + 1) & 1]);
+              if (k4 < 7) tmem_ld16(tS + 16 * (k4 + 1), s[(k4 + 1) & 1]);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
+              for (int k = 0; k < 8; ++k) {
                 const float s0 = __uint_as_float(x[2 * k]), s1 = __uint_as_float(x[2 * k + 1]);
                 top = fmaxf(top, fmaxf(s0, s1));
                 float e0, e1;
@@ -471,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum2 = add_f2(sum2, pack_f2(e0, e1));
-                p[16 * k4 + k] = pack16<BF>(e0, e1);
+                p[8 * k4 + k] = pack16<BF>(e0, e1);
               }
             }
             float sx, sy;
@@ -482,10 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float v = fmaxf(top, m_ref), f = ex2(m_ref - v);
             m_ref = v;
             if (i > sg.begin) {
-              // rescale what has been accumulated, once the last product is in
-              ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
-              if (!ok) break;
-              tc_fence_after();
+              // rescale what has been accumulated (the last product was issued before this
+              // tile's scores, whose commit covers it)
               l *= f;
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
@@ -498,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (m_ref == INFINITY) break;  // (a score of +inf: the row is NaN)
           }
-          if (!ok) break;
           l += sum;
           tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(p));
           tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // the result, or this CTA's part of it
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), (n_s - 1) & 1, ctl, &abort_flag));
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), n_seg++ & 1, ctl, &abort_flag));
         if (!ok) break;
         tc_fence_after();
         const bool starts = sg.begin == 0, ends = sg.end == sg.b.nt;
@@ -579,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ValueWords<TYPE> vw[BLK] = {};
       auto info = [&](uint32_t n) -> const TileInfo& { return ring[n % kRing]; };
       bool ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL), 0, ctl, &abort_flag));
-      bool any = ok && info(0).ord >= 0;
+      bool any = ok && !(info(0).flags & kEnd);
       if (any && c.pages > 0) {
         const uint8_t* src = c.data + info(0).off[w];
 #pragma unroll
@@ -590,11 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t n = 0; any; ++n) {
         const uint32_t slot = n & 1, ph = (n >> 1) & 1;
         const int ord = info(n).ord;
-        const bool clean = info(n).clean;
-        const uint8_t valid_bits = info(n).valid;
+        const bool clean = info(n).flags & kClean;
+        const uint8_t valid_bits = static_cast<uint8_t>(info(n).valid);
         if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL + (n + 1) % kRing), ((n + 1) / kRing) & 1, ctl, &abort_flag)))
           break;
-        any = info(n + 1).ord >= 0;
+        any = !(info(n + 1).flags & kEnd);
         // (the words' loads have no branch of their own kind's: they stay in flight until used)
         const uint8_t* src = c.data + info(n + 1).off[w];
         if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(KFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
@@ -694,10 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < 8) x.off[lane] = off;
           if (lane == 0) {
             x.ord = ord;
-            x.clean = tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu;
-            x.valid = static_cast<uint8_t>(valid_bits);
-            x.two = sg.b.rows > 128;
-            x.edge = (i == sg.begin ? 1 : 0) | (i + 1 == sg.end ? 2 : 0);
+            x.valid = static_cast<int>(valid_bits);
+            x.flags = (i == sg.begin ? kFirst : 0) | (i + 1 == sg.end ? kLast : 0) | (sg.b.rows > 128 ? kTwo : 0) |
+                      (tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu ? kClean : 0);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(RFULL + n % kRing));
@@ -706,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && slot_free()) {
         if (lane < 8) ring[n % kRing].off[lane] = 0;
         if (lane == 0) {
-          ring[n % kRing].ord = -1;
+          ring[n % kRing].flags = kEnd;
           mbar_arrive(bar(RFULL + n % kRing));
         }
         if (segment_free() && lane == 0) {
@@ -718,19 +738,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kMmaWarp) {
       // ---------------- the matrix instructions ----------------
-      // (the whole warp walks and waits, so that operands stay warp-uniform; one lane issues)
+      // (the whole warp waits, so that operands stay warp-uniform; one lane issues.  One
+      // warp for both streams: their products alternate, so that one stream's softmax
+      // runs while the other has the tensor core; a warp a stream fell into step and was
+      // slower)
       constexpr uint32_t idS = idesc_f16(BF, 128, BN, false, false);
       constexpr uint32_t idO = idesc_f16(BF, 128, D, false, false);
       const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024);
-      uint32_t n = 0, n0 = 0, n1 = 0, q0 = 0, q1 = 0;  // tiles; tiles and segments of each stream
+      const uint32_t one = elect_one();
+      const uint32_t tm = uniform(tmem);
+      uint32_t n = 0, n1 = 0, q0 = 0, q1 = 0;  // tiles; stream 1's tiles; segments of each
       bool ok = true;
       auto wait = [&](int i, uint32_t parity) {
         ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity, ctl, &abort_flag));
-        tc_fence_after();
         return ok;
       };
-      const uint32_t one = elect_one();
-      const uint32_t tm = uniform(tmem);
       auto scores = [&](int h, uint32_t slot) {
         const uint64_t q = dQ + h * (C::Q >> 4), k = dK + slot * (C::KV >> 4);
 #pragma unroll
@@ -740,56 +762,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit_one(bar(SFULL + h), one);
       };
-      auto product = [&](int h, uint32_t slot, bool first, bool frees) {
+      auto product = [&](int h, uint32_t slot, bool first) {
         const uint64_t v = dV + slot * (C::KV >> 4);
 #pragma unroll
         for (int i = 0; i < BN / 16; ++i)
           mma_ts(tm + kColO + h * 128, tm + h * 128 + 8 * i, v + (((i >> 2) * C::VCHUNK + (i & 3) * 32) >> 4), idO,
                  i != 0 || !first, one);
-        commit_one(bar(ODONE + h), one);
-        if (frees) commit_one(bar(VFREE + slot), one);
       };
-      while (ok) {
-        // (a tile's products, with the next tile's scores issued in between)
-        if (!wait(RFULL + n % kRing, (n / kRing) & 1)) break;
-        if (uniform(ring[n % kRing].ord) < 0) break;
-        const bool two = uniform(ring[n % kRing].two) != 0;
-        const int edge = uniform(ring[n % kRing].edge);
-        const bool first = edge & 1, more = !(edge & 2);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(RFREE + n % kRing));
+      while (wait(RFULL + n % kRing, (n / kRing) & 1)) {
+        const int flags = uniform(ring[n % kRing].flags);
+        if (flags & kEnd) break;
+        if (one) mbar_arrive(bar(RFREE + n % kRing));
         const uint32_t slot = n & 1, next = (n + 1) & 1;
+        const bool two = flags & kTwo, first = flags & kFirst, more = !(flags & kLast);
         if (first) {
           if (!wait(QFULL, q0++ & 1)) break;
           if (two && !wait(QFULL + 1, q1++ & 1)) break;
           if (!wait(KFULL + slot, (n >> 1) & 1)) break;
+          tc_fence_after();
           scores(0, slot);
           if (two) scores(1, slot);
           commit_one(bar(KFREE + slot), one);
         }
         if (!wait(VFULL + slot, (n >> 1) & 1)) break;
-        if (!wait(PFULL, n0++ & 1)) break;
-        product(0, slot, first, !two);
-        if (more) {
-          if (!wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
+        if (more && !wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
+        if (!wait(PFULL, n & 1)) break;
+        tc_fence_after();
+        product(0, slot, first);
+        if (more)
           scores(0, next);
-        }
+        else
+          commit_one(bar(ODONE), one);
         if (two) {
           if (!wait(PFULL + 1, n1++ & 1)) break;
-          product(1, slot, first, true);
-          if (more) scores(1, next);
+          tc_fence_after();
+          product(1, slot, first);
+          if (more)
+            scores(1, next);
+          else
+            commit_one(bar(ODONE + 1), one);
         }
         if (more) commit_one(bar(KFREE + next), one);
+        commit_one(bar(VFREE + slot), one);
         ++n;
       }
       if (!ok) {  // every product issued ends before tensor memory is freed
         commit_one(bar(DRAIN), one);
         volatile int no_abort = 0;
         (void)mbar_wait(bar(DRAIN), 0, ctl, &no_abort);
-        __syncwarp();
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (tid == 0) {
     desc[blockIdx.x].last = -1;
   }
