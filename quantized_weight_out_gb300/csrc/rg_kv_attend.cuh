@@ -37,10 +37,9 @@ __device__ __forceinline__ void store_out(const Attend& a, int token, int head, 
         make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-// Eight query values as four operand words; finite values beyond fp16 are reported.
+// Eight query values from element `at` on as four operand words; finite values beyond fp16 are reported.
 template <bool BF>
-__device__ __forceinline__ uint4 query8(const Attend& a, int token, int head, int d, int* status) {
-  const int64_t at = token * a.q_t + head * a.q_h + d;
+__device__ __forceinline__ uint4 query8(const Attend& a, int64_t at, int* status) {
   float x[8];
   if (a.atype == RG_F32) {
     load8<RG_F32>(a.q, at, x);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
 #pragma unroll
           for (int k = 0; k < BLK; ++k)
             qreg[m][k][r] =
-                row < rows ? query8<BF>(a, tok, hd, 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
+                row < rows ? query8<BF>(a, tok * a.q_t + hd * a.q_h + 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
         }
     } else {
       for (int u = warp; u < MT * BLK * 2; u += kWarps) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
         const int row = 16 * m + 8 * r + g;
         const int tok = sq.start + (row0 + row) / G, hd = head * G + (row0 + row) % G;
         reinterpret_cast<uint4*>(smem)[u * 32 + lane] =
-            row < rows ? query8<BF>(a, tok, hd, 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
+            row < rows ? query8<BF>(a, tok * a.q_t + hd * a.q_h + 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
       }
       __syncthreads();
     }

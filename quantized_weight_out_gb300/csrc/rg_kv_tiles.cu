@@ -33,9 +33,9 @@ constexpr int BM = 256;          // rows of an item
 constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
-// Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 136 for
-// the softmax, 256 x 80 for the decoders and 128 x 40 for the rest, 60416.
-constexpr int kRegsSoft = 136, kRegsDec = 80, kRegsMma = 40;
+// Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 152 for
+// the softmax, 256 x 72 for the decoders and 128 x 32 for the rest, the same.
+constexpr int kRegsSoft = 152, kRegsDec = 72, kRegsMma = 32;
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -78,6 +78,7 @@ struct Segment {
   Seq sq;
   Block b;
   int seq, head, rb, begin, end;
+  bool holes;      // a page that is not there
   long long last;  // the line's index of the item's last tile
 };
 // Walks a CTA's share (the scheduler warp).
@@ -197,30 +198,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
   // (an asm statement takes 30 operands at most)
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
-      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two F32 at once
@@ -254,12 +231,11 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
 // ahead, so that they wait for no page number and walk nothing.
 struct TileInfo {
   long long off[8];   // byte offset of each granule's keys
-  int flags;          // kEnd: no more tiles; kFirst, kLast: of its segment; kTwo: both streams have
-                      // rows; kClean: values are checked, some row may not see them all
+  int flags;          // kEnd: no more tiles; kClean: values are checked, some row may not see them all
   int ord;            // segment
   int valid;          // bit g: granule g's tokens are there, or hidden by position
 };
-constexpr int kEnd = 1, kFirst = 2, kLast = 4, kTwo = 8, kClean = 16;
+constexpr int kEnd = 1, kClean = 2;
 constexpr int kRing = 8, kSegs = 4;
 
 template <int TYPE, int D>
@@ -269,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool BF = TYPE == RG_BF16;
   constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[17 + 2 * kRing + 2 * kSegs];
+  __shared__ __align__(8) uint64_t bars[13 + 2 * kRing + 2 * kSegs];
   __shared__ TileInfo ring[kRing];
   __shared__ Segment segs[kSegs];                       // begin -1: no more
   __shared__ uint8_t valid[8];                          // by tile ordinal: TileInfo's valid
@@ -283,15 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = base, sK = base + 2 * C::Q, sV = sK + 2 * C::KV;
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
   // barriers: two of each kind
-  constexpr int KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, ODONE = 12, QFULL = 14, DRAIN = 16,
-                RFULL = 17, RFREE = RFULL + kRing, GFULL = RFREE + kRing, GFREE = GFULL + kSegs;
+  constexpr int FULL = 0, FREE = 2, SFULL = 4, PFULL = 6, ODONE = 8, QFULL = 10, DRAIN = 12, RFULL = 13,
+                RFREE = RFULL + kRing, GFULL = RFREE + kRing, GFREE = GFULL + kSegs;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(KFULL + i), kDecWarps);
-      mbar_init(bar(KFREE + i), 1);
-      mbar_init(bar(VFULL + i), kDecWarps);
-      mbar_init(bar(VFREE + i), 1);
+      mbar_init(bar(FULL + i), kDecWarps);
+      mbar_init(bar(FREE + i), 1);
       mbar_init(bar(SFULL + i), 1);
       mbar_init(bar(PFULL + i), 4);
       mbar_init(bar(ODONE + i), 1);
@@ -299,11 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(RFULL + i), 1);
-      mbar_init(bar(RFREE + i), kDecWarps + 1);
+      mbar_init(bar(RFREE + i), kDecWarps);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(GFULL + i), 1);
-      mbar_init(bar(GFREE + i), kSoftWarps);
+      mbar_init(bar(GFREE + i), kSoftWarps + 1);
     }
     mbar_init(bar(DRAIN), 1);
     abort_flag = 0;
@@ -414,49 +388,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float cz = fmaxf(fabsf(a.scale_log2), 1e-37f);
       const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
       uint32_t n_s = 0, n_seg = 0;  // tiles and segments this stream has had
-      uint32_t tile_no = 0;  // tiles of the CTA
+      uint32_t tile_no = 0;         // tiles of the CTA
       bool ok = true, headed = false;
-      for (int ord = 0;; ++ord) {
-        const uint32_t gfree = bar(GFREE + ord % kSegs);
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(GFULL + ord % kSegs), (ord / kSegs) & 1, ctl, &abort_flag));
-        const Segment& sg = segs[ord % kSegs];
-        if (!ok || sg.begin < 0) break;
-        const int row = h * 128 + r;
-        if (h == 1 && sg.b.rows <= 128) {
-          tile_no += sg.end - sg.begin;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(gfree);
+      auto segment = [&](int ord) -> const Segment& { return segs[ord % kSegs]; };
+      auto wait_segment = [&](int ord) {
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(GFULL + ord % kSegs), (ord / kSegs) & 1, ctl, &abort_flag));
+        return ok && segment(ord).begin >= 0;
+      };
+      auto release = [&](int ord) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(GFREE + ord % kSegs));
+      };
+      auto mine = [&](int ord) { return h == 0 || segment(ord).b.rows > 128; };
+      // a segment's queries into shared memory: the lanes of a group take a row's 16-byte words
+      auto load_queries = [&](const Segment& sg) {
+        constexpr int LR = D / 8, RI = 32 / LR;  // lanes a row, rows at a time
+        const int grow = sg.rb * BM + h * 128 + r;
+        const int64_t at = (sg.sq.start + grow / a.group) * a.q_t + (sg.head * a.group + grow % a.group) * a.q_h;
+        const int real = h * 128 + r < sg.b.rows;
+        auto put = [&](int from, uint4 v) {
+          const int row = (warp & 3) * 32 + from, word = lane % LR;
+          sts128(sQ + h * C::Q + (word >> 3) * C::CHUNK + row * 128 + (((word & 7) ^ (row & 7)) << 4), v.x ^ flip,
+                 v.y ^ flip, v.z ^ flip, v.w ^ flip);
+        };
+        if (a.atype == (BF ? RG_BF16 : RG_F16)) {
+          // already the operand type: eight loads at a time (rows that do not exist read
+          // the segment's first instead, and become zeros)
+          const int64_t first = sg.sq.start * a.q_t + static_cast<int64_t>(sg.head) * a.group * a.q_h;
+#pragma unroll 1
+          for (int k0 = 0; k0 < 32 / RI; k0 += 8) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int from = (k0 + k) * RI + lane / LR;
+              const int64_t src = __shfl_sync(0xFFFFFFFFu, real ? at : first, from) + 8 * (lane % LR);
+              v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + src));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int from = (k0 + k) * RI + lane / LR;
+              const bool there = __shfl_sync(0xFFFFFFFFu, real, from);
+              put(from, there ? v[k] : make_uint4(0, 0, 0, 0));
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 32 / RI; ++k) {
+            const int from = k * RI + lane / LR;
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, at, from);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (__shfl_sync(0xFFFFFFFFu, real, from)) v = query8<BF>(a, src + 8 * (lane % LR), ctl.status);
+            put(from, v);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(QFULL + h));
+      };
+      bool loaded = false;
+      for (int ord = 0; wait_segment(ord); ++ord) {
+        const Segment& sg = segment(ord);
+        const int begin = sg.begin, end = sg.end, t0 = sg.b.t0, minpos = sg.b.minpos, maxpos = sg.b.maxpos;
+        if (!mine(ord)) {
+          tile_no += end - begin;
+          release(ord);
           continue;
         }
+        if (!loaded) load_queries(sg);
+        loaded = false;
+        const bool holes = sg.holes;
+        const int row = h * 128 + r, grow = sg.rb * BM + row;
         const bool real = row < sg.b.rows;
-        const int grow = sg.rb * BM + row;
         const int pos = real ? sg.sq.len - sg.sq.n + grow / a.group : -1;
-        const int tok = sg.sq.start + grow / a.group, hd = sg.head * a.group + grow % a.group;
-        {
-          const uint32_t to = sQ + h * C::Q + r * 128;
-#pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (real) v = query8<BF>(a, tok, hd, 8 * k, ctl.status);
-            sts128(to + (k >> 3) * C::CHUNK + (((k & 7) ^ (r & 7)) << 4), v.x ^ flip, v.y ^ flip, v.z ^ flip,
-                   v.w ^ flip);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(QFULL + h));
-        }
         float m_ref = kNone, l = 0.0f;
-        for (int i = sg.begin; i < sg.end; ++i, ++tile_no, ++n_s) {
-          const int t = sg.b.t0 + i;
+        for (int i = begin; i < end; ++i, ++tile_no, ++n_s) {
+          const int t = t0 + i;
           ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(SFULL + h), n_s & 1, ctl, &abort_flag));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t granules = *reinterpret_cast<const volatile uint8_t*>(&valid[tile_no & 7]);
-          const bool masked = tile_masked(sg.b, a.window, t) || granules != 0xFFu;
-          // columns (lim_lo, lim_hi] of the tile are visible to this row
-          const int lim_hi = pos - t * BN, lim_lo = a.window ? pos - a.window - t * BN : -1;
-          if (masked) {
-            // hidden scores become -inf in tensor memory: the passes below have no mask
+          if (holes || t * BN + BN - 1 > minpos || (a.window && t * BN <= maxpos - a.window)) {
+            // hidden scores become -inf in tensor memory: the pass below has no mask
+            const uint32_t granules = holes ? *reinterpret_cast<const volatile uint8_t*>(&valid[tile_no & 7]) : 0xFFu;
+            // columns (lim_lo, lim_hi] of the tile are visible to this row
+            const int lim_hi = pos - t * BN, lim_lo = a.window ? pos - a.window - t * BN : -1;
 #pragma unroll 1
             for (int c0 = 0; c0 < BN; c0 += 32) {
               const bool g0 = (granules >> (c0 / 16)) & 1, g1 = (granules >> (c0 / 16 + 1)) & 1;
@@ -479,15 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t cz2 = pack_f2(cz, cz), off2 = pack_f2(off, off);
             float top = kNone;
             uint64_t sum2 = 0;
-            uint32_t s[2][16];
-            tmem_ld16(tS, s[0]);
+            auto take = [&](const uint32_t (&x)[32], int c0) {
 #pragma unroll
-            for (int k4 = 0; k4 < 8; ++k4) {
-              uint32_t(&x)[16] = s[k4 & 1];
-              tmem_wait_ld(x);
-              if (k4 < 7) tmem_ld16(tS + 16 * (k4 + 1), s[(k4 + 1) & 1]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < 16; ++k) {
                 const float s0 = __uint_as_float(x[2 * k]), s1 = __uint_as_float(x[2 * k + 1]);
                 top = fmaxf(top, fmaxf(s0, s1));
                 float e0, e1;
@@ -495,9 +503,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum2 = add_f2(sum2, pack_f2(e0, e1));
-                p[8 * k4 + k] = pack16<BF>(e0, e1);
+                p[c0 / 2 + k] = pack16<BF>(e0, e1);
               }
-            }
+            };
+            uint32_t x0[32], x1[32], y0[32], y1[32];
+            tmem_ld32(tS, x0);
+            tmem_ld32(tS + 32, x1);
+            tmem_wait_ld(x0);
+            tmem_wait_ld(x1);
+            tmem_ld32(tS + 64, y0);
+            tmem_ld32(tS + 96, y1);
+            take(x0, 0);
+            take(x1, 32);
+            tmem_wait_ld(y0);
+            tmem_wait_ld(y1);
+            take(y0, 64);
+            take(y1, 96);
             float sx, sy;
             unpack_f2(sum2, sx, sy);
             sum = sx + sy;
@@ -505,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__any_sync(0xFFFFFFFFu, top > m_ref + kSlack)) break;
             const float v = fmaxf(top, m_ref), f = ex2(m_ref - v);
             m_ref = v;
-            if (i > sg.begin) {
+            if (i > begin) {
               // rescale what has been accumulated (the last product was issued before this
               // tile's scores, whose commit covers it)
               l *= f;
@@ -518,7 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st32(tO + 32 * k, o);
               }
             }
-            if (m_ref == INFINITY) break;  // (a score of +inf: the row is NaN)
           }
           l += sum;
           tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(p));
@@ -529,27 +549,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(PFULL + h));
         }
         if (!ok) break;
+        // the next segment's queries (this one's have been read: its last scores are in)
+        if (wait_segment(ord + 1) && mine(ord + 1)) {
+          load_queries(segment(ord + 1));
+          loaded = true;
+        }
         // the result, or this CTA's part of it
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), n_seg++ & 1, ctl, &abort_flag));
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), n_seg++ & 1, ctl, &abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const bool starts = sg.begin == 0, ends = sg.end == sg.b.nt;
-        const bool left_out = *reinterpret_cast<volatile int*>(&poison[ord & 3]) == ord;
+        const bool starts = begin == 0, ends = end == sg.b.nt;
+        const int64_t to = (sg.sq.start + grow / a.group) * a.o_t + (sg.head * a.group + grow % a.group) * a.o_h;
         float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * part_floats(BM, D);
         const float inv = starts && ends ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         if (!(starts && ends) && real) {
           part[row] = m_ref;
           part[BM + row] = l;
         }
-        if (__any_sync(0xFFFFFFFFu, left_out)) {
+        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord & 3]) == ord)) {
           // values that are not finite, to the rows that see them (a column at a time: rare)
           const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
 #pragma unroll 1
           for (int d = 0; d < D; ++d) {
             float add = 0.0f;
 #pragma unroll 1
-            for (int j = (sg.b.t0 + sg.begin) * BN; j < (sg.b.t0 + sg.end) * BN && j <= pos; ++j) {
-              if ((a.window && j <= pos - a.window) || !tile_masked(sg.b, a.window, j / BN)) continue;
+            for (int j = (t0 + begin) * BN; j < (t0 + end) * BN && j <= pos; ++j) {
+              if ((a.window && j <= pos - a.window) || !(holes || tile_masked(sg.b, a.window, j / BN))) continue;
               const int page = table[j / c.page_tokens];
               if (page < 0 || page >= c.pages) continue;
               add += value_not_finite<TYPE, D>(c.data + granule_offset(c, page, 1, sg.head, j, GB), j % kGranule, d);
@@ -567,15 +592,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(tO + 32 * k, o);
-          if (real) {
+          if (real && !(starts && ends)) {
+            float4* to4 = reinterpret_cast<float4*>(part + 2 * BM + row * D + 32 * k);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float v[4] = {__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                  __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv};
-              if (starts && ends)
-                store_out(a, tok, hd, 32 * k + e, v);
+            for (int e = 0; e < 8; ++e)
+              to4[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          } else if (real) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float v[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(o[8 * e + u]) * inv;
+              const int64_t at = to + 32 * k + 8 * e;
+              if (a.atype == RG_F32)
+                store8<RG_F32>(a.out, at, v);
+              else if (a.atype == RG_F16)
+                store8<RG_F16>(a.out, at, v);
               else
-                *reinterpret_cast<float4*>(part + 2 * BM + row * D + 32 * k + e) = make_float4(v[0], v[1], v[2], v[3]);
+                store8<RG_BF16>(a.out, at, v);
             }
           }
           __syncwarp();
@@ -586,70 +621,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           desc[blockIdx.x] = Desc{static_cast<int>(sg.last / per), sg.b.rows, sg.sq.start + sg.rb * BM / a.group,
                                   sg.rb * BM % a.group, sg.head};
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(gfree);
+        release(ord);
       }
       if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
     } else if (warp < kSoftWarps + kDecWarps) {
       // ---------------- decoders: granule w of every tile ----------------
+      // In pairs: the values of tile j - 1 and the keys of tile j, the order in which the
+      // tensor core needs them; the next pair's words are loaded before the wait for its slots.
       fewer_regs<kRegsDec>();
       const int w = warp - kSoftWarps, g = lane >> 2, t4 = lane & 3;
       const int key0 = 16 * w + 4 * (g >> 1) + (g & 1);
       const long long to_values = c.kv_heads * c.slab_bytes;
+      // (16-bit types have no registers for both: their keys are loaded when they are needed)
+      constexpr bool AHEAD = has_scales(TYPE) || D < 128;
       KeyWords<TYPE> kw[BLK] = {};
       ValueWords<TYPE> vw[BLK] = {};
-      auto info = [&](uint32_t n) -> const TileInfo& { return ring[n % kRing]; };
-      bool ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL), 0, ctl, &abort_flag));
-      bool any = ok && !(info(0).flags & kEnd);
-      if (any && c.pages > 0) {
-        const uint8_t* src = c.data + info(0).off[w];
+      auto load_keys = [&](const uint8_t* src) {
 #pragma unroll
         for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src + to_values, k, lane);
-      }
-      for (uint32_t n = 0; any; ++n) {
-        const uint32_t slot = n & 1, ph = (n >> 1) & 1;
-        const int ord = info(n).ord;
-        const bool clean = info(n).flags & kClean;
-        const uint8_t valid_bits = static_cast<uint8_t>(info(n).valid);
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL + (n + 1) % kRing), ((n + 1) / kRing) & 1, ctl, &abort_flag)))
+      };
+      const bool pages = c.pages > 0;
+      bool any = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL), 0, ctl, &abort_flag)) && !(ring[0].flags & kEnd);
+      const uint8_t* src = c.data + ring[0].off[w];  // tile j's keys
+      if (AHEAD && any && pages) load_keys(src);
+      bool clean = false;
+      int ord = 0;
+      for (uint32_t j = 0; any || j > 0; ++j) {
+        const TileInfo& x = ring[j % kRing];
+        if (j >= 2 &&
+            !__all_sync(0xFFFFFFFFu, wait_bar(bar(FREE + (j & 1)), ((j - 2) >> 1) & 1, ctl, &abort_flag)))
           break;
-        any = !(info(n + 1).flags & kEnd);
-        // (the words' loads have no branch of their own kind's: they stay in flight until used)
-        const uint8_t* src = c.data + info(n + 1).off[w];
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(KFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
-        {
-          const uint32_t to = sK + slot * C::KV;
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) {
-            uint32_t kb[2][4];
-            key_operand(kw[k], kb);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int row = key0 + 2 * q, chunk = (k & 1) * 4 + t4;
-              sts128(to + (k >> 1) * C::CHUNK + row * 128 + ((chunk ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2],
-                     kb[q][3]);
-            }
-          }
-          if (lane == 0 && w == 0) *reinterpret_cast<volatile uint8_t*>(&valid[n & 7]) = valid_bits;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(KFULL + slot));
-        }
-        if (any && c.pages > 0) {
-#pragma unroll
-          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
-        }
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(VFREE + slot), ph ^ 1, ctl, &abort_flag))) break;
-        {
+        if (j > 0) {
           if (clean) {
             bool bad = false;
 #pragma unroll
             for (int k = 0; k < BLK; ++k) bad |= clean_words(vw[k]);
             if (bad) *reinterpret_cast<volatile int*>(&poison[ord & 3]) = ord;
           }
-          const uint32_t to = sV + slot * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
+          const uint32_t to = sV + ((j - 1) & 1) * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
           const int chunk = (w & 3) * 2 + (t4 >> 1);
 #pragma unroll
           for (int k = 0; k < BLK; ++k) {
@@ -661,17 +670,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(VFULL + slot));
-            mbar_arrive(bar(RFREE + n % kRing));
-          }
         }
-        if (any && c.pages > 0) {
+        if (any) {
+          if (!AHEAD && pages) load_keys(src);
+          const uint32_t to = sK + (j & 1) * C::KV;
+// Two blocks (the 128 bytes of a row's chunk) at a time: a quarter warp's stores
+          // are two rows' four words each; where the odd row stores its other block first,
+          // they fall on all eight 16-byte columns.
+#pragma unroll
+          for (int k = 0; k < BLK; k += 2) {
+            uint32_t kb[2][2][4];
+            key_operand(kw[k], kb[0]);
+            key_operand(kw[k + 1], kb[1]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int row = key0 + 2 * q;
+              const uint32_t at = to + (k >> 1) * C::CHUNK + row * 128;
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int blk = u ^ (g & 1);
+                const uint32_t x0 = (g & 1) ? kb[u ^ 1][q][0] : kb[u][q][0], x1 = (g & 1) ? kb[u ^ 1][q][1] : kb[u][q][1];
+                const uint32_t x2 = (g & 1) ? kb[u ^ 1][q][2] : kb[u][q][2], x3 = (g & 1) ? kb[u ^ 1][q][3] : kb[u][q][3];
+                sts128(at + (((blk * 4 + t4) ^ (row & 7)) << 4), x0, x1, x2, x3);
+              }
+            }
+          }
+          if (lane == 0 && w == 0)
+            *reinterpret_cast<volatile uint8_t*>(&valid[j & 7]) = static_cast<uint8_t>(x.valid);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(FULL + (j & 1)));
+          if (j > 0) mbar_arrive(bar(RFREE + (j - 1) % kRing));
+        }
+        if (!any) break;
+        // the next pair: this tile's values, the next tile's keys
+        clean = x.flags & kClean;
+        ord = x.ord;
+        if (pages) {
 #pragma unroll
           for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src + to_values, k, lane);
         }
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL + (j + 1) % kRing), ((j + 1) / kRing) & 1, ctl, &abort_flag)))
+          break;
+        any = !(ring[(j + 1) % kRing].flags & kEnd);
+        src = c.data + ring[(j + 1) % kRing].off[w];
+        if (AHEAD && any && pages) load_keys(src);
       }
     } else {
       fewer_regs<kRegsMma>();
@@ -693,13 +738,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (; ok && walk.next(c, b, a, sg); ++ord) {
         if (!segment_free()) break;
+        const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
+        const int end = min(sg.sq.len, sg.b.maxpos + 1);
+        bool hole = false;
+        const int first = (sg.b.t0 + sg.begin) * BN, past = min(end, (sg.b.t0 + sg.end) * BN);
+        for (int p = first / c.page_tokens + lane; p * static_cast<long long>(c.page_tokens) < past; p += 32) {
+          const int page = __ldg(table + p);
+          hole |= page < 0 || page >= c.pages;
+        }
+        sg.holes = __any_sync(0xFFFFFFFFu, hole);
         if (lane == 0) {
           segs[ord % kSegs] = sg;
           mbar_arrive(bar(GFULL + ord % kSegs));
         }
         __syncwarp();
-        const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
-        const int end = min(sg.sq.len, sg.b.maxpos + 1);
         for (int i = sg.begin; i < sg.end; ++i, ++n) {
           const int t = sg.b.t0 + i, pos = t * BN + (lane & 7) * kGranule;
           const bool there = pos < end;
@@ -716,8 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             x.ord = ord;
             x.valid = static_cast<int>(valid_bits);
-            x.flags = (i == sg.begin ? kFirst : 0) | (i + 1 == sg.end ? kLast : 0) | (sg.b.rows > 128 ? kTwo : 0) |
-                      (tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu ? kClean : 0);
+            x.flags = tile_masked(sg.b, a.window, t) || valid_bits != 0xFFu ? kClean : 0;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(RFULL + n % kRing));
@@ -769,42 +820,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts(tm + kColO + h * 128, tm + h * 128 + 8 * i, v + (((i >> 2) * C::VCHUNK + (i & 3) * 32) >> 4), idO,
                  i != 0 || !first, one);
       };
-      while (wait(RFULL + n % kRing, (n / kRing) & 1)) {
-        const int flags = uniform(ring[n % kRing].flags);
-        if (flags & kEnd) break;
-        if (one) mbar_arrive(bar(RFREE + n % kRing));
-        const uint32_t slot = n & 1, next = (n + 1) & 1;
-        const bool two = flags & kTwo, first = flags & kFirst, more = !(flags & kLast);
-        if (first) {
-          if (!wait(QFULL, q0++ & 1)) break;
-          if (two && !wait(QFULL + 1, q1++ & 1)) break;
-          if (!wait(KFULL + slot, (n >> 1) & 1)) break;
-          tc_fence_after();
-          scores(0, slot);
-          if (two) scores(1, slot);
-          commit_one(bar(KFREE + slot), one);
-        }
-        if (!wait(VFULL + slot, (n >> 1) & 1)) break;
-        if (more && !wait(KFULL + next, ((n + 1) >> 1) & 1)) break;
-        if (!wait(PFULL, n & 1)) break;
+      // (FREE's event e: the scores of tile e and the products of tile e - 1 are done)
+      int ord = 0;
+      bool first_pair = true;
+      while (wait(GFULL + ord % kSegs, (ord / kSegs) & 1)) {
+        const Segment& sg = segs[ord % kSegs];
+        const int count = uniform(sg.end - sg.begin);
+        const bool two = uniform(sg.b.rows) > 128;
+        if (uniform(sg.begin) < 0) break;
+        if (first_pair && !wait(FULL, 0)) break;
+        first_pair = false;
+        if (!wait(QFULL, q0++ & 1)) break;
         tc_fence_after();
-        product(0, slot, first);
-        if (more)
-          scores(0, next);
-        else
-          commit_one(bar(ODONE), one);
+        scores(0, n & 1);
         if (two) {
-          if (!wait(PFULL + 1, n1++ & 1)) break;
+          if (!wait(QFULL + 1, q1++ & 1)) break;
           tc_fence_after();
-          product(1, slot, first);
-          if (more)
-            scores(1, next);
-          else
-            commit_one(bar(ODONE + 1), one);
+          scores(1, n & 1);
         }
-        if (more) commit_one(bar(KFREE + next), one);
-        commit_one(bar(VFREE + slot), one);
-        ++n;
+        commit_one(bar(FREE + (n & 1)), one);
+        for (int i = 0; i < count; ++i, ++n) {
+          const uint32_t slot = n & 1, next = (n + 1) & 1;
+          const bool more = i + 1 < count;
+          if (!wait(FULL + next, ((n + 1) >> 1) & 1)) break;
+          if (!wait(PFULL, n & 1)) break;
+          tc_fence_after();
+          product(0, slot, i == 0);
+          if (more)
+            scores(0, next);
+          else
+            commit_one(bar(ODONE), one);
+          if (two) {
+            if (!wait(PFULL + 1, n1++ & 1)) break;
+            tc_fence_after();
+            product(1, slot, i == 0);
+            if (more)
+              scores(1, next);
+            else
+              commit_one(bar(ODONE + 1), one);
+          }
+          if (more) commit_one(bar(FREE + next), one);
+        }
+        if (!ok) break;
+        if (one) mbar_arrive(bar(GFREE + ord % kSegs));
+        ++ord;
       }
       if (!ok) {  // every product issued ends before tensor memory is freed
         commit_one(bar(DRAIN), one);
