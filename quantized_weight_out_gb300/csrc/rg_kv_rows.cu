@@ -1,9 +1,10 @@
 // rg_kv_rows.cu - attention of few rows a sequence over the paged cache: single
 // tokens, drafted tokens, short chunks.
 //
-// The rows of a kv head (new tokens x the query heads that share it) are the M
-// side of m16n8k16 products, 16 or 32 at a time; the cache is the N side and
-// is read once, decoded in registers.  With one running maximum and sum a row
+// The rows of a kv head (new tokens x the query heads that share it) are the N
+// side of m16n8k16 products, 8, 16 or 32 at a time, and the cache is the M side
+// (S^T = K Q^T, O^T = V^T P^T: few rows fill their side, and accumulators take
+// D / 4 registers a lane for 8 rows); it is read once and decoded in registers.  With one running maximum and sum a row
 // (out = sum_j 2^(z_j - m) v_j / sum_j 2^(z_j - m), z = score * scale * log2 e)
 // keys can be taken in any order and in parts that are joined later by
 // 2^(m_part - m), so the cache's length is the axis that work is split along:
@@ -27,20 +28,24 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 64;            // tokens: a granule a warp
-template <int TYPE, int D, int MT>
+template <int TYPE, int D, int NT>
 struct Cfg {
-  static constexpr int BM = 16 * MT;
-  static constexpr bool QREG = MT * D <= 128;              // queries in registers (32 words a lane)
+  static constexpr int BM = 8 * NT;
+  static constexpr int OREGS = NT * D / 4;                 // accumulator registers a lane
+  // granules a step: two where decoding is the work, so that the softmax's bookkeeping
+  // and the queries' loads count once for 32 tokens
+  static constexpr int NG = has_scales(TYPE) && OREGS <= 64 ? 2 : 1;
+  static constexpr bool QREG = NT * D <= 128;              // queries in registers (16 words a lane)
   static constexpr int GB = granule_bytes(TYPE, D);
   static constexpr int STAGE = 2 * GB;
-  static constexpr int RANK = MT * D;                      // 64 .. 256: accumulator registers a lane are half of it
-  static constexpr int MINB = STAGE >= 16384 ? 1 : RANK <= 64 ? 4 : RANK <= 128 ? 3 : 2;
-  static constexpr int QBYTES = QREG ? 0 : MT * (D / 32) * 1024;
-  static constexpr int MERGE_LD = D + 8;
+  static constexpr int QBYTES = QREG ? 0 : NT * (D / 32) * 512;
+  // CTAs a SM: as the registers allow, and with a ring of two stages at least
+  static constexpr int fit(int ctas) { return ((227 * 1024) / ctas - 2048 - QBYTES) / (kWarps * STAGE); }
+  static constexpr int most(int ctas) { return ctas > 1 && fit(ctas) < 2 ? most(ctas - 1) : ctas; }
+  static constexpr int MINB = most(OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2);
+  static constexpr int MERGE_LD = D + 4;
   static constexpr int MERGE = kWarps * BM * MERGE_LD * 4;
-  static constexpr int ROOM = (227 * 1024) / MINB - 2048 - QBYTES;
-  static constexpr int FIT = ROOM / (kWarps * STAGE);
-  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int STAGES = fit(MINB) > 6 ? 6 : fit(MINB);
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + QBYTES;
   static_assert(STAGES >= 2, "a ring needs two stages");
@@ -60,15 +65,14 @@ __device__ __forceinline__ Shape shape_of(const Seq& q, int group, int bm, int w
   return s;
 }
 
-template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
     attend_rows_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
-  using C = Cfg<TYPE, D, MT>;
+  using C = Cfg<TYPE, D, NT>;
   constexpr bool BF = TYPE == RG_BF16;
   constexpr int BLK = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kWarps][C::STAGES];
-  __shared__ int usable[kWarps][C::STAGES];
   __shared__ float sm_m[kWarps][C::BM], sm_l[kWarps][C::BM];
   __shared__ long long sh_sum[kWarps];
   __shared__ long long sh_acc;
@@ -150,46 +154,40 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
     const int rows = min(C::BM, nrows - row0);
     const int minpos = first + row0 / G, maxpos = first + (row0 + rows - 1) / G;
 
-    // positions of this lane's rows (below every token: a row that does not exist)
-    int pos[MT][2];
+    // positions of this lane's rows 8m + 2t + r (below every token: a row that does not exist)
+    int pos[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = 16 * m + 8 * r + g;
+        const int row = 8 * m + 2 * t + r;
         pos[m][r] = row < rows ? first + (row0 + row) / G : -1;
       }
 
-    // queries as A operands
-    uint4 qreg[C::QREG ? MT : 1][C::QREG ? BLK : 1][2];
+    // queries as B operands: row 8m + g, dimensions 32k + 8t .. + 7
+    uint4 qreg[C::QREG ? NT : 1][C::QREG ? BLK : 1];
+    auto query = [&](int m, int k) {
+      const int row = row0 + 8 * m + g;
+      return row < row0 + rows ? query8<BF>(a, (sq.start + row / G) * a.q_t + (head * G + row % G) * a.q_h + 32 * k + 8 * t,
+                                            ctl.status)
+                               : make_uint4(0, 0, 0, 0);
+    };
     if constexpr (C::QREG) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = 16 * m + 8 * r + g;
-          const int tok = sq.start + (row0 + row) / G, hd = head * G + (row0 + row) % G;
-#pragma unroll
-          for (int k = 0; k < BLK; ++k)
-            qreg[m][k][r] =
-                row < rows ? query8<BF>(a, tok * a.q_t + hd * a.q_h + 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
-        }
+        for (int k = 0; k < BLK; ++k) qreg[m][k] = query(m, k);
     } else {
-      for (int u = warp; u < MT * BLK * 2; u += kWarps) {
-        const int m = u / (BLK * 2), k = u / 2 % BLK, r = u & 1;
-        const int row = 16 * m + 8 * r + g;
-        const int tok = sq.start + (row0 + row) / G, hd = head * G + (row0 + row) % G;
-        reinterpret_cast<uint4*>(smem)[u * 32 + lane] =
-            row < rows ? query8<BF>(a, tok * a.q_t + hd * a.q_h + 32 * k + 8 * t, ctl.status) : make_uint4(0, 0, 0, 0);
-      }
+      for (int u = warp; u < NT * BLK; u += kWarps) reinterpret_cast<uint4*>(smem)[u * 32 + lane] = query(u / BLK, u % BLK);
       __syncthreads();
     }
 
-    float o[MT][D / 8][4], m_ref[MT][2], l_sum[MT][2];
+    // o[m][i]: dimensions 16i + g (words 0, 1: rows 2t, 2t + 1) and 16i + 8 + g (2, 3)
+    float o[NT][D / 16][4], m_ref[NT][2], l_sum[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NT; ++m) {
 #pragma unroll
-      for (int d = 0; d < D / 8; ++d)
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][d][i] = 0.0f;
       m_ref[m][0] = m_ref[m][1] = kNone;
@@ -201,153 +199,177 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
     const int g0 = 4 * (sh.t0 + tile) + warp;
     const int count = g0 < gend ? (gend - g0 + kWarps - 1) / kWarps : 0;
     const int* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
-    auto load_pages = [&](int k) {
-      return k + lane < count ? table[(g0 + kWarps * (k + lane)) * kGranule / c.page_tokens] : -1;
+    // byte offsets of the keys of 32 of this warp's granules, one a lane (-1: no such page)
+    auto load_offsets = [&](int k) -> long long {
+      if (k + lane >= count) return -1;
+      const int pos = (g0 + kWarps * (k + lane)) * kGranule;
+      const int page = table[pos / c.page_tokens];
+      if (page >= 0 && page < c.pages) return granule_offset(c, page, 0, head, pos, C::GB);
+      report_index(ctl.status);
+      return -1;
     };
-    int pages = load_pages(0), pages_next = load_pages(32);
+    long long offs = load_offsets(0), offs_next = load_offsets(32);
+    const long long to_values = c.kv_heads * c.slab_bytes;
+    uint32_t st_in = it % C::STAGES, usable = 0;  // the next stage to fill; stages that hold something
     // granule k into its stage of the ring (the whole warp)
     auto issue = [&](int k) {
       if (k && (k & 31) == 0) {
-        pages = pages_next;
-        pages_next = load_pages(k + 32);
+        offs = offs_next;
+        offs_next = load_offsets(k + 32);
       }
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, k & 31);
+      const long long off = __shfl_sync(0xFFFFFFFFu, offs, k & 31);
+      usable = off >= 0 ? usable | (1u << st_in) : usable & ~(1u << st_in);
       if (lane == 0) {
-        const uint32_t st = (it + k) % C::STAGES;
-        const uint32_t bar = smem_addr(&full[warp][st]);
-        const bool ok = page >= 0 && page < c.pages;
-        usable[warp][st] = ok;
-        if (ok) {
-          const uint8_t* src =
-              c.data + granule_offset(c, page, 0, head, (g0 + kWarps * k) * kGranule, C::GB);
+        const uint32_t bar = smem_addr(&full[warp][st_in]), to = ring + st_in * C::STAGE;
+        if (off >= 0) {
           mbar_arrive_expect_tx(bar, C::STAGE);
-          bulk_load(ring + st * C::STAGE, src, C::GB, bar);
-          bulk_load(ring + st * C::STAGE + C::GB, src + c.kv_heads * c.slab_bytes, C::GB, bar);
+          bulk_load(to, c.data + off, C::GB, bar);
+          bulk_load(to + C::GB, c.data + off + to_values, C::GB, bar);
         } else {
-          report_index(ctl.status);
           mbar_arrive(bar);
         }
       }
+      st_in = st_in + 1 == C::STAGES ? 0 : st_in + 1;
     };
 
-    // one granule: scores, probabilities, products with the values
-    auto granule = [&](auto masked_c, int gran, uint32_t kbase) {
+    // N granules gran, gran + kWarps, ... in stages at kb[]: scores, probabilities, products
+    // with the values.  have: bit u, granule u's page exists (MASKED only)
+    auto step = [&](auto masked_c, auto n_c, int gran, const uint32_t* kb, uint32_t have) {
       constexpr bool MASKED = decltype(masked_c)::value;
-      const uint32_t vbase = kbase + C::GB;
-      float s[MT][2][4];
+      constexpr int N = decltype(n_c)::value;
+      // s[m][u]: words 0, 1: token 4(g / 2) + g % 2 for rows 2t, 2t + 1; 2, 3: the token two on
+      float s[NT][N][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int u = 0; u < N; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[m][n][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) s[m][u][i] = 0.0f;
 #pragma unroll
       for (int k = 0; k < BLK; ++k) {
-        KeyWords<TYPE> kw;
-        load_words<TYPE, D>(kw, kbase, k, lane);
-        uint32_t kb[2][4];
-        key_operand(kw, kb);
+        uint4 x[NT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint4 x, y;
-          if constexpr (C::QREG) {
-            x = qreg[m][k][0];
-            y = qreg[m][k][1];
-          } else {
-            x = lds128(qbase + (((m * BLK + k) * 2) * 32 + lane) * 16);
-            y = lds128(qbase + (((m * BLK + k) * 2 + 1) * 32 + lane) * 16);
-          }
+        for (int m = 0; m < NT; ++m) {
+          if constexpr (C::QREG)
+            x[m] = qreg[m][k];
+          else
+            x[m] = lds128(qbase + ((m * BLK + k) * 32 + lane) * 16);
+        }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            mma16<BF>(s[m][n], x.x, y.x, x.y, y.y, kb[n][0], kb[n][1]);
-            mma16<BF>(s[m][n], x.z, y.z, x.w, y.w, kb[n][2], kb[n][3]);
+        for (int u = 0; u < N; ++u) {
+          KeyWords<TYPE> kw;
+          load_words<TYPE, D>(kw, kb[u], k, lane);
+          uint32_t op[2][4];
+          key_operand(kw, op);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            mma16<BF>(s[m][u], op[0][0], op[1][0], op[0][1], op[1][1], x[m].x, x[m].y);
+            mma16<BF>(s[m][u], op[0][2], op[1][2], op[0][3], op[1][3], x[m].z, x[m].w);
           }
         }
       }
-      uint32_t p[MT][4];
+      uint32_t p[NT][2 * N];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < NT; ++m) {
         float top[2] = {kNone, kNone};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int u = 0; u < N; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float z = s[m][n][i] * a.scale_log2;
+            float z = s[m][u][i] * a.scale_log2;
             if constexpr (MASKED) {
-              const int j = gran * kGranule + 4 * t + 2 * n + (i & 1), ps = pos[m][i >> 1];
-              if (j > ps || (a.window && j <= ps - a.window)) z = -INFINITY;
+              const int j = (gran + kWarps * u) * kGranule + 4 * (g >> 1) + 2 * (i >> 1) + (g & 1), ps = pos[m][i & 1];
+              if (j > ps || (a.window && j <= ps - a.window) || !((have >> u) & 1)) z = -INFINITY;
             }
-            s[m][n][i] = z;
-            top[i >> 1] = fmaxf(top[i >> 1], z);
+            s[m][u][i] = z;
+            top[i & 1] = fmaxf(top[i & 1], z);
           }
         if (__any_sync(0xFFFFFFFFu, top[0] > m_ref[m][0] + kSlack || top[1] > m_ref[m][1] + kSlack)) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float v = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-            v = fmaxf(v, m_ref[m][r]);
+            float v = fmaxf(top[r], m_ref[m][r]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
             const float f = ex2(m_ref[m][r] - v);
             m_ref[m][r] = v;
             l_sum[m][r] *= f;
 #pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              o[m][d][2 * r] *= f;
-              o[m][d][2 * r + 1] *= f;
+            for (int d = 0; d < D / 16; ++d) {
+              o[m][d][r] *= f;
+              o[m][d][2 + r] *= f;
             }
           }
         }
         const float base0 = m_ref[m][0] - kHead, base1 = m_ref[m][1] - kHead;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float e0 = ex2(s[m][n][0] - base0), e1 = ex2(s[m][n][1] - base0);
-          const float e2 = ex2(s[m][n][2] - base1), e3 = ex2(s[m][n][3] - base1);
-          l_sum[m][0] += e0 + e1;
-          l_sum[m][1] += e2 + e3;
-          p[m][2 * n] = pack16<BF>(e0, e1);
-          p[m][2 * n + 1] = pack16<BF>(e2, e3);
+        for (int u = 0; u < N; ++u) {
+          const float e0 = ex2(s[m][u][0] - base0), e1 = ex2(s[m][u][1] - base1);
+          const float e2 = ex2(s[m][u][2] - base0), e3 = ex2(s[m][u][3] - base1);
+          l_sum[m][0] += e0 + e2;
+          l_sum[m][1] += e1 + e3;
+          // [token][row] -> [row][token]: tokens 4t, 4t + 1 and 4t + 2, 4t + 3 of row g
+          p[m][2 * u] = transpose8x8(pack16<BF>(e0, e1));
+          p[m][2 * u + 1] = transpose8x8(pack16<BF>(e2, e3));
         }
       }
-      bool bad = false;
 #pragma unroll
-      for (int k = 0; k < BLK; ++k) {
-        ValueWords<TYPE> vw;
-        load_words<TYPE, D>(vw, vbase, k, lane);
-        uint32_t vb[4][2];
-        if constexpr (MASKED) bad |= clean_words(vw);
-        value_operand(vw, vb);
+      for (int u = 0; u < N; ++u) {
+        const uint32_t vbase = kb[u] + C::GB;
+        bool bad = false;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int k = 0; k < BLK; ++k) {
+          ValueWords<TYPE> vw;
+          load_words<TYPE, D>(vw, vbase, k, lane);
+          if constexpr (MASKED) bad |= clean_words(vw);
+          uint32_t vb[4][2];
+          value_operand(vw, vb);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mma16<BF>(o[m][4 * k + q], p[m][0], p[m][1], p[m][2], p[m][3], vb[q][0], vb[q][1]);
-      }
-      if constexpr (MASKED) {
-        // values that are not finite were left out of the product (0 x inf would
-        // reach rows that may not see them): add them to the rows that do
-        if (__any_sync(0xFFFFFFFFu, bad)) {
-          for (int jj = 0; jj < kGranule; ++jj) {
-            const int j = gran * kGranule + jj;
+          for (int m = 0; m < NT; ++m)
 #pragma unroll
-            for (int d = 0; d < D / 8; ++d)
+            for (int q = 0; q < 4; q += 2)
+              mma16<BF>(o[m][2 * k + q / 2], vb[q][0], vb[q + 1][0], vb[q][1], vb[q + 1][1], p[m][2 * u], p[m][2 * u + 1]);
+        }
+        if constexpr (MASKED) {
+          // values that are not finite were left out of the product (0 x inf would
+          // reach rows that may not see them): add them to the rows that do
+          if (((have >> u) & 1) && __any_sync(0xFFFFFFFFu, bad)) {
+            for (int jj = 0; jj < kGranule; ++jj) {
+              const int j = (gran + kWarps * u) * kGranule + jj;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float v = value_not_finite<TYPE, D>(vbase, jj, 8 * d + 2 * t + e);
+              for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int e = 0; e < 2; ++e) {
+                  const float v = value_not_finite<TYPE, D>(vbase, jj, 16 * d + 8 * e + g);
 #pragma unroll
-                  for (int r = 0; r < 2; ++r)
-                    if (j <= pos[m][r] && !(a.window && j <= pos[m][r] - a.window)) o[m][d][2 * r + e] += v;
-              }
+                  for (int m = 0; m < NT; ++m)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                      if (j <= pos[m][r] && !(a.window && j <= pos[m][r] - a.window)) o[m][d][2 * e + r] += v;
+                }
+            }
           }
         }
       }
     };
 
     bool gave_up = false;
+    uint32_t st = it % C::STAGES, phase = it / C::STAGES & 1;  // of the next granule to use
     for (int k = 0; k < min(count, C::STAGES); ++k) issue(k);
-    for (int k = 0; k < count; ++k) {
-      const uint32_t st = (it + k) % C::STAGES, phase = (it + k) / C::STAGES & 1;
-      if (!wait_bar(smem_addr(&full[warp][st]), phase, ctl, &sh_abort)) gave_up = true;
+    for (int k = 0; k < count;) {
+      // as many as a step takes, if they are there
+      const int n = C::NG == 2 && k + 1 < count ? 2 : 1;
+      uint32_t kb[2], have = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u >= n) break;
+        if (!gave_up && !wait_bar(smem_addr(&full[warp][st]), phase, ctl, &sh_abort)) gave_up = true;
+        kb[u] = ring + st * C::STAGE;
+        have |= (usable >> st & 1) << u;
+        if (++st == C::STAGES) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
       gave_up = __any_sync(0xFFFFFFFFu, gave_up);
       if (gave_up) {
         // copies already under way must land before the CTA's shared memory is given up
@@ -358,16 +380,27 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
           }
         break;
       }
-      const int gran = g0 + kWarps * k, j0 = gran * kGranule;
-      if (usable[warp][st]) {
-        const bool whole = j0 + kGranule - 1 <= minpos && !(a.window && j0 <= maxpos - a.window);
-        if (whole)
-          granule(std::false_type{}, gran, ring + st * C::STAGE);
-        else
-          granule(std::true_type{}, gran, ring + st * C::STAGE);
+      const int gran = g0 + kWarps * k, j0 = gran * kGranule, j1 = (gran + kWarps * (n - 1)) * kGranule;
+      const bool whole = have == (1u << n) - 1 && j1 + kGranule - 1 <= minpos && !(a.window && j0 <= maxpos - a.window);
+      if (n == 2) {
+        if constexpr (C::NG == 2) {
+          if (whole)
+            step(std::false_type{}, std::integral_constant<int, 2>{}, gran, kb, have);
+          else
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u)
+              step(std::true_type{}, std::integral_constant<int, 1>{}, gran + kWarps * u, &kb[u], have >> u);
+        }
+      } else if (C::NG == 1 && whole) {
+        step(std::false_type{}, std::integral_constant<int, 1>{}, gran, kb, have);
+      } else {
+        step(std::true_type{}, std::integral_constant<int, 1>{}, gran, kb, have);
       }
       __syncwarp();
-      if (k + C::STAGES < count) issue(k + C::STAGES);
+#pragma unroll 1
+      for (int u = 0; u < n; ++u)
+        if (k + u + C::STAGES < count) issue(k + u + C::STAGES);
+      k += n;
     }
     if (__syncthreads_or(gave_up)) {
       if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
@@ -377,22 +410,24 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, MT>::MINB)
 
     // join the four warps
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float l = l_sum[m][r];
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-        const int row = 16 * m + 8 * r + g;
-        if (t == 0) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        const int row = 8 * m + 2 * t + r;
+        if (g == 0) {
           sm_m[warp][row] = m_ref[m][r];
           sm_l[warp][row] = l;
         }
         if (row < rows) {
-          float* to = merge + (warp * C::BM + row) * C::MERGE_LD + 2 * t;
+          float* to = merge + (warp * C::BM + row) * C::MERGE_LD + g;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<float2*>(to + 8 * d) = make_float2(o[m][d][2 * r], o[m][d][2 * r + 1]);
+          for (int d = 0; d < D / 16; ++d) {
+            to[16 * d] = o[m][d][r];
+            to[16 * d + 8] = o[m][d][2 + r];
+          }
         }
       }
     __syncthreads();
@@ -513,14 +548,17 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
 
 constexpr int kMaxCtasPerSm = 4;
 
-int rows_mt(const Batch& b, int group, int dim) {
-  return dim < 256 && static_cast<int64_t>(b.max_new) * group > 16 ? 2 : 1;
+// Rows of eight side by side: as many as the longest sequence has, up to 32 (16 of
+// 256 dimensions: the accumulators' registers).
+int rows_nt(const Batch& b, int group, int dim) {
+  const int64_t rows = static_cast<int64_t>(b.max_new) * group;
+  return rows <= 8 ? 1 : rows <= 16 || dim == 256 ? 2 : 4;
 }
 
-template <int TYPE, int D, int MT>
+template <int TYPE, int D, int NT>
 cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev, cudaStream_t stream) {
-  using K = Cfg<TYPE, D, MT>;
-  auto kern = attend_rows_kernel<TYPE, D, MT>;
+  using K = Cfg<TYPE, D, NT>;
+  auto kern = attend_rows_kernel<TYPE, D, NT>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), K::SMEM);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles there can be
@@ -538,10 +576,16 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
 
 template <int TYPE>
 cudaError_t go_dim(const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev, cudaStream_t s) {
-  const int mt = rows_mt(b, a.group, c.dim);
-  if (c.dim == 64) return mt == 2 ? go<TYPE, 64, 2>(c, b, a, ws, dev, s) : go<TYPE, 64, 1>(c, b, a, ws, dev, s);
-  if (c.dim == 128) return mt == 2 ? go<TYPE, 128, 2>(c, b, a, ws, dev, s) : go<TYPE, 128, 1>(c, b, a, ws, dev, s);
-  return go<TYPE, 256, 1>(c, b, a, ws, dev, s);
+  const int nt = rows_nt(b, a.group, c.dim);
+  if (c.dim == 64)
+    return nt == 4   ? go<TYPE, 64, 4>(c, b, a, ws, dev, s)
+           : nt == 2 ? go<TYPE, 64, 2>(c, b, a, ws, dev, s)
+                     : go<TYPE, 64, 1>(c, b, a, ws, dev, s);
+  if (c.dim == 128)
+    return nt == 4   ? go<TYPE, 128, 4>(c, b, a, ws, dev, s)
+           : nt == 2 ? go<TYPE, 128, 2>(c, b, a, ws, dev, s)
+                     : go<TYPE, 128, 1>(c, b, a, ws, dev, s);
+  return nt == 2 ? go<TYPE, 256, 2>(c, b, a, ws, dev, s) : go<TYPE, 256, 1>(c, b, a, ws, dev, s);
 }
 
 }  // namespace
@@ -562,7 +606,7 @@ cudaError_t launch_join(const Attend& a, const Desc* desc, const float* parts, i
 }
 
 size_t rows_workspace(const Cache& c, const Batch& b, int group, const DevInfo& dev) {
-  const int bm = 16 * rows_mt(b, group, c.dim);
+  const int bm = 8 * rows_nt(b, group, c.dim);
   const int64_t ctas = static_cast<int64_t>(kMaxCtasPerSm) * dev.num_sms;
   return static_cast<size_t>((ctas * sizeof(Desc) + 255) / 256 * 256 + ctas * 2 * part_floats(bm, c.dim) * 4);
 }
