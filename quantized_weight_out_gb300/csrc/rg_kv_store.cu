@@ -2,12 +2,13 @@
 // the paged cache in its storage type, and stored tokens back out.
 //
 // A warp handles one granule (16 tokens) of one head and kind, as far as the
-// new tokens cover it, 32 dimensions at a time: lane (g, t) loads 8 consecutive
-// dimensions of two tokens, so four lanes hold a token's block and two shuffles
-// give its largest magnitude.  Keys leave in that arrangement; values are
-// transposed through 1 KB of shared memory a warp when the granule is whole, and
-// go out byte by byte when it is not (a byte belongs to one token).  Bound by
-// memory for prompts, by latency for single tokens.
+// new tokens cover it, 32 dimensions at a time: lane (g, t), g = 2a + b, loads 8
+// consecutive dimensions of tokens 4a + b and 4a + b + 2, so four lanes hold a
+// token's block and two shuffles give its largest magnitude.  Keys leave in that
+// arrangement; values are transposed by exchanges between the lanes that share
+// the target words (no shared memory), or go out byte by byte when the granule is
+// not whole (a byte belongs to one token).  Several blocks' loads are in flight at
+// a time.  Bound by memory for prompts, by latency for single tokens.
 #include "rg_kv.cuh"
 #include "rg_kv_launch.h"
 
@@ -75,17 +76,15 @@ struct Piece {
   bool ok;
 };
 
-// The piece that starts at packed token i, if one does: i is the first new
-// token of its sequence, or the first token of its granule.
-__device__ __forceinline__ bool piece_at(const Cache& c, const Batch& b, int i, int gran_bytes, int* status,
+// The piece that starts at packed token i of sequence s, if one does: i is the
+// first new token of its sequence, or the first token of its granule.
+__device__ __forceinline__ bool piece_at(const Cache& c, const Batch& b, int i, int s, int gran_bytes, int* status,
                                          Piece* out) {
-  const int s = find_seq(b, i);
   const Seq q = load_seq(b, c.page_tokens, s, status);
   if (i < q.start || i >= q.start + q.n) return false;
   const int first = q.len - q.n;              // position of the first new token (negative: before the cache)
   const int pos = first + (i - q.start);
-  const bool starts = pos < 0 || pos % kGranule == 0 || i == q.start;
-  if (!starts) return false;
+  if (!(pos < 0 || pos % kGranule == 0 || i == q.start)) return false;
   if (pos < 0) {  // one token with no place
     *out = Piece{0, 1, i, 0, false};
     return true;
@@ -100,6 +99,42 @@ __device__ __forceinline__ bool piece_at(const Cache& c, const Batch& b, int i, 
   return true;
 }
 
+// The pieces that start among a block's packed tokens, found by the lanes side by
+// side (window 16) or by the whole warp (window 1).
+struct Pieces {
+  Piece mine;
+  uint32_t starts;
+  __device__ __forceinline__ void find(const Cache& c, const Batch& b, int window, int gran_bytes, int* status) {
+    const int lane = threadIdx.x & 31, i = blockIdx.x * window + (window > 1 ? lane : 0);
+    bool has = false;
+    if (window == 1) {
+      has = piece_at(c, b, i, find_seq(b, i), gran_bytes, status, &mine) && lane == 0;
+    } else if (lane < window && i < b.tokens) {
+      int lo = 0, hi = b.seqs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (b.new_start[mid] <= i)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      has = piece_at(c, b, i, lo, gran_bytes, status, &mine);
+    }
+    starts = __ballot_sync(0xFFFFFFFFu, has);
+  }
+  __device__ __forceinline__ bool next(Piece* p) {
+    if (!starts) return false;
+    const int l = __ffs(starts) - 1;
+    starts &= starts - 1;
+    p->j0 = __shfl_sync(0xFFFFFFFFu, mine.j0, l);
+    p->cnt = __shfl_sync(0xFFFFFFFFu, mine.cnt, l);
+    p->token = __shfl_sync(0xFFFFFFFFu, mine.token, l);
+    p->off = __shfl_sync(0xFFFFFFFFu, mine.off, l);
+    p->ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(mine.ok), l);
+    return true;
+  }
+};
+
 struct Rows {
   const void* p[2];        // keys, values (NULL: left out)
   int64_t t[2], h[2];      // element strides of tokens and heads
@@ -109,173 +144,413 @@ struct OutRows {
   int64_t t[2], h[2];
 };
 
+// 8 activations as loaded, and as F32.
+template <int AT>
+struct Raw {
+  uint4 v[AT == RG_F32 ? 2 : 1];
+};
+template <int AT>
+__device__ __forceinline__ Raw<AT> load_raw(const void* base, int64_t elem) {
+  Raw<AT> r;
+  if constexpr (AT == RG_F32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elem);
+    r.v[0] = __ldg(p);
+    r.v[1] = __ldg(p + 1);
+  } else {
+    r.v[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem));
+  }
+  return r;
+}
+template <int AT>
+__device__ __forceinline__ void raw_f32(const Raw<AT>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (AT == RG_F32) {
+      const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+      x[i] = __uint_as_float(w[i]);
+      x[4 + i] = __uint_as_float(u[i]);
+    } else if constexpr (AT == RG_F16) {
+      x[2 * i] = f16_to_f32(static_cast<uint16_t>(w[i] & 0xFFFFu));
+      x[2 * i + 1] = f16_to_f32(static_cast<uint16_t>(w[i] >> 16));
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+__device__ __forceinline__ uint32_t swap_lane(uint32_t x, int mask) { return __shfl_xor_sync(0xFFFFFFFFu, x, mask); }
+// the e-th bytes of four words
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t e) {
+  const uint32_t s = e | ((4 + e) << 4);
+  return prmt(prmt(w0, w1, s), prmt(w2, w3, s), 0x5410);
+}
+
+// --- values of a whole granule: lane (a, b, t) has dimensions 8t + e of tokens
+// 4a + b (n = 0) and 4a + b + 2 (n = 1); the word of dimension e holds tokens 4a .. 4a + 3
+
+// c[n][h]: codes e = 4h .. 4h + 3 as bytes.  Lane b writes the words of e = 4b .. 4b + 3.
+__device__ __forceinline__ void put_values_q8(uint8_t* out, const uint32_t (&c)[2][2], int a, int b, int t) {
+  const uint32_t m0 = b ? c[0][1] : c[0][0], m1 = b ? c[1][1] : c[1][0];
+  const uint32_t p0 = swap_lane(b ? c[0][0] : c[0][1], 4), p1 = swap_lane(b ? c[1][0] : c[1][1], 4);
+  const uint32_t x0 = b ? p0 : m0, y0 = b ? m0 : p0, x1 = b ? p1 : m1, y1 = b ? m1 : p1;
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    const uint32_t s = e | ((4 + e) << 4);
+    *reinterpret_cast<uint32_t*>(out + (4 * b + e) * 64 + a * 16 + t * 4) = prmt(prmt(x0, y0, s), prmt(x1, y1, s), 0x5410);
+  }
+}
+__device__ __forceinline__ void get_values_q8(const uint32_t (&w)[4], uint32_t (&c)[2][2], int b) {
+  const uint32_t m0 = gather_bytes(w[0], w[1], w[2], w[3], b), m1 = gather_bytes(w[0], w[1], w[2], w[3], b + 2);
+  const uint32_t p0 = swap_lane(gather_bytes(w[0], w[1], w[2], w[3], b ^ 1), 4);
+  const uint32_t p1 = swap_lane(gather_bytes(w[0], w[1], w[2], w[3], (b ^ 1) + 2), 4);
+  c[0][0] = b ? p0 : m0; c[0][1] = b ? m0 : p0;
+  c[1][0] = b ? p1 : m1; c[1][1] = b ? m1 : p1;
+}
+
+// c[n]: codes e as nibbles.  A byte joins the nibbles of lanes t and t ^ 1 (dimensions 8t + e,
+// 8(t ^ 1) + e), a word the bytes [b][n] of tokens 4a + b + 2n; lane (b, t % 2) writes the words
+// of e = 4 (t % 2) + 2b and the next.
+__device__ __forceinline__ void put_values_q4(uint8_t* out, const uint32_t (&c)[2], int a, int b, int t) {
+  const int n = t & 1;
+  const uint32_t other = swap_lane(n ? c[0] : c[1], 1);
+  const uint32_t lo = n ? other : c[0], hi = n ? c[1] : other;  // token n: even and odd q
+  const uint32_t even = (lo & 0x0F0F0F0Fu) | ((hi & 0x0F0F0F0Fu) << 4), odd = ((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
+  const uint32_t e0 = prmt(even, odd, 0x5140), e1 = prmt(even, odd, 0x7362);  // e = 0 .. 3, 4 .. 7
+  const uint32_t got = swap_lane(n ? e0 : e1, 1), own = n ? e1 : e0;
+  const uint32_t n0 = n ? got : own, n1 = n ? own : got;                      // e = 4n .. 4n + 3 of both tokens
+  const uint32_t first = prmt(n0, n1, 0x5410), second = prmt(n0, n1, 0x7632);
+  const uint32_t keep = b ? second : first, r = swap_lane(b ? first : second, 4);
+  const uint32_t b0 = b ? r : keep, b1 = b ? keep : r;
+  uint8_t* to = out + (4 * n + 2 * b) * 32 + a * 8 + (t >> 1) * 4;
+  *reinterpret_cast<uint32_t*>(to) = prmt(b0, b1, 0x6420);
+  *reinterpret_cast<uint32_t*>(to + 32) = prmt(b0, b1, 0x7531);
+}
+// w: the words that put_values_q4 writes; c[n][h]: bytes of e = 4h .. 4h + 3 (both nibbles)
+__device__ __forceinline__ void get_values_q4(const uint32_t (&w)[2], uint32_t (&c)[2][2], int b, int t) {
+  const int n = t & 1;
+  const uint32_t b0 = prmt(w[0], w[1], 0x5140), b1 = prmt(w[0], w[1], 0x7362);
+  const uint32_t keep = b ? b1 : b0, r = swap_lane(b ? b0 : b1, 4);
+  const uint32_t q0 = b ? r : keep, q1 = b ? keep : r;
+  const uint32_t n0 = prmt(q0, q1, 0x5410), n1 = prmt(q0, q1, 0x7632);
+  const uint32_t g0 = swap_lane(n0, 1), g1 = swap_lane(n1, 1);
+  c[0][0] = n ? g0 : n0; c[0][1] = n ? n0 : g0;
+  c[1][0] = n ? g1 : n1; c[1][1] = n ? n1 : g1;
+}
+
+// w[n][i]: dimensions 2i, 2i + 1 as halves.  Lane b writes the 8 bytes of e = 4b .. 4b + 3.
+__device__ __forceinline__ void put_values_16(uint8_t* out, const uint32_t (&w)[2][4], int a, int b, int t) {
+  uint32_t x[2][2], y[2][2];  // tokens of b = 0 and of b = 1
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t own = b ? w[n][2 + i] : w[n][i], got = swap_lane(b ? w[n][i] : w[n][2 + i], 4);
+      x[n][i] = b ? got : own;
+      y[n][i] = b ? own : got;
+    }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t s = (e & 1) ? 0x7632 : 0x5410;
+    *reinterpret_cast<uint2*>(out + (t >> 1) * 512 + (4 * b + e) * 64 + a * 16 + (t & 1) * 8) =
+        make_uint2(prmt(x[0][e >> 1], y[0][e >> 1], s), prmt(x[1][e >> 1], y[1][e >> 1], s));
+  }
+}
+__device__ __forceinline__ void get_values_16(const uint2 (&v)[4], uint32_t (&w)[2][4], int b) {
+  const uint32_t mine = b ? 0x7632 : 0x5410, theirs = b ? 0x5410 : 0x7632;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t m0 = prmt(v[2 * i].x, v[2 * i + 1].x, mine), m1 = prmt(v[2 * i].y, v[2 * i + 1].y, mine);
+    const uint32_t p0 = swap_lane(prmt(v[2 * i].x, v[2 * i + 1].x, theirs), 4);
+    const uint32_t p1 = swap_lane(prmt(v[2 * i].y, v[2 * i + 1].y, theirs), 4);
+    w[0][i] = b ? p0 : m0; w[0][2 + i] = b ? m0 : p0;
+    w[1][i] = b ? p1 : m1; w[1][2 + i] = b ? m1 : p1;
+  }
+}
+
+__device__ __forceinline__ uint32_t nibbles8(const int (&c)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w |= static_cast<uint32_t>(c[e]) << (4 * e);
+  return w;
+}
+
+// One block (32 dimensions) of up to 16 tokens into the cache.  out: the block's codes,
+// scales: the block's scales.
+template <int TYPE>
+__device__ __forceinline__ void store_block(const float (&x)[2][8], uint8_t* out, uint16_t* scales, int kind, bool whole,
+                                            const bool (&have)[2], int* status) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, a = g >> 1, b = g & 1, key0 = 4 * a + b;
+  if constexpr (has_scales(TYPE)) {
+    int code[2][8];
+    uint16_t d[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) d[n] = quantise8<TYPE>(x[n], t, code[n], status);
+    if (t == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        if (have[n]) scales[kind == 0 ? 2 * g + n : key0 + 2 * n] = d[n];
+    }
+    if constexpr (TYPE == RG_Q8_0) {
+      uint32_t c[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          c[n][i] = bytes4(code[n][4 * i], code[n][4 * i + 1], code[n][4 * i + 2], code[n][4 * i + 3]);
+      if (kind == 0) {
+        if (whole) {
+          reinterpret_cast<uint4*>(out)[lane] = make_uint4(c[0][0], c[0][1], c[1][0], c[1][1]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            if (have[n]) *reinterpret_cast<uint2*>(out + lane * 16 + 8 * n) = make_uint2(c[n][0], c[n][1]);
+        }
+      } else if (whole) {
+        put_values_q8(out, c, a, b, t);
+      } else {
+        // dimension 8t + e of token j: [e][j / 4][t][j % 4]
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (have[n])
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[e * 64 + a * 16 + t * 4 + b + 2 * n] = static_cast<uint8_t>(code[n][e]);
+      }
+    } else if (kind == 0) {
+      uint32_t word[2] = {0, 0};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) word[n] |= static_cast<uint32_t>(code[n][e]) << (4 * ((e & 1) * 4 + (e >> 1)));
+      if (whole) {
+        reinterpret_cast<uint2*>(out)[lane] = make_uint2(word[0], word[1]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (have[n]) *reinterpret_cast<uint32_t*>(out + lane * 8 + 4 * n) = word[n];
+      }
+    } else {
+      const uint32_t c[2] = {nibbles8(code[0]), nibbles8(code[1])};
+      if (whole) {
+        put_values_q4(out, c, a, b, t);
+      } else {
+        // lanes t and t ^ 1 share bytes: the even one writes token n = 0, the odd one n = 1
+        const uint32_t other = swap_lane((t & 1) ? c[0] : c[1], 1);
+        const uint32_t lo = (t & 1) ? other : c[0], hi = (t & 1) ? c[1] : other;
+        if ((t & 1) ? have[1] : have[0])
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            out[e * 32 + a * 8 + (t >> 1) * 4 + b * 2 + (t & 1)] =
+                static_cast<uint8_t>(((lo >> (4 * e)) & 15u) | (((hi >> (4 * e)) & 15u) << 4));
+      }
+    }
+  } else {
+    constexpr bool BF = TYPE == RG_BF16;
+    uint32_t word[2][4];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        word[n][e] = pack16<BF>(x[n][2 * e], x[n][2 * e + 1]);
+        over |= overflowed16<BF>(x[n][2 * e], word[n][e]) || overflowed16<BF>(x[n][2 * e + 1], word[n][e] >> 16);
+      }
+    if (over) report_range(status);
+    if (kind == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        if (have[n])
+          reinterpret_cast<uint4*>(out)[n * 32 + lane] = make_uint4(word[n][0], word[n][1], word[n][2], word[n][3]);
+    } else if (whole) {
+      put_values_16(out, word, a, b, t);
+    } else {
+      // dimension 8t + e of token j: [t / 2][e][j / 4][t % 2][j % 4]
+      uint16_t* to = reinterpret_cast<uint16_t*>(out) + (t >> 1) * 256 + a * 8 + (t & 1) * 4 + b;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        if (have[n])
+#pragma unroll
+          for (int e = 0; e < 8; ++e) to[e * 32 + 2 * n] = static_cast<uint16_t>(word[n][e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// blocks of 32 dimensions whose loads are in flight together
+template <int AT>
+constexpr int kAhead = AT == RG_F32 ? 2 : 4;
+
 // grid (windows of `window` packed tokens, groups of kWarps (head, kind) pairs)
 template <int TYPE, int AT>
 __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(Cache c, Batch b, Rows in, int window, int* status) {
-  __shared__ __align__(16) uint8_t stage[kWarps][1024];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.y * kWarps + warp;
   if (unit >= 2 * c.kv_heads) return;
   const int kind = unit / c.kv_heads, head = unit % c.kv_heads;
   const void* src = in.p[kind];
   if (!src) return;
-  const int gb = granule_bytes(TYPE, c.dim), blocks = c.dim / 32;
-  const int key0 = 4 * (g >> 1) + (g & 1);
-  for (int w = 0; w < window; ++w) {
-    const int i = blockIdx.x * window + w;
-    if (i >= b.tokens) return;
-    Piece pc;
-    if (!piece_at(c, b, i, gb, status, &pc) || !pc.ok) continue;
+  const int blocks = c.dim / 32, key0 = 4 * (g >> 1) + (g & 1);
+  Pieces pieces;
+  pieces.find(c, b, window, granule_bytes(TYPE, c.dim), status);
+  Piece pc;
+  while (pieces.next(&pc)) {
+    if (!pc.ok) continue;
     uint8_t* dst = c.data + pc.off + (static_cast<int64_t>(kind) * c.kv_heads + head) * c.slab_bytes;
+    uint16_t* scales = reinterpret_cast<uint16_t*>(dst + blocks * block16_bytes(TYPE));
     bool have[2];
     int64_t at[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int j = key0 + 2 * n;
       have[n] = j >= pc.j0 && j < pc.j0 + pc.cnt;
-      at[n] = (pc.token + j - pc.j0) * in.t[kind] + head * in.h[kind] + 8 * t;
+      // (a token that is not there loads the piece's first: no branch around the loads)
+      at[n] = (pc.token + (have[n] ? j - pc.j0 : 0)) * in.t[kind] + head * in.h[kind] + 8 * t;
     }
-    const bool whole = pc.cnt == kGranule;
-    for (int blk = 0; blk < blocks; ++blk) {
-      float x[2][8];
+    for (int blk = 0; blk < blocks; blk += kAhead<AT>) {
+      Raw<AT> raw[kAhead<AT>][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        if (have[n])
-          load8<AT>(src, at[n] + 32 * blk, x[n]);
-        else
+      for (int u = 0; u < kAhead<AT>; ++u)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[n][e] = 0.0f;
-      }
-      if constexpr (has_scales(TYPE)) {
-        int code[2][8];
-        uint16_t d[2];
+        for (int n = 0; n < 2; ++n) raw[u][n] = load_raw<AT>(src, at[n] + 32 * min(blk + u, blocks - 1));
 #pragma unroll
-        for (int n = 0; n < 2; ++n) d[n] = quantise8<TYPE>(x[n], t, code[n], status);
-        uint8_t* out = dst + blk * block16_bytes(TYPE);
-        uint16_t* scales = reinterpret_cast<uint16_t*>(dst + blocks * block16_bytes(TYPE));
-        if (t == 0) {
+      for (int u = 0; u < kAhead<AT>; ++u) {
+        if (blk + u >= blocks) break;
+        float x[2][8];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-            if (have[n]) scales[16 * blk + (kind == 0 ? 2 * g + n : key0 + 2 * n)] = d[n];
+        for (int n = 0; n < 2; ++n) {
+          raw_f32<AT>(raw[u][n], x[n]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[n][e] = have[n] ? x[n][e] : 0.0f;
         }
-        if constexpr (TYPE == RG_Q8_0) {
-          if (kind == 0) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-              if (have[n])
-                *reinterpret_cast<uint2*>(out + lane * 16 + 8 * n) =
-                    make_uint2(bytes4(code[n][0], code[n][1], code[n][2], code[n][3]),
-                               bytes4(code[n][4], code[n][5], code[n][6], code[n][7]));
-          } else {
-            // dimension 8t + e of token j: [e][j / 4][t][j % 4]
-            uint8_t* to = whole ? stage[warp] : out;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int j = key0 + 2 * n;
-              if (have[n])
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to[e * 64 + (j >> 2) * 16 + t * 4 + (j & 3)] = code[n][e];
-            }
-            if (whole) {
-              __syncwarp();
-              reinterpret_cast<uint4*>(out)[lane] = reinterpret_cast<uint4*>(stage[warp])[lane];
-              __syncwarp();
-            }
-          }
-        } else {
-          if (kind == 0) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              uint32_t word = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) word |= static_cast<uint32_t>(code[n][e]) << (4 * ((e & 1) * 4 + (e >> 1)));
-              if (have[n]) *reinterpret_cast<uint32_t*>(out + lane * 8 + 4 * n) = word;
-            }
-          } else {
-            // a byte holds dimensions 8q + e and 8(q + 1) + e, q even: lanes t = q and q + 1.
-            // Each pair of lanes exchanges its codes; the even one writes token n = 0, the odd one n = 1.
-            uint32_t word[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              word[n] = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) word[n] |= static_cast<uint32_t>(code[n][e]) << (4 * e);
-            }
-            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, (t & 1) ? word[0] : word[1], 1);
-            const uint32_t lo = (t & 1) ? other : word[0], hi = (t & 1) ? word[1] : other;
-            const int j = key0 + 2 * (t & 1);
-            uint8_t* to = whole ? stage[warp] : out;
-            if ((t & 1) ? have[1] : have[0])
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                to[e * 32 + (j >> 2) * 8 + (t >> 1) * 4 + (j & 1) * 2 + ((j >> 1) & 1)] =
-                    static_cast<uint8_t>(((lo >> (4 * e)) & 15u) | (((hi >> (4 * e)) & 15u) << 4));
-            if (whole) {
-              __syncwarp();
-              reinterpret_cast<uint2*>(out)[lane] = reinterpret_cast<uint2*>(stage[warp])[lane];
-              __syncwarp();
-            }
-          }
-        }
-      } else {
-        constexpr bool BF = TYPE == RG_BF16;
-        uint32_t word[2][4];
-        bool over = false;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            word[n][e] = pack16<BF>(x[n][2 * e], x[n][2 * e + 1]);
-            over |= overflowed16<BF>(x[n][2 * e], word[n][e]) || overflowed16<BF>(x[n][2 * e + 1], word[n][e] >> 16);
-          }
-        if (over) report_range(status);
-        if (kind == 0) {
-          uint4* out = reinterpret_cast<uint4*>(dst + blk * 1024);
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            if (have[n]) out[n * 32 + lane] = make_uint4(word[n][0], word[n][1], word[n][2], word[n][3]);
-        } else {
-          // dimension 8t + e of token j: [t / 2][e][j / 4][t % 2][j % 4]
-          uint16_t* to = reinterpret_cast<uint16_t*>(whole ? stage[warp] : dst + blk * 1024);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int j = key0 + 2 * n;
-            if (have[n])
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                to[(t >> 1) * 256 + e * 32 + (j >> 2) * 8 + (t & 1) * 4 + (j & 3)] =
-                    static_cast<uint16_t>(word[n][e >> 1] >> (16 * (e & 1)));
-          }
-          if (whole) {
-            __syncwarp();
-            uint4* out = reinterpret_cast<uint4*>(dst + blk * 1024);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) out[n * 32 + lane] = reinterpret_cast<uint4*>(stage[warp])[n * 32 + lane];
-            __syncwarp();
-          }
-        }
+        store_block<TYPE>(x, dst + (blk + u) * block16_bytes(TYPE), scales + 16 * (blk + u), kind, pc.cnt == kGranule,
+                          have, status);
       }
     }
   }
 }
 
+// The stored words of one block, as loaded.
+template <int TYPE>
+struct Stored {
+  uint32_t w[TYPE == RG_Q8_0 ? 4 : TYPE == RG_Q4_0 ? 2 : 8];
+  uint32_t d;  // scales of the lane's two tokens
+};
+template <int TYPE>
+__device__ __forceinline__ Stored<TYPE> load_stored(const uint8_t* in, const uint16_t* scales, int kind) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, a = g >> 1, b = g & 1;
+  Stored<TYPE> s;
+  if constexpr (has_scales(TYPE)) {
+    if (kind == 0) {
+      s.d = __ldg(reinterpret_cast<const uint32_t*>(scales) + g);
+    } else {
+      const uint32_t d0 = __ldg(scales + 4 * a + b), d1 = __ldg(scales + 4 * a + b + 2);
+      s.d = d0 | (d1 << 16);
+    }
+  }
+  if constexpr (TYPE == RG_Q8_0) {
+    if (kind == 0) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(in) + lane);
+      s.w[0] = v.x; s.w[1] = v.y; s.w[2] = v.z; s.w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s.w[e] = __ldg(reinterpret_cast<const uint32_t*>(in + (4 * b + e) * 64 + a * 16 + t * 4));
+    }
+  } else if constexpr (TYPE == RG_Q4_0) {
+    if (kind == 0) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(in) + lane);
+      s.w[0] = v.x; s.w[1] = v.y;
+    } else {
+      const uint8_t* p = in + (4 * (t & 1) + 2 * b) * 32 + a * 8 + (t >> 1) * 4;
+      s.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      s.w[1] = __ldg(reinterpret_cast<const uint32_t*>(p + 32));
+    }
+  } else {
+    if (kind == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(in) + n * 32 + lane);
+        s.w[4 * n] = v.x; s.w[4 * n + 1] = v.y; s.w[4 * n + 2] = v.z; s.w[4 * n + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint2 v =
+            __ldg(reinterpret_cast<const uint2*>(in + (t >> 1) * 512 + (4 * b + e) * 64 + a * 16 + (t & 1) * 8));
+        s.w[2 * e] = v.x; s.w[2 * e + 1] = v.y;
+      }
+    }
+  }
+  return s;
+}
+template <int TYPE>
+__device__ __forceinline__ void stored_f32(const Stored<TYPE>& s, int kind, float (&x)[2][8]) {
+  const int lane = threadIdx.x & 31, t = lane & 3, b = (lane >> 2) & 1;
+  if constexpr (has_scales(TYPE)) {
+    const float d[2] = {f16_to_f32(static_cast<uint16_t>(s.d & 0xFFFFu)), f16_to_f32(static_cast<uint16_t>(s.d >> 16))};
+    if constexpr (TYPE == RG_Q8_0) {
+      uint32_t c[2][2] = {{s.w[0], s.w[1]}, {s.w[2], s.w[3]}};
+      if (kind != 0) get_values_q8(s.w, c, b);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[n][e] = d[n] * static_cast<float>(static_cast<int8_t>(c[n][e >> 2] >> (8 * (e & 3))));
+    } else if (kind == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[n][e] = d[n] * static_cast<float>(static_cast<int>((s.w[n] >> (4 * ((e & 1) * 4 + (e >> 1)))) & 15u) - 8);
+    } else {
+      uint32_t c[2][2];
+      get_values_q4(s.w, c, b, t);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[n][e] = d[n] * static_cast<float>(static_cast<int>((c[n][e >> 2] >> (8 * (e & 3) + 4 * (t & 1))) & 15u) - 8);
+    }
+  } else {
+    constexpr bool BF = TYPE == RG_BF16;
+    uint32_t w[2][4];
+    if (kind == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[n][i] = s.w[4 * n + i];
+    } else {
+      const uint2 v[4] = {make_uint2(s.w[0], s.w[1]), make_uint2(s.w[2], s.w[3]), make_uint2(s.w[4], s.w[5]),
+                          make_uint2(s.w[6], s.w[7])};
+      get_values_16(v, w, b);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t h = static_cast<uint16_t>(w[n][e >> 1] >> (16 * (e & 1)));
+        x[n][e] = BF ? bf16_to_f32(h) : f16_to_f32(h);
+      }
+  }
+}
+
 template <int TYPE, int AT>
 __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(Cache c, Batch b, OutRows to, int window, int* status) {
-  __shared__ __align__(16) uint8_t stage[kWarps][1024];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.y * kWarps + warp;
   if (unit >= 2 * c.kv_heads) return;
   const int kind = unit / c.kv_heads, head = unit % c.kv_heads;
   void* dst = to.p[kind];
   if (!dst) return;
-  const int gb = granule_bytes(TYPE, c.dim), blocks = c.dim / 32;
-  const int key0 = 4 * (g >> 1) + (g & 1);
-  for (int w = 0; w < window; ++w) {
-    const int i = blockIdx.x * window + w;
-    if (i >= b.tokens) return;
-    Piece pc;
-    if (!piece_at(c, b, i, gb, status, &pc)) continue;
+  const int blocks = c.dim / 32, key0 = 4 * (g >> 1) + (g & 1);
+  constexpr int U = has_scales(TYPE) ? 4 : 2;
+  Pieces pieces;
+  pieces.find(c, b, window, granule_bytes(TYPE, c.dim), status);
+  Piece pc;
+  while (pieces.next(&pc)) {
     const uint8_t* src = c.data + pc.off + (static_cast<int64_t>(kind) * c.kv_heads + head) * c.slab_bytes;
+    const uint16_t* scales = reinterpret_cast<const uint16_t*>(src + blocks * block16_bytes(TYPE));
     bool have[2];
     int64_t at[2];
 #pragma unroll
@@ -284,101 +559,29 @@ __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(Cache c, Batch b, 
       have[n] = j >= pc.j0 && j < pc.j0 + pc.cnt;
       at[n] = (pc.token + j - pc.j0) * to.t[kind] + head * to.h[kind] + 8 * t;
     }
-    for (int blk = 0; blk < blocks; ++blk) {
-      float x[2][8];
-      if (!pc.ok) {  // no place in the cache: zeros
+    for (int blk = 0; blk < blocks; blk += U) {
+      Stored<TYPE> s[U] = {};
+      if (pc.ok) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[n][e] = 0.0f;
-      } else if constexpr (has_scales(TYPE)) {
-        const uint8_t* in = src + blk * block16_bytes(TYPE);
-        const uint16_t* scales = reinterpret_cast<const uint16_t*>(src + blocks * block16_bytes(TYPE)) + 16 * blk;
-        float d[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) d[n] = f16_to_f32(scales[kind == 0 ? 2 * g + n : key0 + 2 * n]);
-        if constexpr (TYPE == RG_Q8_0) {
-          const uint4 v = reinterpret_cast<const uint4*>(in)[lane];
-          if (kind == 0) {
-            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                x[n][e] = d[n] * static_cast<float>(static_cast<int8_t>(word[2 * n + (e >> 2)] >> (8 * (e & 3))));
-          } else {
-            __syncwarp();
-            reinterpret_cast<uint4*>(stage[warp])[lane] = v;
-            __syncwarp();
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int j = key0 + 2 * n;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                x[n][e] = d[n] * static_cast<float>(
-                                     static_cast<int8_t>(stage[warp][e * 64 + (j >> 2) * 16 + t * 4 + (j & 3)]));
-            }
-          }
-        } else {
-          const uint2 v = reinterpret_cast<const uint2*>(in)[lane];
-          if (kind == 0) {
-            const uint32_t word[2] = {v.x, v.y};
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                x[n][e] = d[n] * static_cast<float>(
-                                     static_cast<int>((word[n] >> (4 * ((e & 1) * 4 + (e >> 1)))) & 15u) - 8);
-          } else {
-            __syncwarp();
-            reinterpret_cast<uint2*>(stage[warp])[lane] = v;
-            __syncwarp();
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int j = key0 + 2 * n;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int byte =
-                    stage[warp][e * 32 + (j >> 2) * 8 + (t >> 1) * 4 + (j & 1) * 2 + ((j >> 1) & 1)];
-                x[n][e] = d[n] * static_cast<float>(((byte >> (4 * (t & 1))) & 15) - 8);
-              }
-            }
-          }
-        }
-      } else {
-        constexpr bool BF = TYPE == RG_BF16;
-        const uint4* in = reinterpret_cast<const uint4*>(src + blk * 1024);
-        const uint4 v[2] = {in[lane], in[32 + lane]};
-        if (kind == 0) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t word[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint16_t h = static_cast<uint16_t>(word[e >> 1] >> (16 * (e & 1)));
-              x[n][e] = BF ? bf16_to_f32(h) : f16_to_f32(h);
-            }
-          }
-        } else {
-          __syncwarp();
-          reinterpret_cast<uint4*>(stage[warp])[lane] = v[0];
-          reinterpret_cast<uint4*>(stage[warp])[32 + lane] = v[1];
-          __syncwarp();
-          const uint16_t* in16 = reinterpret_cast<const uint16_t*>(stage[warp]);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int j = key0 + 2 * n;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint16_t h = in16[(t >> 1) * 256 + e * 32 + (j >> 2) * 8 + (t & 1) * 4 + (j & 3)];
-              x[n][e] = BF ? bf16_to_f32(h) : f16_to_f32(h);
-            }
-          }
+        for (int u = 0; u < U; ++u) {
+          const int k = min(blk + u, blocks - 1);
+          s[u] = load_stored<TYPE>(src + k * block16_bytes(TYPE), scales + 16 * k, kind);
         }
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        if (have[n]) store8<AT>(dst, at[n] + 32 * blk, x[n]);
+      for (int u = 0; u < U; ++u) {
+        if (blk + u >= blocks) break;
+        float x[2][8];
+        stored_f32<TYPE>(s[u], kind, x);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (!pc.ok) {  // no place in the cache: zeros
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[n][e] = 0.0f;
+          }
+          if (have[n]) store8<AT>(dst, at[n] + 32 * (blk + u), x[n]);
+        }
+      }
     }
   }
 }
