@@ -18,54 +18,66 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Codes of 8 values of a row whose 32-value block lies in lanes t = 0..3 of
-// the same g: codes[e] (int8 as 0..255, or 0..15) and the block's fp16 scale.
+// Codes of 8 values of two tokens whose 32-value blocks lie in lanes t = 0..3 of
+// the same g: code[n][e], the int8 code's or the unsigned nibble's bits in the low
+// byte (the rest is not zero; for blocks with zero[n] set, nothing is).  Returns the
+// fp16 scale of token 0 in lane t = 0 and that of token 1 in lane t = 2.
 template <int TYPE>
-__device__ __forceinline__ uint16_t quantise8(const float (&x)[8], int t, int (&code)[8], int* status) {
-  // the largest magnitude as an integer: infinities and NaN are larger than every finite value
-  uint32_t m = 0;
-  int at = 0;
+__device__ __forceinline__ uint16_t quantise8(const float (&x)[2][8], int t, uint32_t (&code)[2][8], bool (&zero)[2],
+                                              int* status) {
+  uint32_t big[2];
+  float top[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-    if (b > m) { m = b; at = e; }
-  }
-  uint32_t big = m;
-  big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-  big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-  float top = __uint_as_float(big);
-  if constexpr (TYPE == RG_Q4_0) {
-    // sign of the first value of that magnitude: the smallest index that has it
-    int first = m == big ? 2 * (8 * t + at) + (x[at] < 0.0f) : 1 << 16;
-    first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 1));
-    first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 2));
-    if (first & 1) top = -top;
+  for (int n = 0; n < 2; ++n) {
+    // the largest magnitude as an integer: infinities and NaN are larger than every finite value
+    uint32_t m = 0;
+    int first = 0;  // 2 * its first index + 1 if negative
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = __float_as_uint(x[n][e]) & 0x7FFFFFFFu;
+      if (TYPE == RG_Q4_0 && b > m) first = 2 * (8 * t + e) + (__float_as_uint(x[n][e]) >> 31);
+      m = max(m, b);
+    }
+    uint32_t v = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+    big[n] = v;
+    top[n] = __uint_as_float(v);
+    if constexpr (TYPE == RG_Q4_0) {
+      if (m != v) first = 1 << 16;
+      first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 1));
+      first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 2));
+      if (first & 1) top[n] = -top[n];
+    }
   }
   constexpr float kSteps = TYPE == RG_Q8_0 ? 127.0f : -8.0f;
-  __half d = __float2half_rn(top / kSteps);
-  float inv = kSteps / top;
-  if (big >= 0x7F800000u) {  // a value that is not finite: the block reads back as NaN
-    d = __ushort_as_half(0x7E00);
-    inv = 0.0f;
-  } else {
-    if (big > 0x477FE000u) report_range(status);  // 65504: past the fp16 operands of the attention
-    if ((__half_as_ushort(d) & 0x7FFFu) == 0) inv = 0.0f;  // rounds to zero: zero codes
-  }
+  // four lanes share four divisions: top / steps in t = 0 and 2, steps / top in t = 1 and 3
+  const float mine = t & 2 ? top[1] : top[0];
+  const float quotient = t & 1 ? kSteps / mine : mine / kSteps;
+  uint16_t d = __half_as_ushort(__float2half_rn(quotient));
+  const uint32_t mag = t & 2 ? big[1] : big[0];
+  if (mag >= 0x7F800000u) d = 0x7E00;  // a value that is not finite: the block reads back as NaN
+  else if (mag > 0x477FE000u) report_range(status);  // 65504: past the fp16 operands of the attention
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // inv 0 gives the zero code, also for values that are not finite (their product is NaN or 0)
-    const float r = inv == 0.0f ? 0.0f : rintf(x[e] * inv);
-    if constexpr (TYPE == RG_Q8_0)
-      code[e] = static_cast<int>(r) & 255;
-    else
-      code[e] = min(max(static_cast<int>(r) + 8, 0), 15);
+  for (int n = 0; n < 2; ++n) {
+    const int lane = (threadIdx.x & 28) + 2 * n;
+    const float inv = __shfl_sync(0xFFFFFFFFu, quotient, lane + 1);
+    const uint16_t dn = static_cast<uint16_t>(__shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(d), lane));
+    // a scale that rounds to zero, and a block that is not finite, have zero codes
+    zero[n] = (dn & 0x7FFFu) == 0 || big[n] >= 0x7F800000u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // Adding 1.5 * 2^23 rounds to an integer (nearest even) and leaves it in the low bits.
+      const uint32_t r = __float_as_uint(__fadd_rn(__fmul_rn(x[n][e], inv), 12582912.0f));
+      // (Q4_0: -8 .. 8, of which 8 has no code and becomes 7; + 8)
+      code[n][e] = TYPE == RG_Q8_0 ? r : min(r, 0x4B400007u) + 8u;
+    }
   }
-  return __half_as_ushort(d);
+  return d;
 }
 
-__device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d) {
-  return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 8) | (static_cast<uint32_t>(c) << 16) |
-         (static_cast<uint32_t>(d) << 24);
+// the low bytes of four words
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // A granule's share of the batch's new tokens.
@@ -270,11 +282,14 @@ __device__ __forceinline__ void get_values_16(const uint2 (&v)[4], uint32_t (&w)
   }
 }
 
-__device__ __forceinline__ uint32_t nibbles8(const int (&c)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w |= static_cast<uint32_t>(c[e]) << (4 * e);
-  return w;
+// the low nibbles of eight words: word e's at nibble e, or (KEYS) at nibble (e % 2) * 4 + e / 2
+template <bool KEYS>
+__device__ __forceinline__ uint32_t nibbles8(const uint32_t (&c)[8]) {
+  const uint32_t even = bytes4(c[0], c[2], c[4], c[6]) & 0x0F0F0F0Fu, odd = bytes4(c[1], c[3], c[5], c[7]) & 0x0F0F0F0Fu;
+  if constexpr (!KEYS) return even | (odd << 4);
+  // even values in the low half, odd ones in the high half
+  const uint32_t lo = even | (even >> 4), hi = odd | (odd >> 4);  // bytes 0 and 2 hold two nibbles each
+  return __byte_perm(lo, hi, 0x6420);
 }
 
 // One block (32 dimensions) of up to 16 tokens into the cache.  out: the block's codes,
@@ -284,22 +299,18 @@ __device__ __forceinline__ void store_block(const float (&x)[2][8], uint8_t* out
                                             const bool (&have)[2], int* status) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, a = g >> 1, b = g & 1, key0 = 4 * a + b;
   if constexpr (has_scales(TYPE)) {
-    int code[2][8];
-    uint16_t d[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) d[n] = quantise8<TYPE>(x[n], t, code[n], status);
-    if (t == 0) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        if (have[n]) scales[kind == 0 ? 2 * g + n : key0 + 2 * n] = d[n];
-    }
+    uint32_t code[2][8];
+    bool zero[2];
+    const uint16_t d = quantise8<TYPE>(x, t, code, zero, status);
+    if ((t & 1) == 0 && (t ? have[1] : have[0])) scales[kind == 0 ? 2 * g + (t >> 1) : key0 + t] = d;
     if constexpr (TYPE == RG_Q8_0) {
       uint32_t c[2][2];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          c[n][i] = bytes4(code[n][4 * i], code[n][4 * i + 1], code[n][4 * i + 2], code[n][4 * i + 3]);
+          c[n][i] =
+              zero[n] ? 0u : bytes4(code[n][4 * i], code[n][4 * i + 1], code[n][4 * i + 2], code[n][4 * i + 3]);
       if (kind == 0) {
         if (whole) {
           reinterpret_cast<uint4*>(out)[lane] = make_uint4(c[0][0], c[0][1], c[1][0], c[1][1]);
@@ -316,14 +327,12 @@ __device__ __forceinline__ void store_block(const float (&x)[2][8], uint8_t* out
         for (int n = 0; n < 2; ++n)
           if (have[n])
 #pragma unroll
-            for (int e = 0; e < 8; ++e) out[e * 64 + a * 16 + t * 4 + b + 2 * n] = static_cast<uint8_t>(code[n][e]);
+            for (int e = 0; e < 8; ++e)
+              out[e * 64 + a * 16 + t * 4 + b + 2 * n] = static_cast<uint8_t>(c[n][e >> 2] >> (8 * (e & 3)));
       }
     } else if (kind == 0) {
-      uint32_t word[2] = {0, 0};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) word[n] |= static_cast<uint32_t>(code[n][e]) << (4 * ((e & 1) * 4 + (e >> 1)));
+      const uint32_t word[2] = {zero[0] ? 0x88888888u : nibbles8<true>(code[0]),
+                                zero[1] ? 0x88888888u : nibbles8<true>(code[1])};
       if (whole) {
         reinterpret_cast<uint2*>(out)[lane] = make_uint2(word[0], word[1]);
       } else {
@@ -332,7 +341,8 @@ __device__ __forceinline__ void store_block(const float (&x)[2][8], uint8_t* out
           if (have[n]) *reinterpret_cast<uint32_t*>(out + lane * 8 + 4 * n) = word[n];
       }
     } else {
-      const uint32_t c[2] = {nibbles8(code[0]), nibbles8(code[1])};
+      const uint32_t c[2] = {zero[0] ? 0x88888888u : nibbles8<false>(code[0]),
+                             zero[1] ? 0x88888888u : nibbles8<false>(code[1])};
       if (whole) {
         put_values_q4(out, c, a, b, t);
       } else {
@@ -383,7 +393,7 @@ constexpr int kAhead = AT == RG_F32 ? 2 : 4;
 
 // grid (windows of `window` packed tokens, groups of kWarps (head, kind) pairs)
 template <int TYPE, int AT>
-__global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(Cache c, Batch b, Rows in, int window, int* status) {
+__global__ void __launch_bounds__(32 * kWarps, AT == RG_F32 ? 2 : 3) kv_write_kernel(Cache c, Batch b, Rows in, int window, int* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.y * kWarps + warp;
   if (unit >= 2 * c.kv_heads) return;
@@ -420,8 +430,9 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(Cache c, Batch b,
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           raw_f32<AT>(raw[u][n], x[n]);
+          if (pc.cnt < kGranule)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[n][e] = have[n] ? x[n][e] : 0.0f;
+            for (int e = 0; e < 8; ++e) x[n][e] = have[n] ? x[n][e] : 0.0f;
         }
         store_block<TYPE>(x, dst + (blk + u) * block16_bytes(TYPE), scales + 16 * (blk + u), kind, pc.cnt == kGranule,
                           have, status);
