@@ -547,7 +547,7 @@ __device__ __forceinline__ void stored_f32(const Stored<TYPE>& s, int kind, floa
 }
 
 template <int TYPE, int AT>
-__global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(Cache c, Batch b, OutRows to, int window, int* status) {
+__global__ void __launch_bounds__(32 * kWarps, 4) kv_read_kernel(Cache c, Batch b, OutRows to, int window, int* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.y * kWarps + warp;
   if (unit >= 2 * c.kv_heads) return;
