@@ -65,6 +65,11 @@ __device__ __forceinline__ Shape shape_of(const Seq& q, int group, int bm, int w
   return s;
 }
 
+// a / b for a >= 0, b > 0: 32-bit division where that is enough (it mostly is).
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
     attend_rows_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
@@ -75,14 +80,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
   __shared__ __align__(8) uint64_t full[kWarps][C::STAGES];
   __shared__ float sm_m[kWarps][C::BM], sm_l[kWarps][C::BM];
   __shared__ long long sh_sum[kWarps];
-  __shared__ long long sh_acc;
-  __shared__ int sh_seq, sh_abort;
+  __shared__ int sh_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = a.group;
 
   if (lane < C::STAGES) mbar_init(smem_addr(&full[warp][lane]), 1);
   if (tid == 0) sh_abort = 0;
   fence_mbar_init();
+  pdl_launch_dependents();  // (the joining kernel waits for this one's end before it reads)
 
   // this CTA's share [lo, hi) of the line of tiles
   auto tiles_of = [&](int s) -> long long {
@@ -90,47 +95,55 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
     const Shape sh = shape_of(q, G, C::BM, a.window, a.rows_limit);
     return static_cast<long long>(sh.rb) * sh.nt * c.kv_heads;
   };
-  long long sum = 0;
-  for (int s = tid; s < b.seqs; s += 32 * kWarps) sum += tiles_of(s);
+  // tiles of 32 sequences by lane, and with those before
+  auto scan = [&](int s0, long long* inc) {
+    const long long v = s0 + lane < b.seqs ? tiles_of(s0 + lane) : 0;
+    *inc = v;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) sh_sum[warp] = sum;
-  __syncthreads();
-  long long total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, *inc, o);
+      if (lane >= o) *inc += u;
+    }
+    return v;
+  };
+  long long inc0, total;
+  const long long v0 = scan(0, &inc0);
+  if (b.seqs <= 32) {  // every warp for itself
+    total = __shfl_sync(0xFFFFFFFFu, inc0, 31);
+  } else {
+    long long sum = 0;
+    for (int s = tid; s < b.seqs; s += 32 * kWarps) sum += tiles_of(s);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh_sum[w];
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) sh_sum[warp] = sum;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += sh_sum[w];
+  }
+  const long long per = quotient(total + gridDim.x - 1, gridDim.x);
   const long long lo = per * blockIdx.x, hi = min(total, lo + per);
   if (lo >= hi) {
     if (tid == 0) desc[blockIdx.x].last = -1;
     return;
   }
-  if (warp == 0) {  // the sequence that tile lo belongs to
-    long long acc = 0;
-    for (int s0 = 0;; s0 += 32) {
-      const long long v = s0 + lane < b.seqs ? tiles_of(s0 + lane) : 0;
-      long long inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, acc + inc > lo);
-      if (past || s0 + 32 >= b.seqs) {
-        const int l = past ? __ffs(past) - 1 : 31;
-        const long long before = acc + __shfl_sync(0xFFFFFFFFu, inc - v, l);
-        if (lane == 0) {
-          sh_seq = s0 + l;
-          sh_acc = before;
-        }
-        break;
-      }
-      acc += __shfl_sync(0xFFFFFFFFu, inc, 31);
+  // the sequence that tile lo belongs to
+  int seq = 0;
+  long long acc = 0;
+  for (int s0 = 0;; s0 += 32) {
+    long long inc = inc0, v = v0;
+    if (s0) v = scan(s0, &inc);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, acc + inc > lo);
+    if (past || s0 + 32 >= b.seqs) {
+      const int l = past ? __ffs(past) - 1 : 31;
+      seq = s0 + l;
+      acc += __shfl_sync(0xFFFFFFFFu, inc - v, l);
+      break;
     }
+    acc += __shfl_sync(0xFFFFFFFFu, inc, 31);
   }
   __syncthreads();
-  int seq = sh_seq;
-  long long acc = sh_acc, at = lo;
+  long long at = lo;
   bool headed = false;
   uint32_t it = 0;  // granules this warp has taken from its ring
   const uint32_t ring = smem_addr(smem) + C::QBYTES + warp * C::STAGES * C::STAGE;
@@ -146,8 +159,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
       ++seq;
       continue;
     }
-    const int item = static_cast<int>((at - acc) / sh.nt);
-    const int tile = static_cast<int>((at - acc) % sh.nt);
+    const int item = static_cast<int>(quotient(at - acc, sh.nt));
+    const int tile = static_cast<int>(at - acc - static_cast<long long>(item) * sh.nt);
     const int tend = static_cast<int>(min(static_cast<long long>(sh.nt), tile + (hi - at)));
     const int head = item / sh.rb, rb = item % sh.rb;
     const int row0 = rb * C::BM, nrows = sq.n * G, first = sq.len - sq.n;
@@ -163,24 +176,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
         const int row = 8 * m + 2 * t + r;
         pos[m][r] = row < rows ? first + (row0 + row) / G : -1;
       }
-
-    // queries as B operands: row 8m + g, dimensions 32k + 8t .. + 7
-    uint4 qreg[C::QREG ? NT : 1][C::QREG ? BLK : 1];
-    auto query = [&](int m, int k) {
-      const int row = row0 + 8 * m + g;
-      return row < row0 + rows ? query8<BF>(a, (sq.start + row / G) * a.q_t + (head * G + row % G) * a.q_h + 32 * k + 8 * t,
-                                            ctl.status)
-                               : make_uint4(0, 0, 0, 0);
-    };
-    if constexpr (C::QREG) {
-#pragma unroll
-      for (int m = 0; m < NT; ++m)
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) qreg[m][k] = query(m, k);
-    } else {
-      for (int u = warp; u < NT * BLK; u += kWarps) reinterpret_cast<uint4*>(smem)[u * 32 + lane] = query(u / BLK, u % BLK);
-      __syncthreads();
-    }
 
     // o[m][i]: dimensions 16i + g (words 0, 1: rows 2t, 2t + 1) and 16i + 8 + g (2, 3)
     float o[NT][D / 16][4], m_ref[NT][2], l_sum[NT][2];
@@ -231,6 +226,27 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
       }
       st_in = st_in + 1 == C::STAGES ? 0 : st_in + 1;
     };
+
+    const int first_batch = min(count, C::STAGES);
+    for (int k = 0; k < first_batch; ++k) issue(k);
+
+    // queries as B operands: row 8m + g, dimensions 32k + 8t .. + 7
+    uint4 qreg[C::QREG ? NT : 1][C::QREG ? BLK : 1];
+    auto query = [&](int m, int k) {
+      const int row = row0 + 8 * m + g;
+      return row < row0 + rows ? query8<BF>(a, (sq.start + row / G) * a.q_t + (head * G + row % G) * a.q_h + 32 * k + 8 * t,
+                                            ctl.status)
+                               : make_uint4(0, 0, 0, 0);
+    };
+    if constexpr (C::QREG) {
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) qreg[m][k] = query(m, k);
+    } else {
+      for (int u = warp; u < NT * BLK; u += kWarps) reinterpret_cast<uint4*>(smem)[u * 32 + lane] = query(u / BLK, u % BLK);
+      __syncthreads();
+    }
 
     // N granules gran, gran + kWarps, ... in stages at kb[]: scores, probabilities, products
     // with the values.  have: bit u, granule u's page exists (MASKED only)
@@ -354,7 +370,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
 
     bool gave_up = false;
     uint32_t st = it % C::STAGES, phase = it / C::STAGES & 1;  // of the next granule to use
-    for (int k = 0; k < min(count, C::STAGES); ++k) issue(k);
     for (int k = 0; k < count;) {
       // as many as a step takes, if they are there
       const int n = C::NG == 2 && k + 1 < count ? 2 : 1;
@@ -386,10 +401,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
         if constexpr (C::NG == 2) {
           if (whole)
             step(std::false_type{}, std::integral_constant<int, 2>{}, gran, kb, have);
-          else
+          else {
+            uint32_t at = kb[0];
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u)
-              step(std::true_type{}, std::integral_constant<int, 1>{}, gran + kWarps * u, &kb[u], have >> u);
+            for (int u = 0; u < 2; ++u) {
+              step(std::true_type{}, std::integral_constant<int, 1>{}, gran + kWarps * u, &at, have >> u);
+              at = kb[1];
+            }
+          }
         }
       } else if (C::NG == 1 && whole) {
         step(std::false_type{}, std::integral_constant<int, 1>{}, gran, kb, have);
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
       if (tid == 0) {
         const long long end = acc + static_cast<long long>(item + 1) * sh.nt - 1;
         desc[blockIdx.x] =
-            Desc{static_cast<int>(end / per), rows, sq.start + row0 / G, row0 % G, head};
+            Desc{static_cast<int>(per >> 31 == 0 ? quotient(end, static_cast<int>(per)) : end / per), rows, sq.start + row0 / G, row0 % G, head};
       }
     }
     at += tend - tile;
@@ -472,7 +491,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
     __syncthreads();
   }
   if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
-  pdl_launch_dependents();
 }
 
 // Joins the parts of items that several CTAs share: block (i, y) has `stretch`
@@ -484,7 +502,7 @@ constexpr int kJoin = 512;
 __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc* desc, const float* parts, int bm,
                                                             int dim, int stretch) {
   __shared__ float sm_top[32], sm_inv[32];
-  __shared__ float sm_v[kJoin * 4];
+  __shared__ __align__(16) float sm_v[kJoin * 4];
   pdl_wait();
   const Desc ds = desc[blockIdx.x];
   const int first = blockIdx.y * stretch, rows = min(stretch, ds.rows - first);
@@ -497,12 +515,24 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
   auto part = [&](int i) { return i == 0 ? head : rest + 2 * i * size; };
   for (int r = tid >> 5; r < rows; r += kJoin / 32) {
     const int row = first + r;
-    float top = kNone;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[row]);
+    float top = kNone, l = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 128) {  // 128 parts at a time, their loads together
+      float m[4], s[4];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float l = 0.0f;
-    for (int i = lane; i < n; i += 32) l += ex2(part(i)[row] - top) * part(i)[bm + row];
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + 32 * u + lane;
+        m[u] = i < n ? part(i)[row] : kNone;
+        s[u] = i < n ? part(i)[bm + row] : 0.0f;
+      }
+      float v = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+      v = fmaxf(v, top);
+      l *= ex2(top - v);
+      top = v;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) l += s[u] * ex2(m[u] - top);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     if (lane == 0) {
@@ -520,12 +550,20 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
     float v[4] = {0, 0, 0, 0};
     if (mine) {
       const float top = sm_top[r];
-#pragma unroll 8
-      for (int i = grp; i < n; i += groups) {
-        const float* p = part(i);
-        const float f = ex2(p[row] - top);
-        const float4 x = *reinterpret_cast<const float4*>(p + 2 * bm + row * dim + d);
-        v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
+      for (int i0 = grp; i0 < n; i0 += 8 * groups) {  // eight parts at a time
+        float m[8];
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float* p = part(min(i0 + k * groups, n - 1));
+          m[k] = p[row];
+          x[k] = *reinterpret_cast<const float4*>(p + 2 * bm + row * dim + d);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = i0 + k * groups < n ? ex2(m[k] - top) : 0.0f;
+          v[0] += f * x[k].x; v[1] += f * x[k].y; v[2] += f * x[k].z; v[3] += f * x[k].w;
+        }
       }
     }
     if (groups > 1) {

@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) poison[i] = -1;
     fence_mbar_init();
   }
+  pdl_launch_dependents();  // (the joining kernel waits for this one's end before it reads)
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -881,7 +882,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  pdl_launch_dependents();
 }
 
 template <int TYPE, int D>
