@@ -1,22 +1,28 @@
 // rg_kv_tiles.cu - attention of many rows a sequence over the paged cache:
 // prompts and chunks of prompts, on the 5th-generation tensor cores.
 //
-// An item is 256 rows (new tokens x the query heads of one kv head) of a
-// sequence, two streams of 128, against its 128-token key tiles:
-//   S = Q K^T           tcgen05.mma, both operands in shared memory, S in TMEM
+// An item is 512 rows (new tokens x the query heads of one kv head) of a
+// sequence, two streams of 256, against its 128-token key tiles.  A pair of CTAs
+// (a cluster, two SMs) works on it, 128 rows of each stream a CTA:
+//   S = Q K^T           tcgen05.mma.cta_group::2, M = 256: both operands in shared
+//                       memory, S in TMEM
 //   P = 2^(S c - m)     one thread a row, TMEM -> registers -> TMEM (16 bits, over S)
-//   O += P V            tcgen05.mma, P read from TMEM, V^T from shared memory
-// While one stream's softmax runs, the tensor core works for the other.  Warps:
+//   O += P V            tcgen05.mma.cta_group::2, P read from TMEM, V^T from shared memory
+// Each CTA decodes and holds one half of a tile (64 tokens' keys; half the values'
+// dimensions) for both: one CTA alone, reading whole tiles for its 256 rows and writing
+// them itself, saturated its shared memory.  While one stream's softmax runs, the tensor
+// cores work for the other.  Warps of each CTA:
 //   0 - 7    softmax, a warpgroup a stream; they also load Q and write the result
-//   8 - 15   decoders: a granule (16 tokens) of each tile a warp, global memory ->
-//            registers -> operand tiles (128-byte swizzle), loaded a tile ahead
-//   16       issues the matrix instructions
+//   8 - 15   decoders: half a granule (16 tokens) of keys and of values of each tile a
+//            warp, global memory -> registers -> operand tiles (128-byte swizzle),
+//            loaded a tile ahead
+//   16       issues the matrix instructions (of the pair: the even CTA's)
 //   17       scheduler: page numbers and masks of the next tiles (18, 19 idle:
 //            registers are handed out by warpgroups)
 // The running maximum is a reference that moves only when a score passes it by
 // 2^8 (as in rg_kv_rows.cu), so O is rescaled, which needs the tensor core's
 // previous product finished, a few times an item.
-// All items' key tiles form one line that is cut into equal shares, one a CTA:
+// All items' key tiles form one line that is cut into equal shares, one a pair:
 // causal items of different lengths and ragged sequences balance, and a short
 // prompt over a long cache uses every SM.  An item cut by a border leaves F32
 // parts that a second kernel joins in a fixed order.
@@ -29,13 +35,13 @@ namespace kv {
 namespace {
 
 constexpr int BN = 128;          // tokens of a key tile
-constexpr int BM = 256;          // rows of an item
+constexpr int BM = 512;          // rows of an item
 constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
-// Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 152 for
-// the softmax, 256 x 72 for the decoders and 128 x 32 for the rest, the same.
-constexpr int kRegsSoft = 152, kRegsDec = 72, kRegsMma = 32;
+// Registers a thread: 96 at launch (640 threads), 61440 in all; then 256 x 168 for
+// the softmax, 256 x 56 for the decoders and 128 x 32 for the rest, the same.
+constexpr int kRegsSoft = 168, kRegsDec = 56, kRegsMma = 32;
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -45,11 +51,12 @@ constexpr int kScan = 256;       // sequences counted at a time
 
 template <int D>
 struct Cfg {
-  static constexpr int Q = 128 * D * 2;      // one stream's queries
-  static constexpr int KV = 128 * D * 2;     // one tile's keys, or values
+  static constexpr int Q = 128 * D * 2;      // a CTA's queries of one stream
+  static constexpr int KV = 64 * D * 2;      // its half of a tile's keys, or values
   static constexpr int SMEM = 2 * Q + 4 * KV + 1024;
-  static constexpr int CHUNK = 128 * 128;    // 128 rows x 64 values
-  static constexpr int VCHUNK = D * 128;     // D rows x 64 tokens
+  static constexpr int CHUNK = 128 * 128;    // queries: 128 rows x 64 dimensions
+  static constexpr int KCHUNK = 64 * 128;    // keys: 64 tokens x 64 dimensions
+  static constexpr int VCHUNK = D / 2 * 128; // values: D / 2 dimensions x 64 tokens
 };
 
 // --- the line of key tiles ----------------------------------------------------
@@ -139,7 +146,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdes
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
@@ -149,16 +156,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bde
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
+// (arrives on the barrier at this offset in both CTAs of the pair)
 __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t one) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(one)
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+          bar),
+      "r"(one), "h"(static_cast<uint16_t>(3))
       : "memory");
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
@@ -239,11 +248,11 @@ constexpr int kEnd = 1, kClean = 2;
 constexpr int kRing = 8, kSegs = 4;
 
 template <int TYPE, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_tiles_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
   using C = Cfg<D>;
   constexpr bool BF = TYPE == RG_BF16;
-  constexpr int BLK = D / 32, GB = granule_bytes(TYPE, D);
+  constexpr int HALF = D / 64, GB = granule_bytes(TYPE, D);  // HALF: blocks of 32 dimensions in half a row
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[13 + 2 * kRing + 2 * kSegs];
   __shared__ TileInfo ring[kRing];
@@ -257,19 +266,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sK = base + 2 * C::Q, sV = sK + 2 * C::KV;
+  const int rank = static_cast<int>(cluster_ctarank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
+  auto lead = [&](int i) { return mapa_shared(bar(i), 0); };  // the even CTA's
   // barriers: two of each kind
   constexpr int FULL = 0, FREE = 2, SFULL = 4, PFULL = 6, ODONE = 8, QFULL = 10, DRAIN = 12, RFULL = 13,
                 RFREE = RFULL + kRing, GFULL = RFREE + kRing, GFREE = GFULL + kSegs;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(FULL + i), kDecWarps);
+      mbar_init(bar(FULL + i), 2 * kDecWarps);   // (used in the even CTA)
       mbar_init(bar(FREE + i), 1);
       mbar_init(bar(SFULL + i), 1);
-      mbar_init(bar(PFULL + i), 4);
+      mbar_init(bar(PFULL + i), 8);               // (in the even CTA)
       mbar_init(bar(ODONE + i), 1);
-      mbar_init(bar(QFULL + i), 4);
+      mbar_init(bar(QFULL + i), 8);               // (in the even CTA)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(RFULL + i), 1);
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(GFULL + i), 1);
-      mbar_init(bar(GFREE + i), kSoftWarps + 1);
+      mbar_init(bar(GFREE + i), kSoftWarps + (rank == 0));
     }
     mbar_init(bar(DRAIN), 1);
     abort_flag = 0;
@@ -286,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_launch_dependents();  // (the joining kernel waits for this one's end before it reads)
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
-    tmem_relinquish();
+    tmem_alloc2(smem_addr(&tmem_slot), kTmemCols);
+    tmem_relinquish2();
   }
 
   // This CTA's share of the line: every sequence's tiles are counted by a warp
@@ -318,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += sum;
   }
   const uint32_t tmem = tmem_slot;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = per * blockIdx.x, hi = min(total, lo + per);
+  const long long per = (total + pairs - 1) / pairs;
+  const long long lo = per * pair, hi = min(total, lo + per);
   // where it begins
   long long before = 0;
   bool found = lo >= hi;
@@ -376,7 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       before += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
-  __syncthreads();
+  // (also: the barriers and tensor memory of both CTAs are there)
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
 
   if (lo < hi) {
     if (warp < kSoftWarps) {
@@ -400,16 +414,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(GFREE + ord % kSegs));
       };
-      auto mine = [&](int ord) { return h == 0 || segment(ord).b.rows > 128; };
+      auto mine = [&](int ord) { return h == 0 || segment(ord).b.rows > 256; };
+      const int row = h * 256 + rank * 128 + r;  // of the item
       // a segment's queries into shared memory: the lanes of a group take a row's 16-byte words
       auto load_queries = [&](const Segment& sg) {
         constexpr int LR = D / 8, RI = 32 / LR;  // lanes a row, rows at a time
-        const int grow = sg.rb * BM + h * 128 + r;
+        const int grow = sg.rb * BM + row;
         const int64_t at = (sg.sq.start + grow / a.group) * a.q_t + (sg.head * a.group + grow % a.group) * a.q_h;
-        const int real = h * 128 + r < sg.b.rows;
+        const int real = row < sg.b.rows;
         auto put = [&](int from, uint4 v) {
-          const int row = (warp & 3) * 32 + from, word = lane % LR;
-          sts128(sQ + h * C::Q + (word >> 3) * C::CHUNK + row * 128 + (((word & 7) ^ (row & 7)) << 4), v.x ^ flip,
+          const int at_row = (warp & 3) * 32 + from, word = lane % LR;
+          sts128(sQ + h * C::Q + (word >> 3) * C::CHUNK + at_row * 128 + (((word & 7) ^ (at_row & 7)) << 4), v.x ^ flip,
                  v.y ^ flip, v.z ^ flip, v.w ^ flip);
         };
         if (a.atype == (BF ? RG_BF16 : RG_F16)) {
@@ -444,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(QFULL + h));
+        if (lane == 0) mbar_arrive_cluster(lead(QFULL + h));
       };
       bool loaded = false;
       for (int ord = 0; wait_segment(ord); ++ord) {
@@ -458,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!loaded) load_queries(sg);
         loaded = false;
         const bool holes = sg.holes;
-        const int row = h * 128 + r, grow = sg.rb * BM + row;
+        const int grow = sg.rb * BM + row;
         const bool real = row < sg.b.rows;
         const int pos = real ? sg.sq.len - sg.sq.n + grow / a.group : -1;
         float m_ref = kNone, l = 0.0f;
@@ -547,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(PFULL + h));
+          if (lane == 0) mbar_arrive_cluster(lead(PFULL + h));
         }
         if (!ok) break;
         // the next segment's queries (this one's have been read: its last scores are in)
@@ -561,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool starts = begin == 0, ends = end == sg.b.nt;
         const int64_t to = (sg.sq.start + grow / a.group) * a.o_t + (sg.head * a.group + grow % a.group) * a.o_h;
-        float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * part_floats(BM, D);
+        float* part = parts + (static_cast<int64_t>(pair) * 2 + (starts ? 1 : 0)) * part_floats(BM, D);
         const float inv = starts && ends ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         if (!(starts && ends) && real) {
           part[row] = m_ref;
@@ -617,36 +632,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         tc_fence_before();
-        if (tid == 0 && starts && !ends) {
+        if (tid == 0 && rank == 0 && starts && !ends) {
           headed = true;
-          desc[blockIdx.x] = Desc{static_cast<int>(sg.last / per), sg.b.rows, sg.sq.start + sg.rb * BM / a.group,
+          desc[pair] = Desc{static_cast<int>(sg.last / per), sg.b.rows, sg.sq.start + sg.rb * BM / a.group,
                                   sg.rb * BM % a.group, sg.head};
         }
         release(ord);
       }
-      if (tid == 0 && !headed) desc[blockIdx.x].last = -1;
+      if (tid == 0 && rank == 0 && !headed) desc[pair].last = -1;
     } else if (warp < kSoftWarps + kDecWarps) {
-      // ---------------- decoders: granule w of every tile ----------------
-      // In pairs: the values of tile j - 1 and the keys of tile j, the order in which the
-      // tensor core needs them; the next pair's words are loaded before the wait for its slots.
+      // ---------------- decoders ----------------
+      // Warp w of CTA `rank`: the keys of granule 4 rank + w / 2, half w % 2 of the dimensions;
+      // the values of granule w, half `rank` of the dimensions.  In pairs: the values of tile
+      // j - 1 and the keys of tile j, the order in which the tensor cores need them; the next
+      // pair's words are loaded before the wait for its slots.
       fewer_regs<kRegsDec>();
       const int w = warp - kSoftWarps, g = lane >> 2, t4 = lane & 3;
-      const int key0 = 16 * w + 4 * (g >> 1) + (g & 1);
+      const int kg = 4 * rank + (w >> 1), kb0 = (w & 1) * HALF, vb0 = rank * HALF;
+      const int key0 = 16 * (w >> 1) + 4 * (g >> 1) + (g & 1);
       const long long to_values = c.kv_heads * c.slab_bytes;
-      // (16-bit types have no registers for both: their keys are loaded when they are needed)
-      constexpr bool AHEAD = has_scales(TYPE) || D < 128;
-      KeyWords<TYPE> kw[BLK] = {};
-      ValueWords<TYPE> vw[BLK] = {};
-      auto load_keys = [&](const uint8_t* src) {
+      KeyWords<TYPE> kw[HALF] = {};
+      ValueWords<TYPE> vw[HALF] = {};
+      auto load_keys = [&](long long off) {
 #pragma unroll
-        for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(kw[k], src, k, lane);
+        for (int k = 0; k < HALF; ++k) load_words<TYPE, D>(kw[k], c.data + off, kb0 + k, lane);
       };
       const bool pages = c.pages > 0;
       bool any = __all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL), 0, ctl, &abort_flag)) && !(ring[0].flags & kEnd);
-      const uint8_t* src = c.data + ring[0].off[w];  // tile j's keys
-      if (AHEAD && any && pages) load_keys(src);
+      if (any && pages) load_keys(ring[0].off[kg]);
       bool clean = false;
       int ord = 0;
+      const uint32_t full[2] = {lead(FULL), lead(FULL + 1)};
       for (uint32_t j = 0; any || j > 0; ++j) {
         const TileInfo& x = ring[j % kRing];
         if (j >= 2 &&
@@ -656,13 +672,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (clean) {
             bool bad = false;
 #pragma unroll
-            for (int k = 0; k < BLK; ++k) bad |= clean_words(vw[k]);
-            if (bad) *reinterpret_cast<volatile int*>(&poison[ord & 3]) = ord;
+            for (int k = 0; k < HALF; ++k) bad |= clean_words(vw[k]);
+            if (bad) {  // both CTAs' rows need these dimensions
+#pragma unroll
+              for (int r2 = 0; r2 < 2; ++r2)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_addr(&poison[ord & 3]), r2)),
+                             "r"(ord)
+                             : "memory");
+              asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            }
           }
           const uint32_t to = sV + ((j - 1) & 1) * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
           const int chunk = (w & 3) * 2 + (t4 >> 1);
 #pragma unroll
-          for (int k = 0; k < BLK; ++k) {
+          for (int k = 0; k < HALF; ++k) {
             uint32_t vb[4][2];
             value_operand(vw[k], vb);
 #pragma unroll
@@ -673,20 +696,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (any) {
-          if (!AHEAD && pages) load_keys(src);
           const uint32_t to = sK + (j & 1) * C::KV;
-// Two blocks (the 128 bytes of a row's chunk) at a time: a quarter warp's stores
-          // are two rows' four words each; where the odd row stores its other block first,
-          // they fall on all eight 16-byte columns.
-#pragma unroll
-          for (int k = 0; k < BLK; k += 2) {
+          if constexpr (HALF == 2) {
+            // Two blocks (the 128 bytes of a row's chunk) at a time: a quarter warp's stores
+            // are two rows' four words each; where the odd row stores its other block first,
+            // they fall on all eight 16-byte columns.
             uint32_t kb[2][2][4];
-            key_operand(kw[k], kb[0]);
-            key_operand(kw[k + 1], kb[1]);
+            key_operand(kw[0], kb[0]);
+            key_operand(kw[HALF - 1], kb[1]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const int row = key0 + 2 * q;
-              const uint32_t at = to + (k >> 1) * C::CHUNK + row * 128;
+              const uint32_t at = to + (w & 1) * C::KCHUNK + row * 128;
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const int blk = u ^ (g & 1);
@@ -695,6 +716,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sts128(at + (((blk * 4 + t4) ^ (row & 7)) << 4), x0, x1, x2, x3);
               }
             }
+          } else {
+            uint32_t kb[2][4];
+            key_operand(kw[0], kb);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int row = key0 + 2 * q;
+              sts128(to + row * 128 + ((((w & 1) * 4 + t4) ^ (row & 7)) << 4), kb[q][0], kb[q][1], kb[q][2], kb[q][3]);
+            }
           }
           if (lane == 0 && w == 0)
             *reinterpret_cast<volatile uint8_t*>(&valid[j & 7]) = static_cast<uint8_t>(x.valid);
@@ -702,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(FULL + (j & 1)));
+          mbar_arrive_cluster(full[j & 1]);
           if (j > 0) mbar_arrive(bar(RFREE + (j - 1) % kRing));
         }
         if (!any) break;
@@ -710,14 +739,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         clean = x.flags & kClean;
         ord = x.ord;
         if (pages) {
+          const uint8_t* src = c.data + x.off[w] + to_values;
 #pragma unroll
-          for (int k = 0; k < BLK; ++k) load_words<TYPE, D>(vw[k], src + to_values, k, lane);
+          for (int k = 0; k < HALF; ++k) load_words<TYPE, D>(vw[k], src, vb0 + k, lane);
         }
         if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(RFULL + (j + 1) % kRing), ((j + 1) / kRing) & 1, ctl, &abort_flag)))
           break;
         any = !(ring[(j + 1) % kRing].flags & kEnd);
-        src = c.data + ring[(j + 1) % kRing].off[w];
-        if (AHEAD && any && pages) load_keys(src);
+        if (any && pages) load_keys(ring[(j + 1) % kRing].off[kg]);
       }
     } else {
       fewer_regs<kRegsMma>();
@@ -788,14 +817,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp && rank == 0) {
       // ---------------- the matrix instructions ----------------
       // (the whole warp waits, so that operands stay warp-uniform; one lane issues.  One
       // warp for both streams: their products alternate, so that one stream's softmax
       // runs while the other has the tensor core; a warp a stream fell into step and was
       // slower)
-      constexpr uint32_t idS = idesc_f16(BF, 128, BN, false, false);
-      constexpr uint32_t idO = idesc_f16(BF, 128, D, false, false);
+      constexpr uint32_t idS = idesc_f16(BF, 256, BN, false, false);
+      constexpr uint32_t idO = idesc_f16(BF, 256, D, false, false);
       const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024);
       const uint32_t one = elect_one();
       const uint32_t tm = uniform(tmem);
@@ -809,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q = dQ + h * (C::Q >> 4), k = dK + slot * (C::KV >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = ((i >> 2) * C::CHUNK + (i & 3) * 32) >> 4;
-          mma_ss(tm + h * 128, q + o, k + o, idS, i != 0, one);
+          mma_ss(tm + h * 128, q + (((i >> 2) * C::CHUNK + (i & 3) * 32) >> 4),
+                 k + (((i >> 2) * C::KCHUNK + (i & 3) * 32) >> 4), idS, i != 0, one);
         }
         commit_one(bar(SFULL + h), one);
       };
@@ -827,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (wait(GFULL + ord % kSegs, (ord / kSegs) & 1)) {
         const Segment& sg = segs[ord % kSegs];
         const int count = uniform(sg.end - sg.begin);
-        const bool two = uniform(sg.b.rows) > 128;
+        const bool two = uniform(sg.b.rows) > 256;
         if (uniform(sg.begin) < 0) break;
         if (first_pair && !wait(FULL, 0)) break;
         first_pair = false;
@@ -873,14 +902,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (tid == 0) {
-    desc[blockIdx.x].last = -1;
+  } else if (tid == 0 && rank == 0) {
+    desc[pair].last = -1;
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();  // nothing of the pair's is in flight: each result waited for its products
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc2(tmem, kTmemCols);
   }
 }
 
@@ -889,11 +919,31 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
   auto kern = attend_tiles_kernel<TYPE, D>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
+  // pairs of CTAs that can be on the device at once (an SM without a partner in its
+  // cluster takes none), asked once per kernel and device
+  static std::atomic<int> cached[64];
+  std::atomic<int>& slot = cached[dev.device];
+  int pairs = slot.load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(dev.num_sms / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs <= 0) pairs = dev.num_sms / 2;
+    pairs = std::min(pairs, dev.num_sms / 2);
+    slot.store(pairs, std::memory_order_relaxed);
+  }
   Desc* desc = static_cast<Desc*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + (sizeof(Desc) * dev.num_sms + 255) / 256 * 256);
-  kern<<<dev.num_sms, kThreads, Cfg<D>::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});
+  kern<<<2 * pairs, kThreads, Cfg<D>::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});
   if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
-  return launch_join(a, desc, parts, BM, D, dev.num_sms, stream);
+  return launch_join(a, desc, parts, BM, D, pairs, stream);
 }
 
 template <int TYPE>
@@ -907,7 +957,7 @@ bool tiles_have(int dim) { return dim <= 128; }
 
 size_t tiles_workspace(const Cache& c, const DevInfo& dev) {
   return (sizeof(Desc) * dev.num_sms + 255) / 256 * 256 +
-         (static_cast<size_t>(dev.num_sms) * 2 * part_floats(BM, c.dim) * 4 + 255) / 256 * 256;
+         (static_cast<size_t>(dev.num_sms / 2) * 2 * part_floats(BM, c.dim) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_tiles(int type, const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev,
