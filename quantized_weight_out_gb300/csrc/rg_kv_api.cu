@@ -78,7 +78,7 @@ struct Route {
 };
 Route route_of(const kv::Cache& c, const kv::Batch& b, int group, const DevInfo& dev) {
   Route r;
-  r.tiles = kv::tiles_have(c.dim) && static_cast<int64_t>(b.max_new) * group > kRowsLimit;
+  r.tiles = static_cast<int64_t>(b.max_new) * group > kRowsLimit;
   // (one sequence alone: whatever its length turns out to be, one kernel has it)
   r.rows_limit = !r.tiles ? 2147483647 : b.seqs == 1 ? 0 : kRowsLimit;
   kv::Batch few = b;

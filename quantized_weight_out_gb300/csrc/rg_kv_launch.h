@@ -30,7 +30,6 @@ size_t rows_workspace(const Cache& c, const Batch& b, int group, const DevInfo& 
 cudaError_t launch_rows(int type, const Cache& c, const Batch& b, const Attend& a, void* workspace,
                         const DevInfo& dev, cudaStream_t stream);
 // Tiles of rows on the 5th-generation tensor cores (rg_kv_tiles.cu): the others.
-bool tiles_have(int dim);
 size_t tiles_workspace(const Cache& c, const DevInfo& dev);
 cudaError_t launch_tiles(int type, const Cache& c, const Batch& b, const Attend& a, void* workspace,
                          const DevInfo& dev, cudaStream_t stream);

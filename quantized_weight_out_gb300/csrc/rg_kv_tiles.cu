@@ -35,7 +35,6 @@ namespace kv {
 namespace {
 
 constexpr int BN = 128;          // tokens of a key tile
-constexpr int BM = 512;          // rows of an item
 constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
@@ -51,9 +50,13 @@ constexpr int kScan = 256;       // sequences counted at a time
 
 template <int D>
 struct Cfg {
+  // streams of 256 rows: two of up to 128 dimensions; of 256 one, whose accumulators take half of
+  // tensor memory and which has two score tiles in the other half, used in turn
+  static constexpr int NS = D <= 128 ? 2 : 1;
+  static constexpr int BM = 256 * NS;        // rows of an item
   static constexpr int Q = 128 * D * 2;      // a CTA's queries of one stream
   static constexpr int KV = 64 * D * 2;      // its half of a tile's keys, or values
-  static constexpr int SMEM = 2 * Q + 4 * KV + 1024;
+  static constexpr int SMEM = NS * Q + 4 * KV + 1024;
   static constexpr int CHUNK = 128 * 128;    // queries: 128 rows x 64 dimensions
   static constexpr int KCHUNK = 64 * 128;    // keys: 64 tokens x 64 dimensions
   static constexpr int VCHUNK = D / 2 * 128; // values: D / 2 dimensions x 64 tokens
@@ -66,6 +69,7 @@ struct Block {
   int minpos, maxpos;  // positions of the block's first and last row
   int rows;
 };
+template <int BM>
 __device__ __forceinline__ Block block_of(const Seq& q, int group, int window, int rb) {
   Block b;
   const int first = q.len - q.n, r0 = rb * BM;
@@ -76,6 +80,7 @@ __device__ __forceinline__ Block block_of(const Seq& q, int group, int window, i
   b.nt = max(1, (max(0, min(q.len, b.maxpos + 1)) + BN - 1) / BN - b.t0);
   return b;
 }
+template <int BM>
 __device__ __forceinline__ int blocks_of(const Seq& q, int group, int max_rows) {
   return q.n * group > max_rows ? (q.n * group + BM - 1) / BM : 0;
 }
@@ -93,18 +98,19 @@ struct Walk {
   long long at, hi;
   int seq, head, rb, tile, nrb;
   Seq sq;
+  template <int BM>
   __device__ __forceinline__ bool next(const Cache& c, const Batch& b, const Attend& a, Segment& s) {
     if (at >= hi) return false;
     while (nrb == 0) {  // a new sequence
       if (++seq >= b.seqs) return false;
       sq = load_seq(b, c.page_tokens, seq, nullptr);
-      nrb = blocks_of(sq, a.group, a.rows_limit);
+      nrb = blocks_of<BM>(sq, a.group, a.rows_limit);
     }
     s.sq = sq;
     s.seq = seq;
     s.head = head;
     s.rb = rb;
-    s.b = block_of(sq, a.group, a.window, rb);
+    s.b = block_of<BM>(sq, a.group, a.window, rb);
     s.begin = tile;
     s.end = static_cast<int>(min(static_cast<long long>(s.b.nt), tile + (hi - at)));
     s.last = at + (s.b.nt - tile) - 1;
@@ -252,6 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_tiles_kernel(Cache c, Batch b, Attend a, Desc* desc, float* parts, WaitCtl ctl) {
   using C = Cfg<D>;
   constexpr bool BF = TYPE == RG_BF16;
+  constexpr int BM = C::BM, NS = C::NS;
   constexpr int HALF = D / 64, GB = granule_bytes(TYPE, D);  // HALF: blocks of 32 dimensions in half a row
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[13 + 2 * kRing + 2 * kSegs];
@@ -265,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ long long sh_tiles[kScan];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base, sK = base + 2 * C::Q, sV = sK + 2 * C::KV;
+  const uint32_t sQ = base, sK = base + NS * C::Q, sV = sK + 2 * C::KV;
   const int rank = static_cast<int>(cluster_ctarank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
   auto lead = [&](int i) { return mapa_shared(bar(i), 0); };  // the even CTA's
@@ -288,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(GFULL + i), 1);
-      mbar_init(bar(GFREE + i), kSoftWarps + (rank == 0));
+      mbar_init(bar(GFREE + i), 4 * NS + (rank == 0));
     }
     mbar_init(bar(DRAIN), 1);
     abort_flag = 0;
@@ -306,9 +313,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto count_tiles = [&](int s0, int* status) {
     for (int s = s0 + warp; s < min(b.seqs, s0 + kScan); s += kThreads / 32) {
       const Seq q = load_seq(b, c.page_tokens, s, status);
-      const int nrb = blocks_of(q, a.group, a.rows_limit);
+      const int nrb = blocks_of<BM>(q, a.group, a.rows_limit);
       int n = 0;
-      for (int rb = lane; rb < nrb; rb += 32) n += block_of(q, a.group, a.window, rb).nt;
+      for (int rb = lane; rb < nrb; rb += 32) n += block_of<BM>(q, a.group, a.window, rb).nt;
       long long all = n;
 #pragma unroll
       for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
@@ -361,11 +368,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           w.hi = hi;
           w.seq = s0 + s1 + l;
           w.sq = load_seq(b, c.page_tokens, w.seq, nullptr);
-          w.nrb = blocks_of(w.sq, a.group, a.rows_limit);
+          w.nrb = blocks_of<BM>(w.sq, a.group, a.rows_limit);
           w.head = static_cast<int>(rel / one);
           rel -= w.head * one;
           for (int rb0 = 0;; rb0 += 32) {  // the block, 32 at a time
-            const int nt = rb0 + lane < w.nrb ? block_of(w.sq, a.group, a.window, rb0 + lane).nt : 0;
+            const int nt = rb0 + lane < w.nrb ? block_of<BM>(w.sq, a.group, a.window, rb0 + lane).nt : 0;
             int sum = nt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -393,12 +400,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   if (lo < hi) {
-    if (warp < kSoftWarps) {
+    if (warp < 4 * NS) {
       // ---------------- softmax: a row a thread ----------------
       more_regs<kRegsSoft>();
       const int h = warp >> 2, r = (warp & 3) * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + lanes + h * 128, tO = tmem + lanes + kColO + h * 128;
+      const uint32_t tO = tmem + lanes + kColO + h * 128;
       // (a scale of zero stands for a tiny one: hidden scores are -inf, and -inf x 0 is NaN)
       const float cz = fmaxf(fabsf(a.scale_log2), 1e-37f);
       const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
@@ -479,7 +486,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float m_ref = kNone, l = 0.0f;
         for (int i = begin; i < end; ++i, ++tile_no, ++n_s) {
           const int t = t0 + i;
-          ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(SFULL + h), n_s & 1, ctl, &abort_flag));
+          // this tile's scores: the stream's, or every other tile's
+          const int turn = NS == 2 ? h : n_s & 1;
+          const uint32_t tS = tmem + lanes + turn * 128;
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(SFULL + turn), (NS == 2 ? n_s : n_s >> 1) & 1, ctl, &abort_flag));
           if (!ok) break;
           tc_fence_after();
           if (holes || t * BN + BN - 1 > minpos || (a.window && t * BN <= maxpos - a.window)) {
@@ -543,8 +553,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float v = fmaxf(top, m_ref), f = ex2(m_ref - v);
             m_ref = v;
             if (i > begin) {
-              // rescale what has been accumulated (the last product was issued before this
-              // tile's scores, whose commit covers it)
+              // rescale what has been accumulated (two streams: the last product was issued
+              // before this tile's scores, whose commit covers it)
+              if constexpr (NS == 1) {
+                ok = __all_sync(0xFFFFFFFFu,
+                                wait_bar(bar(ODONE + ((n_s - 1) & 1)), ((n_s - 1) >> 1) & 1, ctl, &abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+              }
               l *= f;
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
@@ -556,13 +572,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             }
           }
+          if (!ok) break;
           l += sum;
           tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(p));
           tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(PFULL + h));
+          if (lane == 0) mbar_arrive_cluster(lead(PFULL + turn));
         }
         if (!ok) break;
         // the next segment's queries (this one's have been read: its last scores are in)
@@ -571,7 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           loaded = true;
         }
         // the result, or this CTA's part of it
-        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(ODONE + h), n_seg++ & 1, ctl, &abort_flag));
+        ok = ok && __all_sync(0xFFFFFFFFu,
+                              NS == 2 ? wait_bar(bar(ODONE + h), n_seg++ & 1, ctl, &abort_flag)
+                                      : wait_bar(bar(ODONE + ((n_s - 1) & 1)), ((n_s - 1) >> 1) & 1, ctl, &abort_flag));
         if (!ok) break;
         tc_fence_after();
         const bool starts = begin == 0, ends = end == sg.b.nt;
@@ -640,13 +659,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         release(ord);
       }
       if (tid == 0 && rank == 0 && !headed) desc[pair].last = -1;
-    } else if (warp < kSoftWarps + kDecWarps) {
+    } else if (warp >= kSoftWarps && warp < kSoftWarps + kDecWarps) {
       // ---------------- decoders ----------------
       // Warp w of CTA `rank`: the keys of granule 4 rank + w / 2, half w % 2 of the dimensions;
       // the values of granule w, half `rank` of the dimensions.  In pairs: the values of tile
       // j - 1 and the keys of tile j, the order in which the tensor cores need them; the next
       // pair's words are loaded before the wait for its slots.
-      fewer_regs<kRegsDec>();
+      if constexpr (NS == 2) fewer_regs<kRegsDec>();  // (one stream: 96 stay, the second warpgroup gives its own)
       const int w = warp - kSoftWarps, g = lane >> 2, t4 = lane & 3;
       const int kg = 4 * rank + (w >> 1), kb0 = (w & 1) * HALF, vb0 = rank * HALF;
       const int key0 = 16 * (w >> 1) + 4 * (g >> 1) + (g & 1);
@@ -697,23 +716,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (any) {
           const uint32_t to = sK + (j & 1) * C::KV;
-          if constexpr (HALF == 2) {
+          if constexpr (HALF >= 2) {
             // Two blocks (the 128 bytes of a row's chunk) at a time: a quarter warp's stores
             // are two rows' four words each; where the odd row stores its other block first,
             // they fall on all eight 16-byte columns.
-            uint32_t kb[2][2][4];
-            key_operand(kw[0], kb[0]);
-            key_operand(kw[HALF - 1], kb[1]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int row = key0 + 2 * q;
-              const uint32_t at = to + (w & 1) * C::KCHUNK + row * 128;
+            for (int k = 0; k < HALF; k += 2) {
+              uint32_t kb[2][2][4];
+              key_operand(kw[k], kb[0]);
+              key_operand(kw[k + 1 < HALF ? k + 1 : k], kb[1]);
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int blk = u ^ (g & 1);
-                const uint32_t x0 = (g & 1) ? kb[u ^ 1][q][0] : kb[u][q][0], x1 = (g & 1) ? kb[u ^ 1][q][1] : kb[u][q][1];
-                const uint32_t x2 = (g & 1) ? kb[u ^ 1][q][2] : kb[u][q][2], x3 = (g & 1) ? kb[u ^ 1][q][3] : kb[u][q][3];
-                sts128(at + (((blk * 4 + t4) ^ (row & 7)) << 4), x0, x1, x2, x3);
+              for (int q = 0; q < 2; ++q) {
+                const int row = key0 + 2 * q;
+                const uint32_t at = to + ((w & 1) * (HALF / 2) + k / 2) * C::KCHUNK + row * 128;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const int blk = u ^ (g & 1);
+                  const bool odd = g & 1;
+                  sts128(at + (((blk * 4 + t4) ^ (row & 7)) << 4), odd ? kb[u ^ 1][q][0] : kb[u][q][0],
+                         odd ? kb[u ^ 1][q][1] : kb[u][q][1], odd ? kb[u ^ 1][q][2] : kb[u][q][2],
+                         odd ? kb[u ^ 1][q][3] : kb[u][q][3]);
+                }
               }
             }
           } else {
@@ -766,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(GFREE + ord % kSegs), ((ord / kSegs) & 1) ^ 1, ctl, &abort_flag));
         return ok;
       };
-      for (; ok && walk.next(c, b, a, sg); ++ord) {
+      for (; ok && walk.template next<BM>(c, b, a, sg); ++ord) {
         if (!segment_free()) break;
         const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
         const int end = min(sg.sq.len, sg.b.maxpos + 1);
@@ -834,20 +857,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity, ctl, &abort_flag));
         return ok;
       };
+      // (one stream: h is the score tile's turn)
       auto scores = [&](int h, uint32_t slot) {
-        const uint64_t q = dQ + h * (C::Q >> 4), k = dK + slot * (C::KV >> 4);
+        const uint64_t q = dQ + (NS == 2 ? h : 0) * (C::Q >> 4), k = dK + slot * (C::KV >> 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int i = 0; i < D / 16; ++i)
           mma_ss(tm + h * 128, q + (((i >> 2) * C::CHUNK + (i & 3) * 32) >> 4),
                  k + (((i >> 2) * C::KCHUNK + (i & 3) * 32) >> 4), idS, i != 0, one);
-        }
         commit_one(bar(SFULL + h), one);
       };
       auto product = [&](int h, uint32_t slot, bool first) {
         const uint64_t v = dV + slot * (C::KV >> 4);
 #pragma unroll
         for (int i = 0; i < BN / 16; ++i)
-          mma_ts(tm + kColO + h * 128, tm + h * 128 + 8 * i, v + (((i >> 2) * C::VCHUNK + (i & 3) * 32) >> 4), idO,
+          mma_ts(tm + kColO + (NS == 2 ? h : 0) * 128, tm + h * 128 + 8 * i, v + (((i >> 2) * C::VCHUNK + (i & 3) * 32) >> 4), idO,
                  i != 0 || !first, one);
       };
       // (FREE's event e: the scores of tile e and the products of tile e - 1 are done)
@@ -862,34 +885,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         first_pair = false;
         if (!wait(QFULL, q0++ & 1)) break;
         tc_fence_after();
-        scores(0, n & 1);
-        if (two) {
-          if (!wait(QFULL + 1, q1++ & 1)) break;
-          tc_fence_after();
-          scores(1, n & 1);
-        }
-        commit_one(bar(FREE + (n & 1)), one);
-        for (int i = 0; i < count; ++i, ++n) {
-          const uint32_t slot = n & 1, next = (n + 1) & 1;
-          const bool more = i + 1 < count;
-          if (!wait(FULL + next, ((n + 1) >> 1) & 1)) break;
-          if (!wait(PFULL, n & 1)) break;
-          tc_fence_after();
-          product(0, slot, i == 0);
-          if (more)
-            scores(0, next);
-          else
-            commit_one(bar(ODONE), one);
-          if (two) {
-            if (!wait(PFULL + 1, n1++ & 1)) break;
+        if constexpr (NS == 1) {
+          // scores a tile ahead of the products, so that a softmax runs beside them
+          scores(n & 1, n & 1);
+          commit_one(bar(FREE + (n & 1)), one);
+          for (int i = 0; i < count; ++i, ++n) {
+            const uint32_t slot = n & 1, next = (n + 1) & 1;
+            const bool more = i + 1 < count;
+            if (!wait(FULL + next, ((n + 1) >> 1) & 1)) break;
             tc_fence_after();
-            product(1, slot, i == 0);
-            if (more)
-              scores(1, next);
-            else
-              commit_one(bar(ODONE + 1), one);
+            if (more) scores(next, next);
+            if (!wait(PFULL + slot, (n >> 1) & 1)) break;
+            tc_fence_after();
+            product(slot, slot, i == 0);
+            // (a barrier for every other product: the softmax may be a product behind)
+            commit_one(bar(ODONE + slot), one);
+            if (more) commit_one(bar(FREE + next), one);
           }
-          if (more) commit_one(bar(FREE + next), one);
+        } else {
+          scores(0, n & 1);
+          if (two) {
+            if (!wait(QFULL + 1, q1++ & 1)) break;
+            tc_fence_after();
+            scores(1, n & 1);
+          }
+          commit_one(bar(FREE + (n & 1)), one);
+          for (int i = 0; i < count; ++i, ++n) {
+            const uint32_t slot = n & 1, next = (n + 1) & 1;
+            const bool more = i + 1 < count;
+            if (!wait(FULL + next, ((n + 1) >> 1) & 1)) break;
+            if (!wait(PFULL, n & 1)) break;
+            tc_fence_after();
+            product(0, slot, i == 0);
+            if (more)
+              scores(0, next);
+            else
+              commit_one(bar(ODONE), one);
+            if (two) {
+              if (!wait(PFULL + 1, n1++ & 1)) break;
+              tc_fence_after();
+              product(1, slot, i == 0);
+              if (more)
+                scores(1, next);
+              else
+                commit_one(bar(ODONE + 1), one);
+            }
+            if (more) commit_one(bar(FREE + next), one);
+          }
         }
         if (!ok) break;
         if (one) mbar_arrive(bar(GFREE + ord % kSegs));
@@ -943,21 +985,21 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + (sizeof(Desc) * dev.num_sms + 255) / 256 * 256);
   kern<<<2 * pairs, kThreads, Cfg<D>::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});
   if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
-  return launch_join(a, desc, parts, BM, D, pairs, stream);
+  return launch_join(a, desc, parts, Cfg<D>::BM, D, pairs, stream);
 }
 
 template <int TYPE>
 cudaError_t go_dim(const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev, cudaStream_t s) {
-  return c.dim == 64 ? go<TYPE, 64>(c, b, a, ws, dev, s) : go<TYPE, 128>(c, b, a, ws, dev, s);
+  return c.dim == 64    ? go<TYPE, 64>(c, b, a, ws, dev, s)
+         : c.dim == 128 ? go<TYPE, 128>(c, b, a, ws, dev, s)
+                        : go<TYPE, 256>(c, b, a, ws, dev, s);
 }
 
 }  // namespace
 
-bool tiles_have(int dim) { return dim <= 128; }
-
 size_t tiles_workspace(const Cache& c, const DevInfo& dev) {
   return (sizeof(Desc) * dev.num_sms + 255) / 256 * 256 +
-         (static_cast<size_t>(dev.num_sms / 2) * 2 * part_floats(BM, c.dim) * 4 + 255) / 256 * 256;
+         (static_cast<size_t>(dev.num_sms / 2) * 2 * part_floats(c.dim == 256 ? Cfg<256>::BM : Cfg<128>::BM, c.dim) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_tiles(int type, const Cache& c, const Batch& b, const Attend& a, void* ws, const DevInfo& dev,

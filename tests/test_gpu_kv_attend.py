@@ -134,18 +134,35 @@ def test_long_context_is_split_and_joined(rg, wtype, D):
     """One sequence's tiles shared by every CTA."""
     _case(rg, wtype, RG_BF16, D, 2, 4, 64, [(1, 20011)])
     _case(rg, wtype, RG_BF16, D, 1, 4, 64, [(6, 9001), (1, 130)])
+    _case(rg, wtype, RG_F32, D, 1, 4, 64, [(40, 9001), (1, 130)])
+
+
+def test_maxima_that_rise_along_the_keys(rg):
+    """Scores that grow by tens along the cache, so that the running reference moves
+    in every tile: the accumulators are rescaled again and again."""
+    for D, n in ((128, 1), (128, 90), (256, 90), (64, 90)):
+        L, G = 1200, 4
+        su = Setup(torch, rg, F16, D, 1, 64, [(n, L)], atype=RG_F32)
+        k, v = _contexts(su, 0.0)
+        q = np.repeat(su.rng.standard_normal((1, G, D)), n, 0).astype(np.float16).astype(np.float32)
+        k += (np.arange(L)[:, None, None] / L * 6).astype(np.float32) * q[0, :1]
+        su.fill(k, v)
+        got = _attend(rg, su, q, G, 0.4)
+        ref, bound = _reference(su, q, k, v, 0.4)
+        assert (np.abs(got - ref) <= bound).all(), (D, n)
 
 
 @pytest.mark.parametrize("n", [1, 40, 200])
-def test_rows_that_see_nothing(rg, n):
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_that_see_nothing(rg, n, D):
     """Lengths below the new tokens' number, of zero too: zeros for the rows before
     the cache's start, and no error."""
-    su, *_ = _case(rg, Q8, RG_F32, 64, 2, 2, 16, [(n, n // 2), (1, 0), (n, 0), (1, 33), (3, 2)])
+    su, *_ = _case(rg, Q8, RG_F32, D, 2, 2, 16, [(n, n // 2), (1, 0), (n, 0), (1, 33), (3, 2)])
     assert su.seqs
 
 
 @pytest.mark.parametrize("wtype", [F16, BF16, Q8, Q4])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n,G", [(4, 2), (20, 2), (150, 2)])
 @pytest.mark.parametrize("window", [0, 9])
 def test_hidden_values_do_not_reach_a_row(rg, wtype, D, n, G, window):
@@ -219,10 +236,11 @@ def test_strides(rg):
 
 
 @pytest.mark.parametrize("n", [1, 70])
-def test_bad_numbers_are_reported_not_followed(rg, n):
+@pytest.mark.parametrize("D", [64, 256])
+def test_bad_numbers_are_reported_not_followed(rg, n, D):
     """A page outside the pool hides its tokens, a bad length or row range empties
     its sequence; the others' results stand."""
-    D, H, G, P = 64, 2, 2, 16
+    H, G, P = 2, 2, 16
     seqs = [(n, n + 60), (n, n + 9), (n, n + 30)]
     su = Setup(torch, rg, Q8, D, H, P, seqs, atype=RG_F32)
     k, v = _contexts(su)
