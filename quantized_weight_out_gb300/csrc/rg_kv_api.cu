@@ -64,9 +64,11 @@ int check_rows(const void* p, int64_t st, int64_t sh, int heads, int dim, int at
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? RG_OK : RG_ERR_CUDA; }
 
-// Sequences of more rows than this run as tiles of 256 rows on the tensor
-// cores' accumulators in tensor memory; the others, which would leave most of a
-// tile empty, in the few-row kernel.
+// Sequences of more rows (new tokens x query heads of a kv head) than this run in
+// the tile kernel; the others, which would leave most of a tile empty, in the few-row
+// kernel.  One sequence over 15,000 tokens, 4 kv heads, us few-row / tile: 32 rows of 128
+// dimensions 39 / 44, 64 rows 39 / 45, 64 rows of 256 dimensions 45 / 62; 16 sequences of 8 to
+// 36 rows 81 / 195.  Beyond 64 rows the few-row kernel reads the cache a third time.
 constexpr int kRowsLimit = 64;
 
 // How a batch is run: the few-row kernel for its short sequences, the tile
