@@ -387,7 +387,7 @@ typedef struct rg_kv_cache {
 
 typedef struct rg_kv_batch {
   int32_t seqs;
-  int32_t max_pages;          /* columns of page_table                                  */
+  int32_t max_pages;          /* columns of page_table; times page_tokens at most 2^30  */
   int32_t max_new;            /* no sequence has more new tokens (sets the launch)      */
   int32_t reserved;           /* 0                                                      */
   int64_t tokens;             /* rows of the packed arrays                              */
@@ -427,7 +427,8 @@ int rg_kv_read(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, vo
  *
  * a token that sees no position gets zeros.  q, out: [tokens][heads]
  * [head_dim].  heads: a multiple of kv_heads, at most 1024 times it
- * (RG_ERR_SHAPE).  scale: finite (RG_ERR_ARG).
+ * (RG_ERR_SHAPE); max_new times their ratio at most 2^30, scale finite
+ * (RG_ERR_ARG).
  *
  * Scores, softmax statistics and sums are F32.  The matrix units take 16-bit
  * operands (fp16; bf16 for a BF16 cache): F32 queries, decoded Q8_0 and Q4_0

@@ -98,6 +98,8 @@ class RgError(RuntimeError):
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load librg.so (once) and declare its signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

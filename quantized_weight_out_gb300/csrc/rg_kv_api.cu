@@ -7,6 +7,8 @@ using namespace rg;
 namespace {
 
 constexpr int64_t kMaxDim = 2147483647;
+// Positions, and rows of a sequence, are 32-bit in the kernels, with room for a tile past the end.
+constexpr int64_t kMaxLen = int64_t{1} << 30;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -23,7 +25,7 @@ int check(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, kv::Cac
       cache->page_tokens > 4096)
     return RG_ERR_SHAPE;
   if (batch->seqs < 0 || batch->max_pages < 0 || batch->max_new < 0 || batch->tokens < 0 ||
-      batch->tokens > kMaxDim || static_cast<int64_t>(batch->max_pages) * cache->page_tokens > kMaxDim)
+      batch->tokens > kMaxDim || static_cast<int64_t>(batch->max_pages) * cache->page_tokens > kMaxLen)
     return RG_ERR_ARG;
   if (batch->seqs == 0 || batch->tokens == 0 || batch->max_new == 0) {
     *empty = true;
@@ -105,8 +107,7 @@ int attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const 
   if (!q || !out) return RG_ERR_ARG;
   if ((st = check_rows(q, q_t, q_h, heads, c.dim, atype)) != RG_OK) return st;
   if ((st = check_rows(out, o_t, o_h, heads, c.dim, atype)) != RG_OK) return st;
-  // a sequence's rows (new tokens x query heads of a kv head) are counted in 32 bits
-  if (static_cast<int64_t>(b.max_new) * (heads / c.kv_heads) > kMaxDim) return RG_ERR_ARG;
+  if (static_cast<int64_t>(b.max_new) * (heads / c.kv_heads) > kMaxLen) return RG_ERR_ARG;
   DevInfo* dev = nullptr;
   if (own_ws || ws) {
     if ((st = current_dev(&dev)) != RG_OK) return st;
@@ -123,7 +124,8 @@ int attend(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const 
   a.heads = heads;
   a.group = heads / c.kv_heads;
   a.atype = atype;
-  a.window = window;
+  // a window as long as a sequence can be hides nothing
+  a.window = window >= static_cast<int64_t>(b.max_pages) * c.page_tokens ? 0 : window;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const Route r = route_of(c, b, a.group, *dev);
   const size_t need = r.rows_bytes + r.tiles_bytes;

@@ -210,6 +210,20 @@ def test_large_scores_and_far_maxima(rg):
         assert (np.abs(got - ref) <= bound).all()
 
 
+@pytest.mark.parametrize("n", [1, 150])
+def test_a_window_of_any_length(rg, n):
+    """Windows past every length hide nothing, the largest int included."""
+    su = Setup(torch, rg, Q8, 64, 2, 16, [(n, n + 300), (n, n // 2)], atype=RG_F32)
+    k, v = _contexts(su)
+    su.fill(k, v)
+    q = su.rng.standard_normal((su.tokens, 4, 64)).astype(np.float32)
+    none = _attend(rg, su, q, 4, 0.125)
+    ref, bound = _reference(su, q, k, v, 0.125)
+    assert (np.abs(none - ref) <= bound).all()
+    for window in (n + 400, 1 << 20, 2 ** 31 - 1):
+        assert (np.abs(_attend(rg, su, q, 4, 0.125, window) - ref) <= bound).all()
+
+
 def test_negative_and_zero_scale(rg):
     _case(rg, Q8, RG_F32, 64, 2, 2, 16, [(1, 100), (30, 90)], scale=0.0)
     _case(rg, Q8, RG_F32, 64, 2, 2, 16, [(1, 100), (30, 90)], scale=-0.2)

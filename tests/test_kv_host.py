@@ -38,6 +38,7 @@ CACHES = [
 BATCHES = [
     (dict(seqs=-1), rg.RG_ERR_ARG), (dict(max_pages=-1), rg.RG_ERR_ARG), (dict(max_new=-1), rg.RG_ERR_ARG),
     (dict(tokens=-1), rg.RG_ERR_ARG), (dict(tokens=1 << 31), rg.RG_ERR_ARG), (dict(max_pages=1 << 30), rg.RG_ERR_ARG),
+    (dict(max_pages=(1 << 24) + 1), rg.RG_ERR_ARG),
     (dict(new_start=None), rg.RG_ERR_ARG), (dict(kv_len=None), rg.RG_ERR_ARG), (dict(page_table=None), rg.RG_ERR_ARG),
     (dict(kv_len=BAD + 2), rg.RG_ERR_ALIGN),
     (dict(seqs=0, new_start=None, kv_len=None, page_table=None), rg.RG_OK), (dict(tokens=0), rg.RG_OK),
