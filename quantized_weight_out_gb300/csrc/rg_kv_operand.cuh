@@ -218,26 +218,6 @@ __device__ __forceinline__ void key_operand(const KeyWords<TYPE>& k, uint32_t (&
   }
 }
 
-// Scales (or 16-bit values) that are not finite become zero; true if there was one.
-template <int TYPE>
-__device__ __forceinline__ bool clean_words(ValueWords<TYPE>& v) {
-  constexpr uint32_t INF = TYPE == RG_BF16 ? 0x7F80u : 0x7C00u;
-  bool bad = false;
-  auto clean = [&](uint32_t& x) {
-    const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
-    bad = bad || lo || hi;
-    x &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
-  };
-  if constexpr (has_scales(TYPE)) {
-    clean(v.s[0]);
-    clean(v.s[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) clean(v.w[i]);
-  }
-  return bad;
-}
-
 // Value operands of block c: b[q][i], n8 block q (dimensions 32c + 8q + g),
 // tokens 4t + 2i, 4t + 2i + 1.
 template <int TYPE>
@@ -266,20 +246,37 @@ __device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_
   }
 }
 
-// What clean_words took out, of token j and dimension d of a granule:
-// 0 where the value is finite.
+// Value operands that are not finite (a block's scale may be, or its product pass
+// fp16's range) become zero; true if there was one.
+template <int TYPE>
+__device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
+  constexpr uint32_t INF = TYPE == RG_BF16 ? 0x7F80u : 0x7C00u;
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = b[q][i];
+      const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
+      bad = bad || lo || hi;
+      b[q][i] = x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
+    }
+  return bad;
+}
+
 __device__ __forceinline__ uint32_t ld32(uint32_t a) { return lds32(a); }
 __device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
 __device__ __forceinline__ uint16_t ld16(uint32_t a) { return static_cast<uint16_t>(lds16(a)); }
 __device__ __forceinline__ uint16_t ld16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint16_t*>(p)); }
 
+// What clean_operand took out, of token j and dimension d of a granule:
+// 0 where the value is finite.
 template <int TYPE, int D, class P>
 __device__ __forceinline__ float value_not_finite(P base, int j, int d) {
   const int c = d >> 5, q = (d >> 3) & 3, g = d & 7, t = j >> 2, k = j & 3;
   float v;
   if constexpr (has_scales(TYPE)) {
     const float s = f16_to_f32(ld16(base + ((D / 32) * block16_bytes(TYPE) + 32 * c + 2 * j)));
-    if (s - s == 0.0f) return 0.0f;
     int code;
     if constexpr (TYPE == RG_Q8_0) {
       const uint32_t w = ld32(base + (c * 512 + (g * 4 + t) * 16 + q * 4));
@@ -289,6 +286,7 @@ __device__ __forceinline__ float value_not_finite(P base, int j, int d) {
       code = static_cast<int>((w >> (4 * ((k & 1) * 4 + (k >> 1) * 2 + (q & 1)))) & 15u) - 8;
     }
     v = s * static_cast<float>(code);
+    if (fabsf(v) >= 65520.0f) v = copysignf(INFINITY, v);  // as the fp16 operand
   } else {
     const uint16_t h = ld16(base + ((2 * c + (q >> 1)) * 512 + (g * 4 + t) * 16 + (q & 1) * 8 + k * 2));
     v = TYPE == RG_BF16 ? bf16_to_f32(h) : f16_to_f32(h);

@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
         for (int k = 0; k < BLK; ++k) {
           ValueWords<TYPE> vw;
           load_words<TYPE, D>(vw, vbase, k, lane);
-          if constexpr (MASKED) bad |= clean_words(vw);
           uint32_t vb[4][2];
           value_operand(vw, vb);
+          if constexpr (MASKED) bad |= clean_operand<TYPE>(vb);
 #pragma unroll
           for (int m = 0; m < NT; ++m)
 #pragma unroll

@@ -693,30 +693,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             !__all_sync(0xFFFFFFFFu, wait_bar(bar(FREE + (j & 1)), ((j - 2) >> 1) & 1, ctl, &abort_flag)))
           break;
         if (j > 0) {
-          if (clean) {
-            bool bad = false;
-#pragma unroll
-            for (int k = 0; k < HALF; ++k) bad |= clean_words(vw[k]);
-            if (bad) {  // both CTAs' rows need these dimensions
-#pragma unroll
-              for (int r2 = 0; r2 < 2; ++r2)
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_addr(&poison[ord & 3]), r2)),
-                             "r"(ord)
-                             : "memory");
-              asm volatile("fence.acq_rel.cluster;" ::: "memory");
-            }
-          }
+          bool bad = false;
           const uint32_t to = sV + ((j - 1) & 1) * C::KV + (w >> 2) * C::VCHUNK + (t4 & 1) * 8;
           const int chunk = (w & 3) * 2 + (t4 >> 1);
 #pragma unroll
           for (int k = 0; k < HALF; ++k) {
             uint32_t vb[4][2];
             value_operand(vw[k], vb);
+            if (clean) bad |= clean_operand<TYPE>(vb);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int row = 32 * k + 8 * q + g;
               sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
             }
+          }
+          if (bad) {  // both CTAs' rows need these dimensions
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2)
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_addr(&poison[ord & 3]), r2)),
+                           "r"(ord)
+                           : "memory");
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
         }
         if (any) {
