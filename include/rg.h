@@ -406,8 +406,9 @@ size_t rg_kv_page_bytes(int type, int head_dim, int kv_heads, int page_tokens);
  * Q4_0: with t the first value of the largest magnitude, d = fp16(t / -8),
  * q = nearest even of x * (-8 / t), plus 8, clamped to 0..15.  A d that
  * rounds to zero stores zeros; a block with a value that is not finite reads
- * back as NaN.  A finite value beyond fp16 (|x| > 65504; BF16 caches: none)
- * is reported as RG_ERR_RANGE.  One launch, no workspace. */
+ * back as NaN.  A finite value beyond fp16 (|x| > 65504; Q8_0, where d may
+ * round up: > 65500; BF16: what rounds to inf) is reported as RG_ERR_RANGE.
+ * One launch, no workspace. */
 int rg_kv_write(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, const void* k, int64_t k_t,
                 int64_t k_h, const void* v, int64_t v_t, int64_t v_h, void* stream);
 

@@ -61,7 +61,9 @@ __device__ __forceinline__ uint16_t quantise8(const float (&x)[2][8], int t, uin
   uint16_t d = __half_as_ushort(__float2half_rn(quotient));
   const uint32_t mag = t & 2 ? big[1] : big[0];
   if (mag >= 0x7F800000u) d = 0x7E00;  // a value that is not finite: the block reads back as NaN
-  else if (mag > 0x477FE000u) report_range(status);  // 65504: past the fp16 operands of the attention
+  // past the fp16 operands of the attention: 65504, and with d rounded up to 516 (from
+  // 515.75) 127 d is 65532
+  else if (__uint_as_float(mag) > (TYPE == RG_Q8_0 ? 65500.0f : 65504.0f)) report_range(status);
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const int lane = (threadIdx.x & 28) + 2 * n;
@@ -79,6 +81,9 @@ __device__ __forceinline__ uint16_t quantise8(const float (&x)[2][8], int t, uin
   }
   return d;
 }
+
+// finite, and more than fp16's largest value
+__device__ __forceinline__ bool beyond_f16(float x) { return fabsf(x) > 65504.0f && x - x == 0.0f; }
 
 // the low bytes of four words
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -370,7 +375,10 @@ __device__ __forceinline__ void store_block(const float (&x)[2][8], uint8_t* out
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         word[n][e] = pack16<BF>(x[n][2 * e], x[n][2 * e + 1]);
-        over |= overflowed16<BF>(x[n][2 * e], word[n][e]) || overflowed16<BF>(x[n][2 * e + 1], word[n][e] >> 16);
+        if constexpr (BF)
+          over |= overflowed16<BF>(x[n][2 * e], word[n][e]) || overflowed16<BF>(x[n][2 * e + 1], word[n][e] >> 16);
+        else
+          over |= beyond_f16(x[n][2 * e]) || beyond_f16(x[n][2 * e + 1]);
       }
     if (over) report_range(status);
     if (kind == 0) {

@@ -113,6 +113,25 @@ def test_special_values(rg, wtype):
     assert rg.rg_check(torch.cuda.current_stream()) == rg.RG_OK
 
 
+@pytest.mark.parametrize("wtype", [inputs.F16, inputs.BF16, inputs.Q8_0, inputs.Q4_0])
+def test_the_largest_values(rg, wtype):
+    """What is stored without a report is finite as an fp16 operand: in a Q8_0 block of
+    65504 d rounds up to 516, and 516 * 127 does not fit."""
+    for x, ok in ((65500.0, True), (65502.0, wtype != inputs.Q8_0), (65504.0, wtype != inputs.Q8_0),
+                  (-65504.0, wtype != inputs.Q8_0), (65508.0, wtype == inputs.BF16)):
+        su = Setup(torch, rg, wtype, 64, 1, 16, [(1, 1)], atype=RG_F32)
+        k = np.ones((1, 1, 64), np.float32)
+        k[0, 0, 40] = x
+        t = su.tensor(k)
+        rg.check(_write(su, t, t, rg))
+        st = rg.rg_check(torch.cuda.current_stream())
+        assert st == (rg.RG_OK if ok else rg.RG_ERR_RANGE), x
+        stored = oracle.kv_values(wtype, k)
+        if ok and wtype != inputs.BF16:
+            with np.errstate(over="ignore"):
+                assert np.isfinite(stored.astype(np.float16)).all()
+
+
 @pytest.mark.parametrize("wtype", [inputs.F16, inputs.Q4_0])
 def test_strides_and_one_side_only(rg, wtype):
     """Head-major arrays and parts of a fused row, keys or values alone; the
