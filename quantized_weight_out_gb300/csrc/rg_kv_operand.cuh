@@ -249,18 +249,19 @@ __device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_
 // Value operands that are not finite (a block's scale may be, or its product pass
 // fp16's range) become zero; true if there was one.
 template <int TYPE>
-__device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
+__device__ __forceinline__ bool clean_pair(uint32_t& x) {
   constexpr uint32_t INF = TYPE == RG_BF16 ? 0x7F80u : 0x7C00u;
+  const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
+  x &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+  return lo || hi;
+}
+template <int TYPE>
+__device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
   bool bad = false;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t x = b[q][i];
-      const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
-      bad = bad || lo || hi;
-      b[q][i] = x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
-    }
+    for (int i = 0; i < 2; ++i) bad |= clean_pair<TYPE>(b[q][i]);
   return bad;
 }
 

@@ -700,11 +700,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < HALF; ++k) {
             uint32_t vb[4][2];
             value_operand(vw[k], vb);
-            if (clean) bad |= clean_operand<TYPE>(vb);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int row = 32 * k + 8 * q + g;
               sts64(to + row * 128 + ((chunk ^ (row & 7)) << 4), vb[q][0], vb[q][1]);
+            }
+          }
+          if (clean) {  // again over what this lane has stored: rare, and no register above
+#pragma unroll 1
+            for (int n = 0; n < 4 * HALF; ++n) {
+              const int row = 8 * n + g;
+              const uint32_t at = to + row * 128 + ((chunk ^ (row & 7)) << 4);
+              uint2 u = lds64(at);
+              if (clean_pair<TYPE>(u.x) | clean_pair<TYPE>(u.y)) {
+                sts64(at, u.x, u.y);
+                bad = true;
+              }
             }
           }
           if (bad) {  // both CTAs' rows need these dimensions
