@@ -27,8 +27,8 @@
 // prompt over a long cache uses every SM.  An item cut by a border leaves F32
 // parts that a second kernel joins in a fixed order.
 // Measured: 1021 tokens of 32 heads over a Q8_0 context of 15,000 (8 kv heads of 128)
-// 231 us, 1.12 PFLOP/s, 0.60 of the measured burst bf16 rate; four packed prompts of
-// 700 to 4,099 tokens, bf16 cache, 447 us, 0.85 PFLOP/s (one item's rows are written
+// 232 us, 1.11 PFLOP/s, 0.59 of the measured burst bf16 rate; four packed prompts of
+// 700 to 4,099 tokens, bf16 cache, 453 us, 0.84 PFLOP/s (one item's rows are written
 // and the next one's first tile started in about 11,000 cycles of 3,300 a tile); 16
 // heads of 256, the same prompts, 559 us.  The tensor pipe is active 55 % of the time:
 // a stream's chain (scores complete, softmax 1,200 cycles, probabilities stored 250,
