@@ -247,13 +247,14 @@ __device__ __forceinline__ void value_operand(const ValueWords<TYPE>& v, uint32_
 }
 
 // Value operands that are not finite (a block's scale may be, or its product pass
-// fp16's range) become zero; true if there was one.
+// fp16's range) become zero; returns their bits set.
 template <int TYPE>
-__device__ __forceinline__ bool clean_pair(uint32_t& x) {
+__device__ __forceinline__ uint32_t clean_pair(uint32_t& x) {
   constexpr uint32_t INF = TYPE == RG_BF16 ? 0x7F80u : 0x7C00u;
   const bool lo = (x & INF) == INF, hi = (x & (INF << 16)) == (INF << 16);
-  x &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
-  return lo || hi;
+  const uint32_t out = (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+  x &= ~out;
+  return out;
 }
 template <int TYPE>
 __device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
@@ -261,7 +262,7 @@ __device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) bad |= clean_pair<TYPE>(b[q][i]);
+    for (int i = 0; i < 2; ++i) bad |= clean_pair<TYPE>(b[q][i]) != 0;
   return bad;
 }
 

@@ -254,6 +254,7 @@ struct TileInfo {
   int flags;          // kEnd: no more tiles; kClean: values are checked, some row may not see them all
   int ord;            // segment
   int valid;          // bit g: granule g's tokens are there, or hidden by position
+  uint16_t seen[8];   // bit j: token j of the granule is there, and some row of the item may see it
 };
 constexpr int kEnd = 1, kClean = 2;
 constexpr int kRing = 8, kSegs = 4;
@@ -707,14 +708,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (clean) {  // again over what this lane has stored: rare, and no register above
+            // Operands that are not finite become zero.  They are reported where a row of the
+            // item may see them; elsewhere (past the newest token, before every window, a
+            // page that is not there) they are bytes of anything, which nobody misses.
+            const uint32_t seen = ring[(j - 1) % kRing].seen[w] >> (4 * t4);  // of this lane's four tokens
+            const uint32_t seen_x = (seen & 1 ? 0xFFFFu : 0u) | (seen & 2 ? 0xFFFF0000u : 0u);
+            const uint32_t seen_y = (seen & 4 ? 0xFFFFu : 0u) | (seen & 8 ? 0xFFFF0000u : 0u);
 #pragma unroll 1
             for (int n = 0; n < 4 * HALF; ++n) {
               const int row = 8 * n + g;
               const uint32_t at = to + row * 128 + ((chunk ^ (row & 7)) << 4);
               uint2 u = lds64(at);
-              if (clean_pair<TYPE>(u.x) | clean_pair<TYPE>(u.y)) {
+              const uint32_t out_x = clean_pair<TYPE>(u.x), out_y = clean_pair<TYPE>(u.y);
+              if (out_x | out_y) {
                 sts64(at, u.x, u.y);
-                bad = true;
+                bad |= ((out_x & seen_x) | (out_y & seen_y)) != 0;
               }
             }
           }
@@ -828,9 +836,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // its keys do not matter, and its values only have to be finite (cleaned).
           const long long off = granule_offset(c, paged ? page : 0, 0, sg.head, pos, GB);
           const uint32_t valid_bits = __ballot_sync(0xFFFFFFFFu, paged || !there) & 0xFFu;
+          // tokens from_j .. to_j - 1 of the granule lie where some row may see them
+          const int to_j = max(0, min(kGranule, end - pos));
+          const int from_j = a.window ? max(0, min(kGranule, sg.b.minpos - a.window + 1 - pos)) : 0;
+          const uint32_t seen = paged ? ((1u << to_j) - 1) & ~((1u << from_j) - 1) : 0u;
           if (!slot_free()) break;
           TileInfo& x = ring[n % kRing];
-          if (lane < 8) x.off[lane] = off;
+          if (lane < 8) {
+            x.off[lane] = off;
+            x.seen[lane] = static_cast<uint16_t>(seen);
+          }
           if (lane == 0) {
             x.ord = ord;
             x.valid = static_cast<int>(valid_bits);

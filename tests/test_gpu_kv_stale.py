@@ -1,0 +1,74 @@
+"""What a cache's memory holds where nothing has been stored, or where no row may look,
+changes neither a result of rg_kv_attend nor, by much, its time."""
+import numpy as np
+import pytest
+
+from quantized_weight_out_gb300 import inputs
+
+from kv_common import RG_BF16, Setup
+from test_gpu_kv_attend import rg  # noqa: F401  (the fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+F16, BF16, Q8, Q4 = inputs.F16, inputs.BF16, inputs.Q8_0, inputs.Q4_0
+
+
+class Call:
+    """A batch over a cache whose memory was `fill` before the contexts were stored."""
+
+    def __init__(self, rg, wtype, D, H, G, P, seqs, fill, window=0, spoil=None):  # noqa: F811
+        self.rg, self.G, self.window = rg, G, window
+        self.su = su = Setup(torch, rg, wtype, D, H, P, seqs, seed=2, atype=RG_BF16)
+        su.pool_d.fill_(fill)
+        g = torch.Generator(device="cuda").manual_seed(7)
+        k, v = (torch.randn(int(su.len.sum()), H, D, generator=g, device=su.dev) for _ in range(2))
+        if spoil:
+            spoil(su, k, v)
+        rg.check(rg.rg_kv_write(su.cache, su.whole()[0], inputs.F32, k, H * D, D, v, H * D, D,
+                                torch.cuda.current_stream()), "rg_kv_write")
+        self.q = torch.randn(su.tokens, H * G, D, generator=g, device=su.dev).bfloat16()
+        self.out = torch.empty_like(self.q)
+        need = rg.rg_kv_attend_workspace_bytes(su.cache, su.batch, H * G)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=su.dev)
+
+    def go(self):
+        su, rg, row = self.su, self.rg, self.su.H * self.G * self.su.D
+        rg.check(rg.rg_kv_attend_ws(su.cache, su.batch, RG_BF16, self.q, row, su.D, su.H * self.G, self.out, row, su.D,
+                                    su.D ** -0.5, self.window, self.ws, self.ws.numel(), torch.cuda.current_stream()),
+                 "rg_kv_attend")
+
+    def result(self):
+        self.go()
+        torch.cuda.synchronize()
+        return self.out.view(torch.int16).cpu().numpy()
+
+    def time(self, replays=20):
+        """us of a call inside a replayed graph, the least of several."""
+        self.go()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.go()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        best = float("inf")
+        for _ in range(replays):
+            torch.cuda.synchronize()
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b) * 1e3)
+        return best
+
+
+# Bytes 0xFF are a NaN as a scale and as a 16-bit value.  Twice the time allows for noise;
+# where such bytes were taken for values that rows miss, the calls took 180 times as long and more.
+@pytest.mark.parametrize("wtype", [F16, BF16, Q8, Q4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seqs,window", [([(1001, 1001)], 0), ([(301, 5005)], 0), ([(301, 5005)], 700)])
+def test_prompts_over_stale_memory(rg, wtype, D, seqs, window):  # noqa: F811
+    zero, stale = (Call(rg, wtype, D, 2, 4, 64, seqs, fill, window) for fill in (0, 255))
+    assert np.array_equal(zero.result(), stale.result())
+    t0, t1 = zero.time(), stale.time()
+    assert t1 <= 2 * t0, (t0, t1)
