@@ -838,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t valid_bits = __ballot_sync(0xFFFFFFFFu, paged || !there) & 0xFFu;
           // tokens from_j .. to_j - 1 of the granule lie where some row may see them
           const int to_j = max(0, min(kGranule, end - pos));
-          const int from_j = a.window ? max(0, min(kGranule, sg.b.minpos - a.window + 1 - pos)) : 0;
+          const int from_j = a.window ? max(0, min(kGranule, max(0, sg.b.minpos - a.window + 1) - pos)) : 0;
           const uint32_t seen = paged ? ((1u << to_j) - 1) & ~((1u << from_j) - 1) : 0u;
           if (!slot_free()) break;
           TileInfo& x = ring[n % kRing];
