@@ -256,14 +256,16 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t& x) {
   x &= ~out;
   return out;
 }
+// (seen[i]: the halves of tokens 4t + 2i, 4t + 2i + 1 that some row may see) True if one
+// of those was taken out.
 template <int TYPE>
-__device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2]) {
-  bool bad = false;
+__device__ __forceinline__ bool clean_operand(uint32_t (&b)[4][2], const uint32_t (&seen)[2]) {
+  uint32_t out[2] = {0, 0};
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) bad |= clean_pair<TYPE>(b[q][i]) != 0;
-  return bad;
+    for (int i = 0; i < 2; ++i) out[i] |= clean_pair<TYPE>(b[q][i]);
+  return ((out[0] & seen[0]) | (out[1] & seen[1])) != 0;
 }
 
 __device__ __forceinline__ uint32_t ld32(uint32_t a) { return lds32(a); }

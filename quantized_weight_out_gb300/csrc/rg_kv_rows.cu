@@ -339,13 +339,21 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
       for (int u = 0; u < N; ++u) {
         const uint32_t vbase = kb[u] + C::GB;
         bool bad = false;
+        uint32_t seen[2] = {0, 0};  // the lane's tokens that some row may see (others hold anything)
+        if constexpr (MASKED) {
+          const int j = (gran + kWarps * u) * kGranule + 4 * t;
+          const int from = a.window ? minpos - a.window + 1 : 0, to = (have >> u) & 1 ? maxpos : -1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j + i >= from && j + i <= to) seen[i >> 1] |= i & 1 ? 0xFFFF0000u : 0xFFFFu;
+        }
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
           ValueWords<TYPE> vw;
           load_words<TYPE, D>(vw, vbase, k, lane);
           uint32_t vb[4][2];
           value_operand(vw, vb);
-          if constexpr (MASKED) bad |= clean_operand<TYPE>(vb);
+          if constexpr (MASKED) bad |= clean_operand<TYPE>(vb, seen);
 #pragma unroll
           for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
         if constexpr (MASKED) {
           // values that are not finite were left out of the product (0 x inf would
           // reach rows that may not see them): add them to the rows that do
-          if (((have >> u) & 1) && __any_sync(0xFFFFFFFFu, bad)) {
+          if (__any_sync(0xFFFFFFFFu, bad)) {
             for (int jj = 0; jj < kGranule; ++jj) {
               const int j = (gran + kWarps * u) * kGranule + jj;
 #pragma unroll

@@ -72,3 +72,13 @@ def test_prompts_over_stale_memory(rg, wtype, D, seqs, window):  # noqa: F811
     assert np.array_equal(zero.result(), stale.result())
     t0, t1 = zero.time(), stale.time()
     assert t1 <= 2 * t0, (t0, t1)
+
+
+# (A decode's last granule alone is looked at: 2.5 times the time where its stale bytes counted.)
+@pytest.mark.parametrize("wtype", [F16, BF16, Q8, Q4])
+@pytest.mark.parametrize("seqs,window", [([(1, 1001)], 0), ([(1, 1001)], 500), ([(1, 1001), (3, 70), (1, 5)], 0)])
+def test_decoding_over_stale_memory(rg, wtype, seqs, window):  # noqa: F811
+    zero, stale = (Call(rg, wtype, 256, 4, 4, 64, seqs, fill, window) for fill in (0, 255))
+    assert np.array_equal(zero.result(), stale.result())
+    t0, t1 = zero.time(60), stale.time(60)
+    assert t1 <= 1.5 * t0, (t0, t1)
