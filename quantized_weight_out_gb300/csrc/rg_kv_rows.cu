@@ -571,12 +571,15 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float* p = part(min(i0 + k * groups, n - 1));
-          m[k] = p[row];
+          // (past the last part: nothing, by way of its loads; 0 x an infinity would be NaN)
+          const bool there = i0 + k * groups < n;
+          m[k] = there ? p[row] : -INFINITY;
           x[k] = *reinterpret_cast<const float4*>(p + 2 * bm + row * dim + d);
+          if (!there) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float f = i0 + k * groups < n ? ex2(m[k] - top) : 0.0f;
+          const float f = ex2(m[k] - top);
           v[0] += f * x[k].x; v[1] += f * x[k].y; v[2] += f * x[k].z; v[3] += f * x[k].w;
         }
       }
