@@ -608,25 +608,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           part[BM + row] = l;
         }
         if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord & 3]) == ord)) {
-          // values that are not finite, to the rows that see them (a column at a time: rare)
+          // Values that are not finite were left out of the products of tiles that some row sees
+          // in part.  What this row sees of them in dimensions 32 k .. + 31: an infinity of either
+          // sign a bit (both: NaN).  The warp looks at a token's 32 dimensions together.
           const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
+          const int from = a.window ? max(0, minpos - a.window + 1) : 0;  // the first position that any row sees
 #pragma unroll 1
-          for (int d = 0; d < D; ++d) {
-            float add = 0.0f;
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t plus = 0, minus = 0;
 #pragma unroll 1
-            for (int j = (t0 + begin) * BN; j < (t0 + end) * BN && j <= pos; ++j) {
-              if ((a.window && j <= pos - a.window) || !(holes || tile_masked(sg.b, a.window, j / BN))) continue;
-              const int page = table[j / c.page_tokens];
+            for (int j0 = (t0 + begin) * BN; j0 < (t0 + end) * BN && j0 <= maxpos; j0 += kGranule) {
+              if (j0 + kGranule <= from || !(holes || tile_masked(sg.b, a.window, j0 / BN))) continue;
+              const int page = table[j0 / c.page_tokens];
               if (page < 0 || page >= c.pages) continue;
-              add += value_not_finite<TYPE, D>(c.data + granule_offset(c, page, 1, sg.head, j, GB), j % kGranule, d);
+              const uint8_t* src = c.data + granule_offset(c, page, 1, sg.head, j0, GB);
+              // (mostly there is none in the granule's block)
+              ValueWords<TYPE> vw;
+              load_words<TYPE, D>(vw, src, k, lane);
+              uint32_t vb[4][2];
+              value_operand(vw, vb);
+              const uint32_t all[2] = {~0u, ~0u};
+              if (!__any_sync(0xFFFFFFFFu, clean_operand<TYPE>(vb, all))) continue;
+#pragma unroll 1
+              for (int j = 0; j < kGranule; ++j) {
+                const float v = value_not_finite<TYPE, D>(src, j, 32 * k + lane);
+                const uint32_t up = __ballot_sync(0xFFFFFFFFu, !(v <= 0.0f)), down = __ballot_sync(0xFFFFFFFFu, !(v >= 0.0f));
+                if (j0 + j <= pos && !(a.window && j0 + j <= pos - a.window)) {
+                  plus |= up;
+                  minus |= down;
+                }
+              }
             }
-            __syncwarp();
-            uint32_t o;
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-                         : "=r"(o) : "r"(tO + d) : "memory");
-            o = __float_as_uint(__uint_as_float(o) + add);
-            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tO + d), "r"(o) : "memory");
-            tmem_wait_st();
+            if (__any_sync(0xFFFFFFFFu, plus | minus)) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO + 32 * k, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (plus >> e & 1) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
+                if (minus >> e & 1) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
+              }
+              tmem_st32(tO + 32 * k, o);
+              tmem_wait_st();
+            }
           }
         }
 #pragma unroll 1

@@ -82,3 +82,35 @@ def test_decoding_over_stale_memory(rg, wtype, seqs, window):  # noqa: F811
     assert np.array_equal(zero.result(), stale.result())
     t0, t1 = zero.time(60), stale.time(60)
     assert t1 <= 1.5 * t0, (t0, t1)
+
+
+# A value of +inf (a NaN block in Q8_0) at one of the newest tokens: the rows behind it see it,
+# those before it must not.  The call looks for it among the tiles at the diagonal, and where a
+# page is missing among all of an item's; neither may take so long that another wait of the kernel
+# runs out.  Looked for row by row and value by value it took 180 to 900 times as long.
+@pytest.mark.parametrize("wtype", [BF16, Q8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("hole", [False, True])
+def test_a_visible_infinity_costs_little(rg, wtype, D, hole):  # noqa: F811
+    n, L, at = 301, 9011, 8900
+
+    def spoil(su, k, v):
+        v[at, 1, 3] = float("inf")
+
+    clean, call = (Call(rg, wtype, D, 2, 4, 64, [(n, L)], 0, spoil=how) for how in (None, spoil))
+    if hole:
+        for c in (clean, call):
+            c.su.table_d[0, 5] = 1 << 20
+    clean.go()
+    call.go()
+    s = torch.cuda.current_stream()
+    assert rg.rg_check(s) == (rg.RG_ERR_INDEX if hole else rg.RG_OK)
+    want, got = clean.out.float(), call.out.float()
+    see = torch.arange(L - n, L, device="cuda") >= at
+    spoilt = torch.zeros_like(want, dtype=torch.bool)
+    spoilt[see, 4:, 0 if wtype == Q8 else 3:32 if wtype == Q8 else 4] = True
+    assert (torch.isnan(got[spoilt]) if wtype == Q8 else got[spoilt] == float("inf")).all()
+    assert torch.equal(got[~spoilt], want[~spoilt])
+    t0, t1 = clean.time(), call.time()
+    rg.rg_check(s)
+    assert t1 <= 5 * t0, (t0, t1)
