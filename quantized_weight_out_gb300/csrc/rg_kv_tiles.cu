@@ -258,6 +258,11 @@ struct TileInfo {
 };
 constexpr int kEnd = 1, kClean = 2;
 constexpr int kRing = 8, kSegs = 4;
+// Flags of values left out, by segment.  Both CTAs' decoders write both CTAs' flags, and a CTA
+// is held back by its own segments' release only, so it may be kSegs segments ahead of the
+// other, which may itself have kSegs that are not released: a flag read late is not yet written
+// for a later segment with twice as many.
+constexpr int kFlags = 2 * kSegs;
 
 template <int TYPE, int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -271,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ TileInfo ring[kRing];
   __shared__ Segment segs[kSegs];                       // begin -1: no more
   __shared__ uint8_t valid[8];                          // by tile ordinal: TileInfo's valid
-  __shared__ int poison[4];                             // by segment ordinal: values left out of the product
+  __shared__ int poison[kFlags];                        // by segment ordinal: values left out of the product
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ Walk sh_walk;
@@ -305,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(DRAIN), 1);
     abort_flag = 0;
-    for (int i = 0; i < 4; ++i) poison[i] = -1;
+    for (int i = 0; i < kFlags; ++i) poison[i] = -1;
     fence_mbar_init();
   }
   pdl_launch_dependents();  // (the joining kernel waits for this one's end before it reads)
@@ -607,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           part[row] = m_ref;
           part[BM + row] = l;
         }
-        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord & 3]) == ord)) {
+        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord % kFlags]) == ord)) {
           // Values that are not finite were left out of the products of tiles that some row sees
           // in part.  What this row sees of them in dimensions 32 k .. + 31: an infinity of either
           // sign a bit (both: NaN).  The warp looks at a token's 32 dimensions together.
@@ -752,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (bad) {  // both CTAs' rows need these dimensions
 #pragma unroll
             for (int r2 = 0; r2 < 2; ++r2)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_addr(&poison[ord & 3]), r2)),
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_addr(&poison[ord % kFlags]), r2)),
                            "r"(ord)
                            : "memory");
             asm volatile("fence.acq_rel.cluster;" ::: "memory");

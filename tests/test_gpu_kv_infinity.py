@@ -32,3 +32,25 @@ def test_an_infinity_stays_one(rg, wtype, n, sign, back):  # noqa: F811
     rest = np.arange(D) != 9
     assert (np.abs(got - ref) <= bound)[..., rest].all()
     assert (got[..., 9] == sign * np.inf).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinities_in_many_short_items(rg, D):  # noqa: F811
+    """Items of more than 256 rows among shorter ones, several a CTA pair, each with an infinity
+    that only its last rows see: every item's own, time after time."""
+    G, H = 4, 2
+    lens = [(128, 128) if s % 4 == 0 else (17 + s % 40, 17 + s % 40) for s in range(240)]
+    su = Setup(torch, rg, inputs.BF16, D, H, 16, lens, seed=6, atype=RG_F32)
+    k, v = _contexts(su, 0.0)
+    at = np.cumsum([n for n, _ in lens]) - 2  # each sequence's last token but one
+    v[at, np.arange(len(lens)) % H, np.arange(len(lens)) % D] = np.inf
+    su.fill(k, v)
+    q = su.rng.standard_normal((su.tokens, H * G, D)).astype(np.float32)
+    want = np.zeros((su.tokens, H, D), bool)
+    for s, t in enumerate(at):
+        want[t:t + 2, s % H, s % D] = True
+    want = np.repeat(want, G, 1)
+    first = _attend(rg, su, q, H * G, D ** -0.5)
+    assert (first[want] == np.inf).all() and np.isfinite(first[~want]).all()
+    for _ in range(20):
+        assert np.array_equal(first, _attend(rg, su, q, H * G, D ** -0.5))
