@@ -9,7 +9,8 @@
 namespace rg {
 namespace kv {
 
-constexpr float kNone = -3.0e38f;    // the reference before any visible score
+constexpr float kNone = -3.40282347e38f;  // the reference before any score above -inf
+constexpr float kMinusInf = -3.4e38f;     // ... of a part whose row has seen scores of -inf only
 constexpr float kHead = 7.0f;        // probabilities are scaled by 2^7
 constexpr float kSlack = 8.0f;       // scores may pass the reference by this
 
@@ -24,6 +25,24 @@ struct Desc {
   int lead;    // ... and the row's index in the kv head's group
   int head;    // kv head
 };
+
+// What a row's sum of products is multiplied by: 1 / l, 0 where it has seen nothing, NaN
+// (the definition's 0 / 0) where all that it has seen scored -inf.
+__device__ __forceinline__ float row_factor(float m_ref, float l) {
+  return l != 0.0f ? 1.0f / l : m_ref > kNone ? NAN : 0.0f;
+}
+// Whether the row at `pos` sees one of the positions lo .. hi - 1: asked for rows whose
+// reference has not moved, of which there are few.
+__device__ __forceinline__ bool sees_any(const Cache& c, const int* table, int window, int pos, int lo, int hi) {
+  if (window) lo = max(lo, pos - window + 1);
+  hi = min(hi, pos + 1);
+  while (lo < hi) {
+    const int p = lo / c.page_tokens, page = table[p];
+    if (page >= 0 && page < c.pages) return true;
+    lo = (p + 1) * c.page_tokens;
+  }
+  return false;
+}
 
 __device__ __forceinline__ void store_out(const Attend& a, int token, int head, int d, const float (&v)[4]) {
   const int64_t at = token * a.o_t + head * a.o_h + d;

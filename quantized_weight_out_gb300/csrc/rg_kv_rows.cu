@@ -480,8 +480,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<TYPE, D, NT>::MINB)
         l += f * sm_l[w][row];
         v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
       }
+      if (top == kNone && sees_any(c, table, a.window, first + (row0 + row) / G, (sh.t0 + tile) * kTile,
+                                   (sh.t0 + tend) * kTile))
+        top = kMinusInf;
       if (starts && ends) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = row_factor(top, l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= inv;
         store_out(a, sq.start + (row0 + row) / G, head * G + (row0 + row) % G, d, v);
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kJoin) attend_join_kernel(Attend a, const Desc
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     if (lane == 0) {
       sm_top[r] = top;
-      sm_inv[r] = l == 0.0f ? 0.0f : 1.0f / l;
+      sm_inv[r] = row_factor(top, l);
     }
   }
   __syncthreads();

@@ -605,9 +605,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const bool starts = begin == 0, ends = end == sg.b.nt;
+        if (m_ref == kNone && sees_any(c, b.table + static_cast<int64_t>(sg.seq) * b.max_pages, a.window, pos,
+                                       (t0 + begin) * BN, (t0 + end) * BN))
+          m_ref = kMinusInf;
         const int64_t to = (sg.sq.start + grow / a.group) * a.o_t + (sg.head * a.group + grow % a.group) * a.o_h;
         float* part = parts + (static_cast<int64_t>(pair) * 2 + (starts ? 1 : 0)) * part_floats(BM, D);
-        const float inv = starts && ends ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        const float inv = starts && ends ? row_factor(m_ref, l) : 1.0f;
         if (!(starts && ends) && real) {
           part[row] = m_ref;
           part[BM + row] = l;
