@@ -1023,9 +1023,7 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
   // pairs of CTAs that can be on the device at once (an SM without a partner in its
   // cluster takes none), asked once per kernel and device
   static std::atomic<int> cached[64];
-  std::atomic<int>& slot = cached[dev.device];
-  int pairs = slot.load(std::memory_order_relaxed);
-  if (pairs == 0) {
+  const int pairs = std::min(dev.num_sms / 2, resident(cached[dev.device & 63], dev.num_sms / 2, [&](int* n) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(dev.num_sms / 2 * 2);
     cfg.blockDim = dim3(kThreads);
@@ -1036,10 +1034,8 @@ cudaError_t go(const Cache& c, const Batch& b, const Attend& a, void* ws, const 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs <= 0) pairs = dev.num_sms / 2;
-    pairs = std::min(pairs, dev.num_sms / 2);
-    slot.store(pairs, std::memory_order_relaxed);
-  }
+    return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+  }));
   Desc* desc = static_cast<Desc*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + (sizeof(Desc) * dev.num_sms + 255) / 256 * 256);
   kern<<<2 * pairs, kThreads, Cfg<D>::SMEM, stream>>>(c, b, a, desc, parts, WaitCtl{dev.status, dev.wait_limit_ns});

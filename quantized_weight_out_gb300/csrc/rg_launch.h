@@ -39,6 +39,22 @@ inline cudaError_t counted(cudaError_t e) {
   return e;
 }
 
+// What a query of the runtime says can be resident (query(int*) -> cudaError_t), kept in `slot`;
+// threads that race on the first call store the same value.  Where the query fails, `guess`,
+// which is not kept, and the runtime forgets the failure: a launch's own status is read from
+// cudaGetLastError() and is not to answer for it.
+template <class Query>
+int resident(std::atomic<int>& slot, int guess, Query&& query) {
+  int n = slot.load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (query(&n) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    return guess;
+  }
+  slot.store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // f(std::integral_constant<int, WT>{}) for the run-time weight type wtype;
 // `fallback` for a type the library does not know (callers validate first).
 template <class R, class F>

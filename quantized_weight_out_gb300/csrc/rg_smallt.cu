@@ -1382,21 +1382,18 @@ __global__ void __launch_bounds__(256) smallt_reduce_wide(const float* __restric
 // Resident CTAs per SM of smallt_kernel<WT, TB> on this device (queried once).
 template <int WT, int TB>
 static int smallt_residency(const DevInfo& dev) {
-  // per device; threads that race on the first call store the same value
+  // per device; threads that race on the first call store the same value.  (One where it
+  // cannot be asked, and that is kept: workspace and launch are planned with the same number.)
   static std::atomic<int> cache[64];
   std::atomic<int>& slot = cache[dev.device & 63];
-  int c = slot.load(std::memory_order_relaxed);
-  if (c == 0) {
+  const int c = resident(slot, 1, [](int* n) {
     auto kern = smt::smallt_kernel<WT, TB>;
     constexpr size_t smem = smt::smem_bytes<WT, TB>();
-    int n = 0;
-    if (ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, smt::THREADS + 32, smem) != cudaSuccess ||
-        n <= 0)
-      n = 1;
-    slot.store(n, std::memory_order_relaxed);
-    c = n;
-  }
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+    return e != cudaSuccess ? e
+                            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, smt::THREADS + 32, smem);
+  });
+  slot.store(c, std::memory_order_relaxed);
   return c;
 }
 
@@ -1517,16 +1514,10 @@ static cudaError_t launch_smallt_fwd_t(const void* W, int64_t N, int64_t K, cons
   constexpr size_t smem = smt::fwd_smem_bytes<WT>();
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  // per device; threads that race on the first call store the same value
-  static std::atomic<int> cache[64];
-  std::atomic<int>& slot = cache[dev.device & 63];
-  int per_sm = slot.load(std::memory_order_relaxed);
-  if (per_sm == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, smt::THREADS + 32, smem) != cudaSuccess ||
-        per_sm <= 0)
-      per_sm = 1;
-    slot.store(per_sm, std::memory_order_relaxed);
-  }
+  static std::atomic<int> cache[64];  // per device
+  const int per_sm = resident(cache[dev.device & 63], 1, [&](int* n) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, smt::THREADS + 32, smem);
+  });
   // blocks of rows: the largest of 32 (16 for F32), 16 and 8 rows that still
   // gives at least half a wave of CTAs
   const int64_t n_tchunks = (T + TB - 1) / TB;

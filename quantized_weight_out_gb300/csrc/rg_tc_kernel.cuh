@@ -1609,19 +1609,12 @@ static cudaError_t launch_tc_t(const CUtensorMap& mw, const CUtensorMap& my,
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  // persistent grid: no more clusters than can be resident at once
-  // (per device; threads that race on the first call store the same value)
+  // persistent grid: no more clusters than can be resident at once (per device)
   static std::atomic<int> max_clusters[64];
-  std::atomic<int>& mc_slot = max_clusters[dev.device & 63];
-  int mc = mc_slot.load(std::memory_order_relaxed);
-  if (mc == 0) {
+  const int mc = resident(max_clusters[dev.device & 63], dev.num_sms / CG, [&](int* n) {
     cfg.gridDim = dim3(static_cast<unsigned>(CG * (dev.num_sms / CG)), 1, 1);
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
-      n = dev.num_sms / CG;
-    mc_slot.store(n, std::memory_order_relaxed);
-    mc = n;
-  }
+    return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+  });
   const int units = std::min(p.grid / CG, mc);
   cfg.gridDim = dim3(static_cast<unsigned>(units * CG), 1, 1);
   if (SK && part == nullptr) return cudaErrorInvalidValue;
