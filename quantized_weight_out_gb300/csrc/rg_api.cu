@@ -68,6 +68,7 @@ const Env& env() {
 int current_dev(DevInfo** out) {
   int d = 0;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return RG_ERR_CUDA;
+  (void)cudaGetLastError();  // of an earlier call that has reported it: launches read their status from there
   std::lock_guard<std::mutex> lk(g_mu);
   if (!g_dev_ready[d]) {
     DevInfo info{};
