@@ -855,7 +855,8 @@ const char* rg_strerror(int status) {
     case RG_ERR_CUDA: return "CUDA call or kernel launch failed";
     case RG_ERR_TIMEOUT: return "a bounded device-side wait gave up";
     case RG_ERR_RANGE:
-      return "a dY value lay outside the 16-bit tensor-core operand range (fp16: |dY| >= 65520)";
+      return "a finite value (dY, X; a cached key or value, a query) lay outside the range of the 16-bit "
+             "tensor-core operands (fp16: 65504)";
     case RG_ERR_INDEX:
       return "a device array of lengths or page numbers holds a value outside the cache or the batch";
     default: return "unknown status";
