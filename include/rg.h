@@ -389,7 +389,7 @@ typedef struct rg_kv_batch {
   int32_t seqs;
   int32_t max_pages;          /* columns of page_table; times page_tokens at most 2^30  */
   int32_t max_new;            /* no sequence has more new tokens (sets the launch)      */
-  int32_t reserved;           /* 0                                                      */
+  int32_t reserved;           /* 0 (else RG_ERR_ARG)                                    */
   int64_t tokens;             /* rows of the packed arrays                              */
   const int32_t* new_start;   /* device [seqs + 1], ascending                           */
   const int32_t* kv_len;      /* device [seqs]                                          */

@@ -24,7 +24,7 @@ int check(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, kv::Cac
   if ((cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) || cache->page_tokens % 16 ||
       cache->page_tokens > 4096)
     return RG_ERR_SHAPE;
-  if (batch->seqs < 0 || batch->max_pages < 0 || batch->max_new < 0 || batch->tokens < 0 ||
+  if (batch->seqs < 0 || batch->max_pages < 0 || batch->max_new < 0 || batch->reserved != 0 || batch->tokens < 0 ||
       batch->tokens > kMaxDim || static_cast<int64_t>(batch->max_pages) * cache->page_tokens > kMaxLen)
     return RG_ERR_ARG;
   if (batch->seqs == 0 || batch->tokens == 0 || batch->max_new == 0) {
