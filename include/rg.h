@@ -367,7 +367,9 @@ int rg_out_prod_lora(int variant, int wtype, const void* W, int64_t N, int64_t K
  * below 0 (kv_len less than the new tokens, as for a padding sequence of
  * length 0) is no error: the token is not stored, reads back as zeros, and
  * sees nothing.  Rows that belong to no sequence are left as they are.
- * Page numbers past a sequence's length are not looked at.
+ * Page numbers past a sequence's length are not looked at.  A batch of no
+ * sequences, of no rows or with max_new 0 has nothing to do: RG_OK, no launch,
+ * and its arrays are not looked at.
  *
  * Activations (`atype`: RG_F32, RG_F16 or RG_BF16) are addressed by element
  * strides of tokens and heads, the head_dim values of a row contiguous:
@@ -432,14 +434,19 @@ int rg_kv_read(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, vo
  * (RG_ERR_ARG).
  *
  * Scores, softmax statistics and sums are F32.  The matrix units take 16-bit
- * operands (fp16; bf16 for a BF16 cache): F32 queries, decoded Q8_0 and Q4_0
- * values and the probabilities are rounded once to them, each a relative
- * error of at most 2^-11 (bf16: 2^-8).  Queries and cached values beyond
- * fp16's range are reported as RG_ERR_RANGE (queries here, cached values when
- * they are stored).  Keys and values at positions a token may not see do not
- * reach its result, whatever they hold, NaN included.  Results do not change
- * from call to call on one kind of GPU; they depend on the batch in the order
- * of summation only.
+ * operands (fp16; bf16 for a BF16 cache): queries of another type than that,
+ * decoded Q8_0 and Q4_0 values and the probabilities are rounded once to them,
+ * each a relative error of at most 2^-11 (bf16: 2^-8); below fp16's normal
+ * range, 2^-14, the error of a query is at most 2^-25, that of a probability
+ * 2^-32 of the row's largest.  The sum that a result is divided by is that of
+ * the probabilities before they are rounded.  Queries and cached values beyond
+ * the operands' range are reported as RG_ERR_RANGE (queries here, cached values
+ * when they are stored).  Keys and values at positions a token may not see do
+ * not reach its result, whatever they hold, NaN included; what it sees counts
+ * as the definition has it: an infinite value gives an infinity (NaN where its
+ * probability rounds to zero), a score that is NaN and scores that are all -inf
+ * give NaN.  Results do not change from call to call on one kind of GPU; they
+ * depend on the batch in the order of summation only.
  *
  * The workspace (rg_kv_attend_workspace_bytes) comes from the library's
  * stream-ordered pool, or from the caller in rg_kv_attend_ws (256-byte
