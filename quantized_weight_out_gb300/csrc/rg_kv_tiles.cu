@@ -325,9 +325,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = s0 + warp; s < min(b.seqs, s0 + kScan); s += kThreads / 32) {
       const Seq q = load_seq(b, c.page_tokens, s, status);
       const int nrb = blocks_of<BM>(q, a.group, a.rows_limit);
-      int n = 0;
-      for (int rb = lane; rb < nrb; rb += 32) n += block_of<BM>(q, a.group, a.window, rb).nt;
-      long long all = n;
+      long long all = 0;  // (2^21 blocks of 2^23 tiles at most)
+      for (int rb = lane; rb < nrb; rb += 32) all += block_of<BM>(q, a.group, a.window, rb).nt;
 #pragma unroll
       for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
       if (lane == 0) sh_tiles[s - s0] = all * c.kv_heads;
