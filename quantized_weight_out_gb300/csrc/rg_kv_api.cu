@@ -200,7 +200,7 @@ size_t rg_kv_attend_workspace_bytes(const rg_kv_cache* cache, const rg_kv_batch*
   kv::Batch b;
   bool empty;
   if (check(cache, batch, RG_F32, &c, &b, &empty) != RG_OK || empty || heads < 1 || heads % c.kv_heads ||
-      heads / c.kv_heads > 1024)
+      heads / c.kv_heads > 1024 || static_cast<int64_t>(b.max_new) * (heads / c.kv_heads) > kMaxLen)
     return 0;
   DevInfo* dev = nullptr;
   if (current_dev(&dev) != RG_OK) return 0;

@@ -30,3 +30,15 @@ def test_a_failed_allocation_is_not_the_next_calls(rg):  # noqa: F811
         assert good() == rg.RG_OK
     rg.check(rg.rg_check(s), "rg_check")
     assert torch.equal(out, torch.ones_like(out))
+
+
+def test_workspace_of_a_refused_batch(rg):  # noqa: F811
+    """0 for what rg_kv_attend refuses: more rows a sequence than 2^30."""
+    su = Setup(torch, rg, inputs.Q8_0, 64, 1, 16, [(1, 1)], atype=RG_F32)
+    x = torch.zeros(64, device="cuda")
+    for max_new, ok in ((1 << 20, True), ((1 << 20) + 1, False)):
+        b = rg.kv_batch(su.start_d, su.len_d, su.table_d, 1 << 30, max_new)
+        assert (rg.rg_kv_attend_workspace_bytes(su.cache, b, 1024) > 0) == ok
+        if not ok:
+            assert rg.rg_kv_attend(su.cache, b, RG_F32, x, 64, 64, 1024, x, 64, 64, 0.1, 0,
+                                   torch.cuda.current_stream()) == rg.RG_ERR_ARG
