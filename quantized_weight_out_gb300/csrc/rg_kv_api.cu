@@ -83,11 +83,12 @@ struct Route {
 Route route_of(const kv::Cache& c, const kv::Batch& b, int group, const DevInfo& dev) {
   Route r;
   r.tiles = static_cast<int64_t>(b.max_new) * group > kRowsLimit;
-  // (one sequence alone: whatever its length turns out to be, one kernel has it)
-  r.rows_limit = !r.tiles ? 2147483647 : b.seqs == 1 ? 0 : kRowsLimit;
+  // (one sequence alone: whatever its length turns out to be, one kernel has it; and where
+  // one token is more rows than that, none is left for the few-row kernel)
+  r.rows_limit = !r.tiles ? 2147483647 : b.seqs == 1 || group > kRowsLimit ? 0 : kRowsLimit;
   kv::Batch few = b;
   if (r.tiles) few.max_new = std::max(1, kRowsLimit / group);
-  r.rows_bytes = (kv::rows_workspace(c, few, group, dev) + 255) / 256 * 256;
+  r.rows_bytes = r.rows_limit ? (kv::rows_workspace(c, few, group, dev) + 255) / 256 * 256 : 0;
   r.tiles_bytes = r.tiles ? kv::tiles_workspace(c, dev) : 0;
   return r;
 }
