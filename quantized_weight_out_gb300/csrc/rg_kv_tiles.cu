@@ -27,10 +27,10 @@
 // prompt over a long cache uses every SM.  An item cut by a border leaves F32
 // parts that a second kernel joins in a fixed order.
 // Measured: 1021 tokens of 32 heads over a Q8_0 context of 15,000 (8 kv heads of 128)
-// 232 us, 1.11 PFLOP/s, 0.59 of the measured burst bf16 rate; four packed prompts of
-// 700 to 4,099 tokens, bf16 cache, 453 us, 0.84 PFLOP/s (one item's rows are written
+// 235 us, 1.10 PFLOP/s, 0.59 of the measured burst bf16 rate; four packed prompts of
+// 700 to 4,099 tokens, bf16 cache, 443 us, 0.85 PFLOP/s (one item's rows are written
 // and the next one's first tile started in about 11,000 cycles of 3,300 a tile); 16
-// heads of 256, the same prompts, 559 us.  The tensor pipe is active 55 % of the time:
+// heads of 256, the same prompts, 588 us a call.  The tensor pipe is active 53 % of the time:
 // a stream's chain (scores complete, softmax 1,200 cycles, probabilities stored 250,
 // waits 400, products and next scores 1,400) is longer than the other stream covers.
 #include "rg_kv_attend.cuh"
@@ -603,6 +603,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                       : wait_bar(bar(ODONE + ((n_s - 1) & 1)), ((n_s - 1) >> 1) & 1, ctl, &abort_flag));
         if (!ok) break;
         tc_fence_after();
+        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord % kFlags]) == ord)) {
+          // Values that are not finite were left out of the products of tiles that some row sees
+          // in part.  What this row sees of them in dimensions 32 k .. + 31: an infinity of either
+          // sign a bit (both: NaN).  The warp looks at a token's 32 dimensions together.  (The
+          // segment is read again, past the compiler: with its copies in registers for this, rare,
+          // the tiles' loop took 2 to 5 % longer.)
+          const volatile Segment& v = *const_cast<const volatile Segment*>(&sg);
+          const int* table = b.table + static_cast<int64_t>(v.seq) * b.max_pages;
+          const int low = v.b.minpos, high = v.b.maxpos, head = v.head;
+          const int at = real ? v.sq.len - v.sq.n + (v.rb * BM + row) / a.group : -1;  // this row's position
+          const int past = min((v.b.t0 + v.end) * BN, high + 1);
+          const bool all = v.holes;
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t plus = 0, minus = 0;
+#pragma unroll 1
+            for (int j0 = (v.b.t0 + v.begin) * BN; j0 < past; j0 += kGranule) {
+              const int t = j0 / BN * BN;
+              if (!(all || t + BN - 1 > low || (a.window && t <= high - a.window))) continue;  // (as tile_masked())
+              if (a.window && j0 + kGranule - 1 <= low - a.window) continue;
+              const int page = table[j0 / c.page_tokens];
+              if (page < 0 || page >= c.pages) continue;
+              const uint8_t* src = c.data + granule_offset(c, page, 1, head, j0, GB);
+              // (mostly there is none in the granule's block)
+              ValueWords<TYPE> vw;
+              load_words<TYPE, D>(vw, src, k, lane);
+              uint32_t vb[4][2];
+              value_operand(vw, vb);
+              const uint32_t every[2] = {~0u, ~0u};
+              if (!__any_sync(0xFFFFFFFFu, clean_operand<TYPE>(vb, every))) continue;
+#pragma unroll 1
+              for (int j = 0; j < kGranule; ++j) {
+                const float x = value_not_finite<TYPE, D>(src, j, 32 * k + lane);
+                const uint32_t up = __ballot_sync(0xFFFFFFFFu, !(x <= 0.0f)), down = __ballot_sync(0xFFFFFFFFu, !(x >= 0.0f));
+                if (j0 + j <= at && !(a.window && j0 + j <= at - a.window)) {
+                  plus |= up;
+                  minus |= down;
+                }
+              }
+            }
+            uint32_t any = plus | minus;
+#pragma unroll
+            for (int i = 16; i; i >>= 1) any |= __shfl_xor_sync(0xFFFFFFFFu, any, i);
+#pragma unroll 1
+            for (; any; any &= any - 1) {
+              const int e = __ffs(any) - 1;
+              uint32_t o;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                           : "=r"(o) : "r"(tO + 32 * k + e) : "memory");
+              float x = __uint_as_float(o);
+              if (plus >> e & 1) x += INFINITY;
+              if (minus >> e & 1) x -= INFINITY;
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tO + 32 * k + e),
+                           "r"(__float_as_uint(x))
+                           : "memory");
+              tmem_wait_st();
+            }
+          }
+        }
         const bool starts = begin == 0, ends = end == sg.b.nt;
         if (m_ref == kNone && sees_any(c, b.table + static_cast<int64_t>(sg.seq) * b.max_pages, a.window, pos,
                                        (t0 + begin) * BN, (t0 + end) * BN))
@@ -613,51 +672,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(starts && ends) && real) {
           part[row] = m_ref;
           part[BM + row] = l;
-        }
-        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&poison[ord % kFlags]) == ord)) {
-          // Values that are not finite were left out of the products of tiles that some row sees
-          // in part.  What this row sees of them in dimensions 32 k .. + 31: an infinity of either
-          // sign a bit (both: NaN).  The warp looks at a token's 32 dimensions together.
-          const int* table = b.table + static_cast<int64_t>(sg.seq) * b.max_pages;
-          const int from = a.window ? max(0, minpos - a.window + 1) : 0;  // the first position that any row sees
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t plus = 0, minus = 0;
-#pragma unroll 1
-            for (int j0 = (t0 + begin) * BN; j0 < (t0 + end) * BN && j0 <= maxpos; j0 += kGranule) {
-              if (j0 + kGranule <= from || !(holes || tile_masked(sg.b, a.window, j0 / BN))) continue;
-              const int page = table[j0 / c.page_tokens];
-              if (page < 0 || page >= c.pages) continue;
-              const uint8_t* src = c.data + granule_offset(c, page, 1, sg.head, j0, GB);
-              // (mostly there is none in the granule's block)
-              ValueWords<TYPE> vw;
-              load_words<TYPE, D>(vw, src, k, lane);
-              uint32_t vb[4][2];
-              value_operand(vw, vb);
-              const uint32_t all[2] = {~0u, ~0u};
-              if (!__any_sync(0xFFFFFFFFu, clean_operand<TYPE>(vb, all))) continue;
-#pragma unroll 1
-              for (int j = 0; j < kGranule; ++j) {
-                const float v = value_not_finite<TYPE, D>(src, j, 32 * k + lane);
-                const uint32_t up = __ballot_sync(0xFFFFFFFFu, !(v <= 0.0f)), down = __ballot_sync(0xFFFFFFFFu, !(v >= 0.0f));
-                if (j0 + j <= pos && !(a.window && j0 + j <= pos - a.window)) {
-                  plus |= up;
-                  minus |= down;
-                }
-              }
-            }
-            if (__any_sync(0xFFFFFFFFu, plus | minus)) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO + 32 * k, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (plus >> e & 1) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
-                if (minus >> e & 1) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
-              }
-              tmem_st32(tO + 32 * k, o);
-              tmem_wait_st();
-            }
-          }
         }
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
