@@ -55,7 +55,7 @@ int check(const rg_kv_cache* cache, const rg_kv_batch* batch, int atype, kv::Cac
 }
 
 // A packed array of `heads` rows of head_dim values a token: 16-byte aligned
-// rows; strides at least a row long, so that no two rows overlap.
+// rows; strides at least a row long.
 int check_rows(const void* p, int64_t st, int64_t sh, int heads, int dim, int atype) {
   if (st < 0 || sh < 0) return RG_ERR_ARG;
   const int64_t unit = atype == RG_F32 ? 4 : 8;

@@ -18,13 +18,13 @@
 // probabilities are at most 2^15, the range fp16 has to spare, and the
 // accumulators are rescaled a few times a row instead of at every granule.
 // What bounds it: Q8_0 at G = 4, 64 ragged contexts of 300 to 15,000 tokens (1.15 GB),
-// 196 us, 5.9 TB/s, 0.87 of the copy bandwidth; fewer bytes a value leave the decode's
-// instructions in front: Q4_0 at 131,072 tokens 62 us, 2.4 TB/s (500 warp instructions a
-// granule, of which 230 turn nibbles into scaled halves; about 20 us are launch, shares,
-// first copies and the join).  Rows on the M side, as first built, took 250 us for the
+// 200 us, 5.8 TB/s, 0.85 of the copy bandwidth; fewer bytes a value leave the decode's
+// instructions in front: Q4_0 at 131,072 tokens 65 us, 2.3 TB/s (550 warp instructions a
+// granule, issued in 62 % of the cycles of a kernel of 58 us; the rest is the join).  Rows on the M side, as first built, took 250 us for the
 // ragged batch: 16 rows where 4 exist, twice the accumulators and matrix instructions.
-// Scores, statistics and accumulators are F32; queries (F32 ones), decoded
-// values and probabilities are rounded once to fp16 (a BF16 cache: bf16).
+// Scores, statistics and accumulators are F32; queries (of another type), decoded
+// values and probabilities are rounded once to fp16 (a BF16 cache: bf16), since the
+// matrix instructions take 16-bit operands, both of one type.
 #include "rg_kv_launch.h"
 #include "rg_kv_attend.cuh"
 

@@ -11,9 +11,9 @@
 // a time.  Bound by memory for prompts, by latency for single tokens.  Measured
 // (GB300, a call inside a replayed graph): 121,000 tokens of 8 heads of 128 read back
 // from Q8_0 as bf16 in 137 us, 5.5 TB/s of what has to move, four fifths of the copy
-// bandwidth; prompts of 15,000 tokens stored and read back in 53 us (the write's part,
-// about 35, is half instruction issue: a maximum, a product and a rounding per value);
-// one token each of 7 sequences stored and read back in 9 us, two launches.
+// bandwidth; prompts of 15,000 tokens stored in 30 us (instructions issued in 57 % of the
+// cycles, a maximum, a product and a rounding per value, and latency for the rest) and read
+// back in 21; one token each of 7 sequences stored and read back in 9 us, two launches.
 #include "rg_kv.cuh"
 #include "rg_kv_launch.h"
 

@@ -27,10 +27,10 @@
 // prompt over a long cache uses every SM.  An item cut by a border leaves F32
 // parts that a second kernel joins in a fixed order.
 // Measured: 1021 tokens of 32 heads over a Q8_0 context of 15,000 (8 kv heads of 128)
-// 235 us, 1.10 PFLOP/s, 0.59 of the measured burst bf16 rate; four packed prompts of
+// 233 us, 1.11 PFLOP/s, 0.59 of the measured burst bf16 rate; four packed prompts of
 // 700 to 4,099 tokens, bf16 cache, 443 us, 0.85 PFLOP/s (one item's rows are written
 // and the next one's first tile started in about 11,000 cycles of 3,300 a tile); 16
-// heads of 256, the same prompts, 588 us a call.  The tensor pipe is active 53 % of the time:
+// heads of 256, the same prompts, 557 us a call.  The tensor pipe is active 54 % of the time:
 // a stream's chain (scores complete, softmax 1,200 cycles, probabilities stored 250,
 // waits 400, products and next scores 1,400) is longer than the other stream covers.
 #include "rg_kv_attend.cuh"
