@@ -121,7 +121,9 @@ typedef enum {
                             operands' range (rg_kv_write, rg_kv_attend)                */
     RG_ERR_INDEX = -8    /* paged cache: a length, a first token or a page number in a device
                             array lies outside the batch or the cache (reported by rg_check;
-                            the sequence counts as empty, the page's tokens as not there)  */
+                            the sequence counts as empty, the page's tokens as not there).
+                            Indexed calls: an id past the table or the experts, a range or a
+                            slot outside the batch (it counts as pointing nowhere)         */
 } rg_status;
 
 /* Kernel variants of rg_out_prod_variant. */
@@ -461,6 +463,151 @@ int rg_kv_attend_ws(const rg_kv_cache* cache, const rg_kv_batch* batch, int atyp
 /* Device workspace bytes of one rg_kv_attend call on the current device (0
  * for descriptions that it refuses and for an empty batch). */
 size_t rg_kv_attend_workspace_bytes(const rg_kv_cache* cache, const rg_kv_batch* batch, int heads);
+
+/*
+ * Indexed work on resident weights: rows of a table by token, the router of a
+ * mixture of experts, and the experts' products, each expert with the slots
+ * that chose it.
+ *
+ * Activations (`atype`: RG_F32, RG_F16 or RG_BF16) are rows an element stride
+ * apart, 16-byte aligned: pointers, and strides times the element size,
+ * multiples of 16 (RG_ERR_ALIGN); strides at least a row long (RG_ERR_ARG).
+ * Indices are device int32 arrays, read by the kernels, so a captured graph
+ * serves every step.  An index below 0 is one that points nowhere (padding):
+ * it reads as a row of zeros and adds nothing.  One past the end counts the
+ * same and is reported as RG_ERR_INDEX (rg_check).  Results do not depend on
+ * timing: no sum's order does.
+ */
+
+/* out[i, :] = scale * deq(W)[ids[i], :] for i < n: W is a table of N rows of
+ * any weight type, K as for rg_out_prod (multiples of 256, or 8), rows of any
+ * alignment.  Values are decoded as rg_dequant does, multiplied in F32 and
+ * rounded once to atype.  One launch, no workspace. */
+int rg_get_rows(int wtype, const void* W, int64_t N, int64_t K, const int32_t* ids, int64_t n, float scale, int atype,
+                void* out, int64_t out_row, void* stream);
+
+/* The gradient of a table that is trained (an F32 table, or an adapter's half
+ * on a resident one, whose rows are as long as its rank):
+ *
+ *     G[r, :] = beta * G[r, :] + scale * sum over ids[i] == r of dY[i, :]
+ *
+ * for every r < N.  dY: [n, K] of atype; G: [N, K] F32, rows g_row apart; K a
+ * multiple of 8 (RG_ERR_SHAPE).  With beta 0 the old G is not read; with beta 1
+ * rows that no id names are left alone.  The ids are sorted on the device
+ * (stable), and each row's sum is taken in F32 in the order of i, in windows of
+ * the sorted order: the same bits every time.  The workspace comes from the
+ * library's pool, or from the caller in rg_get_rows_back_ws (256-byte aligned;
+ * RG_ERR_ARG if too small), which allocates nothing. */
+int rg_get_rows_back(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int64_t n, float scale, float* G,
+                     int64_t g_row, int64_t N, int64_t K, float beta, void* stream);
+int rg_get_rows_back_ws(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int64_t n, float scale, float* G,
+                        int64_t g_row, int64_t N, int64_t K, float beta, void* workspace, size_t workspace_bytes,
+                        void* stream);
+/* Device workspace bytes of one rg_get_rows_back call (0 for sizes it refuses
+ * or has nothing to sort for). */
+size_t rg_get_rows_back_workspace_bytes(int64_t n, int64_t N, int64_t K);
+
+/* Over which experts the router's weights sum to `scale`. */
+typedef enum {
+    RG_ROUTE_TOP = 0,  /* those that the token chose  */
+    RG_ROUTE_ALL = 1   /* all of them                 */
+} rg_route_mode;
+
+/* The router: of each of T tokens the `top` experts of the largest logits, in
+ * falling order, of equal ones the lower number first:
+ *
+ *     weights[t, j] = scale * exp(l[t, ids[t, j]]) / sum_e exp(l[t, e]),
+ *
+ * the sum over the chosen experts or over all (`mode`), in F32 with the largest
+ * logit subtracted.  logits: F32, rows l_row apart (rg_mul_mat's Y); ids and
+ * weights: [T, top].  An expert whose logit is -inf or NaN takes no part; a
+ * token with fewer than `top` others gets id -1 and weight 0 for the rest.
+ * experts at most 1024, top at most 32 and at most experts (RG_ERR_SHAPE);
+ * scale finite (RG_ERR_ARG).
+ *
+ * start [experts + 1] and order [T * top] (both or neither NULL) receive the
+ * slots by expert, as rg_group gives them for ids.  No workspace. */
+int rg_route(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale, int32_t* ids,
+             float* weights, int32_t* start, int32_t* order, void* stream);
+
+/* The gradient of rg_route's weights with respect to the logits: dlogits
+ * [T, experts] (rows dl_row apart; zeros where an expert takes no part) from
+ * dweights [T, top], the logits and the ids that rg_route chose.  One launch. */
+int rg_route_back(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale,
+                  const int32_t* ids, const float* dweights, float* dlogits, int64_t dl_row, void* stream);
+
+/* Slots by group: order [n] is a permutation of 0 .. n - 1, sorted by (ids[i],
+ * i), those of no group (an id below 0; one of `groups` or more, which is
+ * reported) behind the last group's; group g's are order[start[g]] ..
+ * order[start[g + 1] - 1], start [groups + 1].  groups at most 1024
+ * (RG_ERR_SHAPE).  One launch, no workspace. */
+int rg_group(const int32_t* ids, int64_t n, int groups, int32_t* start, int32_t* order, void* stream);
+
+/* The slots of one call of the products below: per_token of them a token, slot
+ * s token s / per_token's.  start and order as rg_route or rg_group gives them;
+ * the kernels check what they read (a range of start that is none counts as
+ * empty, an entry of order outside the slots as none, either is reported as
+ * RG_ERR_INDEX).  order is a permutation of the slots; where it is not, rows
+ * named twice hold either of their results and sums over tokens are undefined. */
+typedef struct rg_id_batch {
+  int32_t experts;       /* matrices in W, at most 1024 (RG_ERR_SHAPE)     */
+  int32_t per_token;     /* at least 1; divides slots (RG_ERR_SHAPE)       */
+  int64_t slots;
+  const int32_t* start;  /* device [experts + 1]                           */
+  const int32_t* order;  /* device [slots]                                 */
+} rg_id_batch;
+
+/* Whose rows an array of a product holds. */
+typedef enum {
+    RG_ROWS_SLOT = 0,   /* a row per slot                                                */
+    RG_ROWS_TOKEN = 1   /* a row per token: read by each of its slots; written as the sum
+                           of its slots' rows                                            */
+} rg_rows_of;
+
+/*
+ * The forward and the activation gradient through a stack of resident weights,
+ * each slot with its expert's: W is `experts` matrices of N rows of K values,
+ * one after another, of any weight type.  For a slot s of expert e
+ *
+ *     rg_mul_mat_id:   y_s = w_s * X[row of s] . deq(W_e)^T     (K values to N)
+ *     rg_out_prod_id:  x_s = w_s * dY[row of s] . deq(W_e)      (N values to K)
+ *
+ * with w_s = weights[s] (F32 [slots], or NULL: 1).  Written by slot, row s is
+ * beta times itself plus that; rows of slots that have no expert are left as
+ * they are.  Written by token, row t is beta times itself plus the sum over the
+ * token's slots that have an expert, in their order, in F32.  With beta 0 old
+ * rows are not read.  K a multiple of 256 (8 for 16- and 32-bit types), N of 8
+ * (RG_ERR_SHAPE).  No slots: RG_OK, nothing launched; no experts or an empty
+ * contraction: RG_ERR_SHAPE.
+ *
+ * Sums are F32.  The tensor cores take 16-bit operands, fp16 (bf16 for BF16 W):
+ * W's values are decoded into them as in rg_mul_mat, and an input row is rounded
+ * once, after a power of two that brings its largest magnitude to 2^14 (fp16),
+ * undone exactly afterwards: rows of any magnitude keep 11 bits and none
+ * overflows, so RG_ERR_RANGE is not reported.  |err| <= 5e-3 * sum |in||deq W|
+ * (times |w_s|) plus the result's own rounding to atype.  F32 W, and rows of W
+ * that are not 16-byte aligned (Q6_K, Q3_K with K % 2048 != 0, Q2_K with K %
+ * 1024, MXFP4 with K % 512), take a slower route with exact values and F32
+ * products.
+ *
+ * The workspace (rg_*_id_workspace_bytes) comes from the library's
+ * stream-ordered pool, or from the caller in the _ws forms (256-byte aligned;
+ * RG_ERR_ARG if too small), which allocate nothing.
+ */
+int rg_mul_mat_id(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* X,
+                  int64_t x_row, int x_of, void* Y, int64_t y_row, int y_of, const float* weights, float beta,
+                  void* stream);
+int rg_mul_mat_id_ws(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* X,
+                     int64_t x_row, int x_of, void* Y, int64_t y_row, int y_of, const float* weights, float beta,
+                     void* workspace, size_t workspace_bytes, void* stream);
+size_t rg_mul_mat_id_workspace_bytes(int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int y_of);
+int rg_out_prod_id(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* dY,
+                   int64_t dy_row, int dy_of, void* dX, int64_t dx_row, int dx_of, const float* weights, float beta,
+                   void* stream);
+int rg_out_prod_id_ws(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype,
+                      const void* dY, int64_t dy_row, int dy_of, void* dX, int64_t dx_row, int dx_of,
+                      const float* weights, float beta, void* workspace, size_t workspace_bytes, void* stream);
+size_t rg_out_prod_id_workspace_bytes(int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int dx_of);
 
 /* The variant RG_VARIANT_AUTO picks for this shape (ignores RG_VARIANT). */
 int rg_select_variant(int wtype, int64_t N, int64_t K, int64_t T);

@@ -17,3 +17,6 @@ from .quant_out_prod import (  # noqa: F401
 from .kv_attention import (  # noqa: F401
     kv_row_bytes, kv_page_bytes, kv_quantise, kv_values, kv_places, kv_store, kv_attend, bf16_round,
 )
+from .indexed import (  # noqa: F401
+    get_rows, get_rows_back, group, route, route_back, product_id, ROUTE_TOP, ROUTE_ALL,
+)

@@ -48,6 +48,12 @@ class rg_kv_batch(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
+class rg_id_batch(ctypes.Structure):
+    """include/rg.h rg_id_batch (id_batch() fills one in)."""
+    _fields_ = [("experts", ctypes.c_int32), ("per_token", ctypes.c_int32), ("slots", ctypes.c_int64),
+                ("start", ctypes.c_void_p), ("order", ctypes.c_void_p)]
+
+
 # (name, restype, argtypes) of every exported function
 _I64, _VP, _F, _I, _SZ = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
 SIGNATURES = [
@@ -81,7 +87,24 @@ SIGNATURES = [
     ("rg_kv_attend", _I, [_VP, _VP, _I, _VP, _I64, _I64, _I, _VP, _I64, _I64, _F, _I, _VP]),
     ("rg_kv_attend_ws", _I, [_VP, _VP, _I, _VP, _I64, _I64, _I, _VP, _I64, _I64, _F, _I, _VP, _SZ, _VP]),
     ("rg_kv_attend_workspace_bytes", _SZ, [_VP, _VP, _I]),
+    ("rg_get_rows", _I, [_I, _VP, _I64, _I64, _VP, _I64, _F, _I, _VP, _I64, _VP]),
+    ("rg_get_rows_back", _I, [_I, _VP, _I64, _VP, _I64, _F, _VP, _I64, _I64, _I64, _F, _VP]),
+    ("rg_get_rows_back_ws", _I, [_I, _VP, _I64, _VP, _I64, _F, _VP, _I64, _I64, _I64, _F, _VP, _SZ, _VP]),
+    ("rg_get_rows_back_workspace_bytes", _SZ, [_I64, _I64, _I64]),
+    ("rg_route", _I, [_VP, _I64, _I64, _I, _I, _I, _F, _VP, _VP, _VP, _VP, _VP]),
+    ("rg_route_back", _I, [_VP, _I64, _I64, _I, _I, _I, _F, _VP, _VP, _VP, _I64, _VP]),
+    ("rg_group", _I, [_VP, _I64, _I, _VP, _VP, _VP]),
+    ("rg_mul_mat_id", _I, [_I, _VP, _I64, _I64, _VP, _I, _VP, _I64, _I, _VP, _I64, _I, _VP, _F, _VP]),
+    ("rg_mul_mat_id_ws", _I, [_I, _VP, _I64, _I64, _VP, _I, _VP, _I64, _I, _VP, _I64, _I, _VP, _F, _VP, _SZ, _VP]),
+    ("rg_mul_mat_id_workspace_bytes", _SZ, [_I, _I64, _I64, _VP, _I]),
+    ("rg_out_prod_id", _I, [_I, _VP, _I64, _I64, _VP, _I, _VP, _I64, _I, _VP, _I64, _I, _VP, _F, _VP]),
+    ("rg_out_prod_id_ws", _I, [_I, _VP, _I64, _I64, _VP, _I, _VP, _I64, _I, _VP, _I64, _I, _VP, _F, _VP, _SZ, _VP]),
+    ("rg_out_prod_id_workspace_bytes", _SZ, [_I, _I64, _I64, _VP, _I]),
 ]
+
+# include/rg.h rg_route_mode and rg_rows_of
+RG_ROUTE_TOP, RG_ROUTE_ALL = 0, 1
+RG_ROWS_SLOT, RG_ROWS_TOKEN = 0, 1
 
 RG_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -222,6 +245,76 @@ def rg_kv_attend_ws(cache, batch, atype, q, q_t, q_h, heads, out, o_t, o_h, scal
 
 def rg_kv_attend_workspace_bytes(cache, batch, heads) -> int:
     return load().rg_kv_attend_workspace_bytes(_ref(cache), _ref(batch), heads)
+
+
+def rg_get_rows(wtype, W, N, K, ids, n, scale, atype, out, out_row, stream=None) -> int:
+    return load().rg_get_rows(wtype, _ptr(W), N, K, _ptr(ids), n, scale, atype, _ptr(out), out_row, _stream(stream))
+
+
+def rg_get_rows_back(atype, dY, dy_row, ids, n, scale, G, g_row, N, K, beta, stream=None) -> int:
+    return load().rg_get_rows_back(atype, _ptr(dY), dy_row, _ptr(ids), n, scale, _ptr(G), g_row, N, K, beta,
+                                   _stream(stream))
+
+
+def rg_get_rows_back_ws(atype, dY, dy_row, ids, n, scale, G, g_row, N, K, beta, workspace, workspace_bytes,
+                        stream=None) -> int:
+    return load().rg_get_rows_back_ws(atype, _ptr(dY), dy_row, _ptr(ids), n, scale, _ptr(G), g_row, N, K, beta,
+                                      _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rg_get_rows_back_workspace_bytes(n, N, K) -> int:
+    return load().rg_get_rows_back_workspace_bytes(n, N, K)
+
+
+def rg_route(logits, l_row, T, experts, top, mode, scale, ids, weights, start, order, stream=None) -> int:
+    return load().rg_route(_ptr(logits), l_row, T, experts, top, mode, scale, _ptr(ids), _ptr(weights), _ptr(start),
+                           _ptr(order), _stream(stream))
+
+
+def rg_route_back(logits, l_row, T, experts, top, mode, scale, ids, dweights, dlogits, dl_row, stream=None) -> int:
+    return load().rg_route_back(_ptr(logits), l_row, T, experts, top, mode, scale, _ptr(ids), _ptr(dweights),
+                                _ptr(dlogits), dl_row, _stream(stream))
+
+
+def rg_group(ids, n, groups, start, order, stream=None) -> int:
+    return load().rg_group(_ptr(ids), n, groups, _ptr(start), _ptr(order), _stream(stream))
+
+
+def id_batch(experts, per_token, start, order, slots=None) -> rg_id_batch:
+    """A batch of slots over device int32 arrays that the caller keeps (their
+    number from order's length unless given)."""
+    return rg_id_batch(experts, per_token, order.numel() if slots is None else slots, _ptr(start), _ptr(order))
+
+
+def rg_mul_mat_id(wtype, W, N, K, batch, atype, X, x_row, x_of, Y, y_row, y_of, weights, beta, stream=None) -> int:
+    return load().rg_mul_mat_id(wtype, _ptr(W), N, K, _ref(batch), atype, _ptr(X), x_row, x_of, _ptr(Y), y_row, y_of,
+                                _ptr(weights), beta, _stream(stream))
+
+
+def rg_mul_mat_id_ws(wtype, W, N, K, batch, atype, X, x_row, x_of, Y, y_row, y_of, weights, beta, workspace,
+                     workspace_bytes, stream=None) -> int:
+    return load().rg_mul_mat_id_ws(wtype, _ptr(W), N, K, _ref(batch), atype, _ptr(X), x_row, x_of, _ptr(Y), y_row, y_of,
+                                   _ptr(weights), beta, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rg_mul_mat_id_workspace_bytes(wtype, N, K, batch, y_of) -> int:
+    return load().rg_mul_mat_id_workspace_bytes(wtype, N, K, _ref(batch), y_of)
+
+
+def rg_out_prod_id(wtype, W, N, K, batch, atype, dY, dy_row, dy_of, dX, dx_row, dx_of, weights, beta,
+                   stream=None) -> int:
+    return load().rg_out_prod_id(wtype, _ptr(W), N, K, _ref(batch), atype, _ptr(dY), dy_row, dy_of, _ptr(dX), dx_row,
+                                 dx_of, _ptr(weights), beta, _stream(stream))
+
+
+def rg_out_prod_id_ws(wtype, W, N, K, batch, atype, dY, dy_row, dy_of, dX, dx_row, dx_of, weights, beta, workspace,
+                      workspace_bytes, stream=None) -> int:
+    return load().rg_out_prod_id_ws(wtype, _ptr(W), N, K, _ref(batch), atype, _ptr(dY), dy_row, dy_of, _ptr(dX), dx_row,
+                                    dx_of, _ptr(weights), beta, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rg_out_prod_id_workspace_bytes(wtype, N, K, batch, dx_of) -> int:
+    return load().rg_out_prod_id_workspace_bytes(wtype, N, K, _ref(batch), dx_of)
 
 
 def rg_workspace_bytes(variant, wtype, N, K, T) -> int:

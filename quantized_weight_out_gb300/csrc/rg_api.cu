@@ -423,7 +423,7 @@ CUresult encode_tiled_uncached(CUtensorMap* map, CUtensorMapDataType dtype, cons
   const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
   const cuuint32_t box[3] = {box0, box1, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, dtype, dim2 > 1 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+  return fn(map, dtype, dim2 > 1 || stride2_bytes != 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
@@ -858,7 +858,8 @@ const char* rg_strerror(int status) {
       return "a finite value (dY, X; a cached key or value, a query) lay outside the range of the 16-bit "
              "tensor-core operands (fp16: 65504)";
     case RG_ERR_INDEX:
-      return "a device array of lengths or page numbers holds a value outside the cache or the batch";
+      return "a device array of lengths, page numbers, ids or slots holds a value outside the cache, the "
+             "table, the experts or the batch";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,286 @@
+// rg_id.cu - products by slot around the tensor-core kernel: the table of
+// tiles and the input's copy in sorted order, the sum over a token's slots, and
+// the product in F32 by plain threads for rows of W that TMA cannot address.
+#include <algorithm>
+
+#include "rg_act.cuh"
+#include "rg_id_launch.h"
+
+namespace rg {
+namespace id {
+
+namespace {
+
+constexpr int THREADS = 256;
+
+// The table of tiles, by one block: a running sum of the experts' tiles.  An
+// expert whose range is not one (reported) has no slots; one whose tiles would
+// pass the table's end (ranges that overlap) is reported, and empty tiles stand
+// where its would.
+__device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, int* status) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ int64_t base_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) base_s = 0;
+  __syncthreads();
+  for (int e0 = 0; e0 < b.experts; e0 += THREADS) {
+    const int e = e0 + threadIdx.x;
+    int first = 0, rows = 0;
+    if (e < b.experts) {
+      const int lo = __ldg(b.start + e), hi = __ldg(b.start + e + 1);
+      if (lo < 0 || hi < lo || hi > b.slots) report_index(status);
+      else first = lo, rows = hi - lo;
+    }
+    const int64_t mine = rows / bt + (rows % bt != 0);
+    int64_t upto = mine;  // tiles of this warp's experts up to and with this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t at = base_s + upto - mine;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    const bool fits = at + mine <= cap;
+    if (!fits) report_index(status);
+    for (int64_t i = at; i < at + mine && i < cap; ++i)
+      tiles[i] = fits ? Tile{e, first, rows, static_cast<int>(at)} : Tile{0, 0, 0, static_cast<int>(i)};
+    __syncthreads();
+    if (threadIdx.x == THREADS - 1) base_s = at + mine;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *n_tiles = static_cast<int>(base_s < cap ? base_s : cap);
+}
+
+// Block 0 builds the table; the other blocks' warps take the sorted slots in
+// turn.  A row of an fp16 copy is multiplied by the power of two that brings
+// its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
+// fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
+// and none overflows; the product's rows are multiplied by the inverse, which
+// is exact, in F32.
+template <int AT, bool BF16>
+__global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* tiles, int* n_tiles, int cap,
+                                                         const void* __restrict__ in, int64_t in_row, int in_tokens,
+                                                         int wide, uint16_t* __restrict__ x16, int64_t ld,
+                                                         float* __restrict__ unscale, uint8_t* __restrict__ live,
+                                                         int* status) {
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    build_tiles(b, bt, tiles, n_tiles, cap, status);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int step = (gridDim.x - 1) * (THREADS / 32);
+  const int total = __ldg(b.start + b.experts);
+  for (int i = (blockIdx.x - 1) * (THREADS / 32) + (threadIdx.x >> 5); i < b.slots; i += step) {
+    const int s = __ldg(b.order + i);
+    const bool ok = static_cast<unsigned>(s) < static_cast<unsigned>(b.slots);
+    if (lane == 0) {
+      if (!ok) report_index(status);
+      else if (live != nullptr) live[s] = i < total;
+    }
+    if (x16 == nullptr || i >= total) continue;
+    uint16_t* to = x16 + i * ld;
+    const int64_t row = ok ? (in_tokens ? s / b.per_token : s) : 0;
+    const char* from = static_cast<const char*>(in) + row * in_row * act_bytes(AT);
+    float mul = 1.0f;
+    if constexpr (!BF16) {
+      float top = 0.0f;
+      for (int c = 8 * lane; c < wide; c += 256) {
+        float v[8];
+        load_act8<AT>(from, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // top in 2^(e - 127) .. 2^(e - 126); rows of zeros, and those with an infinity, stay as they are
+      const int e = static_cast<int>(__float_as_uint(top) >> 23);
+      const int shift = top == 0.0f || e == 255 ? 0 : min(141 - e, 120);
+      mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      if (lane == 0) unscale[i] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+    }
+    for (int c = 8 * lane; c < wide; c += 256) {
+      float v[8];
+      load_act8<AT>(from, c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = ok ? v[j] * mul : 0.0f;
+      store_act8<BF16 ? RG_BF16 : RG_F16>(to, c, v);
+    }
+  }
+}
+
+template <int AT>
+__global__ void __launch_bounds__(THREADS) join_kernel(const float* rows, int64_t groups, int64_t total,
+                                                       const uint8_t* live, int per_token,
+                                                       const float* __restrict__ weights, void* __restrict__ out,
+                                                       int64_t out_row, float beta) {
+  pdl_wait();  // the rows come from the kernel before this one
+  const int64_t width = groups * 8;
+  for (int64_t g = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x; g < total;
+       g += static_cast<int64_t>(gridDim.x) * THREADS) {
+    const int64_t t = g / groups, c = (g - t * groups) * 8;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int j = 0; j < per_token; ++j) {
+      const int64_t s = t * per_token + j;
+      if (!__ldcg(live + s)) continue;
+      const float w = weights != nullptr ? __ldg(weights + s) : 1.0f;
+      float v[8];
+      const float4* p = reinterpret_cast<const float4*>(rows + s * width + c);
+      const float4 a = __ldcg(p), b = __ldcg(p + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+    }
+    char* to = static_cast<char*>(out) + t * out_row * act_bytes(AT);
+    if (beta != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(beta, load_act(to, AT, c + i), sum[i]);
+    }
+    store_act8<AT>(to, c, sum);
+  }
+}
+
+// A tile of 64 slots by 64 outputs; 32 contraction values a step, each thread
+// 4 x 4 sums.  F32 values of W decoded exactly, F32 products and sums.
+template <int WT, bool FWD>
+__global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* __restrict__ W, int64_t N, int64_t K,
+                                                       int64_t rb, const void* __restrict__ in, int64_t in_row,
+                                                       int in_tokens, int atype) {
+  __shared__ float sx[32][kSimtTile + 4];  // [contraction][slot]
+  __shared__ float sw[32][kSimtTile + 4];  // [contraction][output]
+  __shared__ int s_slot[kSimtTile];
+  pdl_wait();  // the table comes from the kernel before this one
+  if (static_cast<int>(blockIdx.x) >= __ldcg(g.n_tiles)) return;
+  const int4 tile = __ldcg(reinterpret_cast<const int4*>(g.tiles) + blockIdx.x);
+  const int pos = tile.y + (static_cast<int>(blockIdx.x) - tile.w) * kSimtTile;
+  const int rows = min(kSimtTile, tile.y + tile.z - pos);
+  const int64_t out_w = FWD ? N : K, wide = FWD ? K : N;
+  const int64_t o0 = static_cast<int64_t>(blockIdx.y) * kSimtTile;
+  const uint8_t* we = W + tile.x * N * rb;
+  const int tid = threadIdx.x;
+  if (tid < kSimtTile) {
+    int s = tid < rows ? __ldg(g.order + pos + tid) : -1;
+    if (static_cast<unsigned>(s) >= static_cast<unsigned>(g.slots)) s = -1;
+    s_slot[tid] = s;
+  }
+  __syncthreads();
+  float acc[4][4] = {};
+  const int tx = tid & 15, ty = tid >> 4;  // outputs 4 tx .., slots 4 ty ..
+  for (int64_t c0 = 0; c0 < wide; c0 += 32) {
+    {
+      // eight values of one slot's row
+      const int r = tid >> 2, cc = 8 * (tid & 3);
+      const int s = s_slot[r];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v = 0.0f;
+        if (s >= 0 && c0 + cc + i < wide)
+          v = load_act(static_cast<const char*>(in) + static_cast<int64_t>(in_tokens ? s / g.per_token : s) * in_row *
+                                                          act_bytes(atype),
+                       atype, c0 + cc + i);
+        sx[cc + i][r] = v;
+      }
+    }
+    {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if constexpr (FWD) {
+        const int n = tid >> 2, cc = 8 * (tid & 3);
+        if (o0 + n < N && c0 + cc < K) decode8_f32<WT>(we + (o0 + n) * rb, static_cast<int>(c0) + cc, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sw[cc + i][n] = v[i];
+      } else {
+        const int n = tid >> 3, kk = 8 * (tid & 7);
+        if (c0 + n < N && o0 + kk < K) decode8_f32<WT>(we + (c0 + n) * rb, static_cast<int>(o0) + kk, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sw[n][kk + i] = v[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int c = 0; c < 32; ++c) {
+      float x[4], w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = sx[c][4 * ty + i], w[i] = sw[c][4 * tx + i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int s = s_slot[4 * ty + i];
+    if (s < 0) continue;
+    const float m = g.weights != nullptr ? __ldg(g.weights + s) : 1.0f;
+    char* to = static_cast<char*>(g.out) + static_cast<int64_t>(s / g.out_div) * g.out_row * act_bytes(g.otype);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t o = o0 + 4 * tx + j;
+      if (o >= out_w) continue;
+      float v = acc[i][j] * m;
+      if (g.beta != 0.0f) v = fmaf(g.beta, load_act(to, g.otype, o), v);
+      store_act(to, g.otype, o, v);
+    }
+  }
+}
+
+template <class F>
+cudaError_t with_atype(int atype, F&& f) {
+  switch (atype) {
+    case RG_F32: return f(std::integral_constant<int, RG_F32>{});
+    case RG_F16: return f(std::integral_constant<int, RG_F16>{});
+    default: return f(std::integral_constant<int, RG_BF16>{});
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, const Product& p, bool bf16,
+                          uint16_t* x16, int64_t ld, float* unscale, uint8_t* live, const DevInfo& dev,
+                          cudaStream_t stream) {
+  const int64_t blocks = x16 == nullptr && live == nullptr
+                             ? 0
+                             : std::min<int64_t>((b.slots + THREADS / 32 - 1) / (THREADS / 32), dev.num_sms * 8);
+  return with_atype(p.atype, [&](auto at) {
+    constexpr int AT = decltype(at)::value;
+    auto kern = bf16 ? gather_kernel<AT, true> : gather_kernel<AT, false>;
+    kern<<<static_cast<unsigned>(1 + blocks), THREADS, 0, stream>>>(
+        b, bt, tiles, n_tiles, cap, p.in, p.in_row, p.in_tokens ? 1 : 0, static_cast<int>(p.wide()), x16, ld, unscale,
+        live, dev.status);
+    return counted(cudaGetLastError());
+  });
+}
+
+cudaError_t launch_join(const float* rows, int64_t width, const uint8_t* live, const Batch& b, const Product& p,
+                        const DevInfo& dev, cudaStream_t stream) {
+  const int64_t groups = width / 8, total = static_cast<int64_t>(b.slots / b.per_token) * groups;
+  return with_atype(p.atype, [&](auto at) {
+    constexpr int AT = decltype(at)::value;
+    return counted(launch_after_prev(join_kernel<AT>, dim3(static_cast<unsigned>(grid_for(total, THREADS, dev))),
+                                     dim3(THREADS), stream, rows, groups, total, live, b.per_token, p.weights, p.out,
+                                     p.out_row, p.beta));
+  });
+}
+
+cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int cap, const DevInfo& dev,
+                        cudaStream_t stream) {
+  (void)b;
+  (void)dev;
+  const int64_t rb = p.K / block_values(p.wtype) * block_bytes(p.wtype);
+  const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;
+  if (gy > 65535) return cudaErrorInvalidConfiguration;
+  return with_wtype(p.wtype, cudaErrorInvalidValue, [&](auto wt) {
+    constexpr int WT = decltype(wt)::value;
+    auto kern = p.fwd ? simt_kernel<WT, true> : simt_kernel<WT, false>;
+    return counted(launch_after_prev(kern, dim3(static_cast<unsigned>(cap), static_cast<unsigned>(gy)), dim3(THREADS),
+                                     stream, s, static_cast<const uint8_t*>(p.W), p.N, p.K, rb, p.in, p.in_row,
+                                     p.in_tokens ? 1 : 0, p.atype));
+  });
+}
+
+}  // namespace id
+}  // namespace rg

@@ -1,0 +1,359 @@
+// rg_id_api.cu - the C ABI of the indexed calls: argument checks and
+// workspaces.
+#include <algorithm>
+
+#include "rg_id_launch.h"
+#include "rg_internal.cuh"
+
+using namespace rg;
+
+namespace {
+
+constexpr int64_t kMaxDim = 2147483647;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool valid_act(int t) { return t == RG_F32 || t == RG_F16 || t == RG_BF16; }
+bool finite(float x) { return x - x == 0.0f; }
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? RG_OK : RG_ERR_CUDA; }
+
+// Rows of `width` values of an activation type, `row` apart: 16-byte aligned.
+int check_rows(const void* p, int64_t row, int64_t width, int atype) {
+  if (!p || row < width) return RG_ERR_ARG;
+  if (!aligned(p, 16) || row % (atype == RG_F32 ? 4 : 8)) return RG_ERR_ALIGN;
+  return RG_OK;
+}
+
+// A weight of rows of K values (and how many rows): types, sizes and shapes.
+int check_weight(int wtype, int64_t N, int64_t K) {
+  if (!valid_wtype(wtype)) return RG_ERR_TYPE;
+  if (N < 0 || K < 0 || N > kMaxDim || K > kMaxDim) return RG_ERR_ARG;
+  return K % (is_quant(wtype) ? 256 : 8) ? RG_ERR_SHAPE : RG_OK;
+}
+
+// Memory from the library's pool for one call, or the caller's.
+struct Work {
+  void* p = nullptr;
+  bool own = false;
+  cudaStream_t stream = nullptr;
+  int take(size_t need, void* ws, size_t ws_bytes, bool own_ws, const DevInfo& dev, cudaStream_t s) {
+    stream = s;
+    if (!own_ws) {
+      if (need && (!ws || ws_bytes < need)) return RG_ERR_ARG;
+      if (!aligned(ws, 256)) return RG_ERR_ALIGN;
+      p = ws;
+      return RG_OK;
+    }
+    if (!need) return RG_OK;
+    cudaMemPool_t pool{};
+    const int st = pool_for(dev.device, &pool);
+    if (st != RG_OK) return st;
+    if (cudaMallocFromPoolAsync(&p, need, pool, s) != cudaSuccess) return RG_ERR_CUDA;
+    own = true;
+    return RG_OK;
+  }
+  int done(cudaError_t e) {
+    if (own) {
+      const cudaError_t f = cudaFreeAsync(p, stream);
+      if (e == cudaSuccess) e = f;
+    }
+    return from_cuda(e);
+  }
+};
+
+// --- products by slot ---
+
+int check_batch(const rg_id_batch* x, id::Batch* b) {
+  if (!x) return RG_ERR_ARG;
+  if (x->experts < 0 || x->per_token < 1 || x->slots < 0 || x->slots > kMaxDim) return RG_ERR_ARG;
+  if (x->experts > id::kMaxExperts || x->slots % x->per_token) return RG_ERR_SHAPE;
+  b->experts = x->experts;
+  b->per_token = x->per_token;
+  b->slots = static_cast<int>(x->slots);
+  b->start = x->start;
+  b->order = x->order;
+  return RG_OK;
+}
+
+// The rows of W start at multiples of 16 bytes, which TMA needs.
+bool aligned_rows(int wtype, int64_t K) {
+  return (K / block_values(wtype) * block_bytes(wtype)) % 16 == 0;
+}
+
+struct Plan {
+  bool simt;
+  int cg, bt, cap;
+  bool joined;    // rows of `out` are the tokens'
+  bool bf16;
+  size_t tiles, count, x16, unscale, live, rows, total;  // offsets, and the bytes of all
+};
+
+Plan plan(const id::Product& p, const id::Batch& b) {
+  Plan r{};
+  r.simt = p.wtype == RG_F32 || !aligned_rows(p.wtype, p.K);
+  r.cg = b.slots > 128 * static_cast<int64_t>(b.experts) ? 2 : 1;
+  r.bt = r.simt ? id::kSimtTile : 128 * r.cg;
+  r.cap = static_cast<int>(id::max_tiles(b.slots, b.experts, r.bt));
+  r.joined = p.out_tokens;
+  r.bf16 = p.wtype == RG_BF16;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t o = at;
+    at += static_cast<size_t>(id::up256(bytes));
+    return o;
+  };
+  const int64_t slots = b.slots;
+  r.tiles = take(static_cast<int64_t>(sizeof(id::Tile)) * r.cap);
+  r.count = take(4);
+  r.x16 = take(r.simt ? 0 : slots * p.wide() * 2);
+  r.unscale = take(r.simt || r.bf16 ? 0 : slots * 4);
+  r.live = take(r.joined ? slots : 0);
+  r.rows = take(r.joined ? slots * p.out_w() * 4 : 0);
+  r.total = at;
+  return r;
+}
+
+cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void* ws, const DevInfo& dev,
+                   cudaStream_t stream) {
+  char* base = static_cast<char*>(ws);
+  id::Tile* tiles = reinterpret_cast<id::Tile*>(base + r.tiles);
+  int* count = reinterpret_cast<int*>(base + r.count);
+  uint16_t* x16 = r.simt ? nullptr : reinterpret_cast<uint16_t*>(base + r.x16);
+  float* unscale = r.simt || r.bf16 ? nullptr : reinterpret_cast<float*>(base + r.unscale);
+  uint8_t* live = r.joined ? reinterpret_cast<uint8_t*>(base + r.live) : nullptr;
+  float* rows = reinterpret_cast<float*>(base + r.rows);
+  cudaError_t e = id::launch_gather(b, r.bt, tiles, count, r.cap, p, r.bf16, x16, p.wide(), unscale, live, dev, stream);
+  if (e != cudaSuccess) return e;
+  id::Slots s{};
+  s.tiles = tiles;
+  s.n_tiles = count;
+  s.order = b.order;
+  s.slots = b.slots;
+  s.per_token = b.per_token;
+  s.unscale = unscale;
+  s.weights = r.joined ? nullptr : p.weights;
+  s.out = r.joined ? rows : p.out;
+  s.out_row = r.joined ? p.out_w() : p.out_row;
+  s.otype = r.joined ? RG_F32 : p.atype;
+  s.out_div = 1;
+  s.beta = r.joined ? 0.0f : p.beta;
+  if (r.simt)
+    e = id::launch_simt(p, b, s, r.cap, dev, stream);
+  else
+    e = (p.fwd ? id::launch_mm_id : id::launch_tc_id)(p.wtype, p.W, b.experts, p.N, p.K, x16, p.wide(), s, r.cg, dev,
+                                                      stream);
+  if (e == cudaSuccess && r.joined) e = id::launch_join(rows, p.out_w(), live, b, p, dev, stream);
+  return e;
+}
+
+// Everything but the pointers, as the workspace query has it too.
+int check_shape(bool fwd, int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int out_of, id::Batch* b,
+                id::Product* p) {
+  int st = check_batch(batch, b);
+  if (st != RG_OK || (st = check_weight(wtype, N, K)) != RG_OK) return st;
+  if (N % 8) return RG_ERR_SHAPE;
+  if (out_of != RG_ROWS_SLOT && out_of != RG_ROWS_TOKEN) return RG_ERR_ARG;
+  p->fwd = fwd;
+  p->wtype = wtype;
+  p->N = N;
+  p->K = K;
+  p->out_tokens = out_of == RG_ROWS_TOKEN;
+  return RG_OK;
+}
+
+int product(bool fwd, int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype,
+            const void* in, int64_t in_row, int in_of, void* out, int64_t out_row, int out_of, const float* weights,
+            float beta, void* ws, size_t ws_bytes, bool own_ws, cudaStream_t stream) {
+  id::Batch b;
+  id::Product p{};
+  int st = check_shape(fwd, wtype, N, K, batch, out_of, &b, &p);
+  if (st != RG_OK) return st;
+  if (!valid_act(atype)) return RG_ERR_TYPE;
+  if (in_of != RG_ROWS_SLOT && in_of != RG_ROWS_TOKEN) return RG_ERR_ARG;
+  if (b.slots == 0 || p.out_w() == 0) return RG_OK;
+  // (no contraction, or no experts: nothing to multiply with; the rows would be beta times themselves)
+  if (p.wide() == 0 || b.experts == 0) return RG_ERR_SHAPE;
+  if (!W || !b.start || !b.order) return RG_ERR_ARG;
+  if (!aligned(W, 16) || !aligned(b.start, 4) || !aligned(b.order, 4) || !aligned(weights, 4)) return RG_ERR_ALIGN;
+  if ((st = check_rows(in, in_row, p.wide(), atype)) != RG_OK) return st;
+  if ((st = check_rows(out, out_row, p.out_w(), atype)) != RG_OK) return st;
+  DevInfo* dev = nullptr;
+  if ((st = current_dev(&dev)) != RG_OK) return st;
+  p.W = W;
+  p.atype = atype;
+  p.in = in;
+  p.in_row = in_row;
+  p.in_tokens = in_of == RG_ROWS_TOKEN;
+  p.out = out;
+  p.out_row = out_row;
+  p.weights = weights;
+  p.beta = beta;
+  const Plan r = plan(p, b);
+  Work w;
+  if ((st = w.take(r.total, ws, ws_bytes, own_ws, *dev, stream)) != RG_OK) return st;
+  return w.done(launch(p, b, r, w.p, *dev, stream));
+}
+
+size_t product_bytes(bool fwd, int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int out_of) {
+  id::Batch b;
+  id::Product p{};
+  if (check_shape(fwd, wtype, N, K, batch, out_of, &b, &p) != RG_OK || b.slots == 0 || N == 0 || K == 0 ||
+      b.experts == 0)
+    return 0;
+  return plan(p, b).total;
+}
+
+int check_route(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale) {
+  if (mode != RG_ROUTE_TOP && mode != RG_ROUTE_ALL) return RG_ERR_TYPE;
+  if (T < 0 || T > kMaxDim || experts < 1 || top < 1 || T * top > kMaxDim || !finite(scale)) return RG_ERR_ARG;
+  if (experts > id::kMaxExperts || top > id::kMaxChosen || top > experts) return RG_ERR_SHAPE;
+  if (T == 0) return RG_OK;
+  if (!logits || l_row < experts) return RG_ERR_ARG;
+  return aligned(logits, 4) ? RG_OK : RG_ERR_ALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rg_get_rows(int wtype, const void* W, int64_t N, int64_t K, const int32_t* ids, int64_t n, float scale, int atype,
+                void* out, int64_t out_row, void* stream) {
+  int st = check_weight(wtype, N, K);
+  if (st != RG_OK) return st;
+  if (!valid_act(atype)) return RG_ERR_TYPE;
+  if (n < 0 || n > kMaxDim) return RG_ERR_ARG;
+  if (n == 0 || K == 0) return RG_OK;
+  if ((N > 0 && !W) || !ids) return RG_ERR_ARG;
+  if (!aligned(W, 16) || !aligned(ids, 4)) return RG_ERR_ALIGN;
+  if ((st = check_rows(out, out_row, K, atype)) != RG_OK) return st;
+  DevInfo* dev = nullptr;
+  if ((st = current_dev(&dev)) != RG_OK) return st;
+  return from_cuda(id::launch_get_rows(wtype, W, N, K, ids, n, scale, atype, out, out_row, *dev,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t rg_get_rows_back_workspace_bytes(int64_t n, int64_t N, int64_t K) {
+  if (n < 1 || N < 1 || K < 1 || n > kMaxDim || N > kMaxDim || K > kMaxDim || K % 8) return 0;
+  return id::rows_back_workspace(n, N, K);
+}
+
+}  // extern "C"
+
+namespace {
+
+int rows_back(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int64_t n, float scale, float* G,
+              int64_t g_row, int64_t N, int64_t K, float beta, void* ws, size_t ws_bytes, bool own_ws,
+              cudaStream_t stream) {
+  if (!valid_act(atype)) return RG_ERR_TYPE;
+  if (n < 0 || N < 0 || K < 0 || n > kMaxDim || N > kMaxDim || K > kMaxDim) return RG_ERR_ARG;
+  if (K % 8) return RG_ERR_SHAPE;
+  if (N == 0 || K == 0) return RG_OK;
+  int st = check_rows(G, g_row, K, RG_F32);
+  if (st != RG_OK) return st;
+  if (n > 0) {
+    if (!ids) return RG_ERR_ARG;
+    if (!aligned(ids, 4)) return RG_ERR_ALIGN;
+    if ((st = check_rows(dY, dy_row, K, atype)) != RG_OK) return st;
+  }
+  DevInfo* dev = nullptr;
+  if ((st = current_dev(&dev)) != RG_OK) return st;
+  if (n == 0) return beta == 1.0f ? RG_OK : from_cuda(launch_scale(G, N, K, g_row, beta, *dev, stream));
+  Work w;
+  if ((st = w.take(id::rows_back_workspace(n, N, K), ws, ws_bytes, own_ws, *dev, stream)) != RG_OK) return st;
+  return w.done(id::launch_rows_back(atype, dY, dy_row, ids, n, scale, G, g_row, N, K, beta, w.p, *dev, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int rg_get_rows_back(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int64_t n, float scale, float* G,
+                     int64_t g_row, int64_t N, int64_t K, float beta, void* stream) {
+  return rows_back(atype, dY, dy_row, ids, n, scale, G, g_row, N, K, beta, nullptr, 0, true,
+                   static_cast<cudaStream_t>(stream));
+}
+
+int rg_get_rows_back_ws(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int64_t n, float scale, float* G,
+                        int64_t g_row, int64_t N, int64_t K, float beta, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  return rows_back(atype, dY, dy_row, ids, n, scale, G, g_row, N, K, beta, workspace, workspace_bytes, false,
+                   static_cast<cudaStream_t>(stream));
+}
+
+int rg_group(const int32_t* ids, int64_t n, int groups, int32_t* start, int32_t* order, void* stream) {
+  if (n < 0 || n > kMaxDim || groups < 1) return RG_ERR_ARG;
+  if (groups > id::kMaxExperts) return RG_ERR_SHAPE;
+  if (!start || (n > 0 && (!ids || !order))) return RG_ERR_ARG;
+  if (!aligned(ids, 4) || !aligned(start, 4) || !aligned(order, 4)) return RG_ERR_ALIGN;
+  DevInfo* dev = nullptr;
+  const int st = current_dev(&dev);
+  if (st != RG_OK) return st;
+  return from_cuda(
+      id::launch_sort(ids, n, groups, start, order, nullptr, nullptr, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int rg_route(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale, int32_t* ids,
+             float* weights, int32_t* start, int32_t* order, void* stream) {
+  int st = check_route(logits, l_row, T, experts, top, mode, scale);
+  if (st != RG_OK) return st;
+  if (T > 0 && (!ids || !weights || !start != !order)) return RG_ERR_ARG;
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(start, 4) || !aligned(order, 4)) return RG_ERR_ALIGN;
+  if (T == 0 && !start) return RG_OK;
+  DevInfo* dev = nullptr;
+  if ((st = current_dev(&dev)) != RG_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (T > 0) e = id::launch_route(logits, l_row, T, experts, top, mode, scale, ids, weights, *dev, s);
+  if (e == cudaSuccess && start)
+    e = id::launch_sort(ids, T * top, experts, start, order, nullptr, nullptr, *dev, s);
+  return from_cuda(e);
+}
+
+int rg_route_back(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale,
+                  const int32_t* ids, const float* dweights, float* dlogits, int64_t dl_row, void* stream) {
+  int st = check_route(logits, l_row, T, experts, top, mode, scale);
+  if (st != RG_OK || T == 0) return st;
+  if (!ids || !dweights || !dlogits || dl_row < experts) return RG_ERR_ARG;
+  if (!aligned(ids, 4) || !aligned(dweights, 4) || !aligned(dlogits, 4)) return RG_ERR_ALIGN;
+  DevInfo* dev = nullptr;
+  if ((st = current_dev(&dev)) != RG_OK) return st;
+  return from_cuda(id::launch_route_back(logits, l_row, T, experts, top, mode, scale, ids, dweights, dlogits, dl_row,
+                                         *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int rg_mul_mat_id(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* X,
+                  int64_t x_row, int x_of, void* Y, int64_t y_row, int y_of, const float* weights, float beta,
+                  void* stream) {
+  return product(true, wtype, W, N, K, batch, atype, X, x_row, x_of, Y, y_row, y_of, weights, beta, nullptr, 0, true,
+                 static_cast<cudaStream_t>(stream));
+}
+
+int rg_mul_mat_id_ws(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* X,
+                     int64_t x_row, int x_of, void* Y, int64_t y_row, int y_of, const float* weights, float beta,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return product(true, wtype, W, N, K, batch, atype, X, x_row, x_of, Y, y_row, y_of, weights, beta, workspace,
+                 workspace_bytes, false, static_cast<cudaStream_t>(stream));
+}
+
+size_t rg_mul_mat_id_workspace_bytes(int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int y_of) {
+  return product_bytes(true, wtype, N, K, batch, y_of);
+}
+
+int rg_out_prod_id(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype, const void* dY,
+                   int64_t dy_row, int dy_of, void* dX, int64_t dx_row, int dx_of, const float* weights, float beta,
+                   void* stream) {
+  return product(false, wtype, W, N, K, batch, atype, dY, dy_row, dy_of, dX, dx_row, dx_of, weights, beta, nullptr, 0,
+                 true, static_cast<cudaStream_t>(stream));
+}
+
+int rg_out_prod_id_ws(int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype,
+                      const void* dY, int64_t dy_row, int dy_of, void* dX, int64_t dx_row, int dx_of,
+                      const float* weights, float beta, void* workspace, size_t workspace_bytes, void* stream) {
+  return product(false, wtype, W, N, K, batch, atype, dY, dy_row, dy_of, dX, dx_row, dx_of, weights, beta, workspace,
+                 workspace_bytes, false, static_cast<cudaStream_t>(stream));
+}
+
+size_t rg_out_prod_id_workspace_bytes(int wtype, int64_t N, int64_t K, const rg_id_batch* batch, int dx_of) {
+  return product_bytes(false, wtype, N, K, batch, dx_of);
+}
+
+}  // extern "C"

@@ -100,11 +100,12 @@ cudaError_t launch_dequant_t16(int wtype, const void* W, int64_t N, int64_t K, b
 // that kernel writes.  A kernel before it that never triggers its
 // dependents (every kernel outside this library) is waited for as usual.
 template <class... P, class... A>
-cudaError_t launch_after_prev(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream,
-                              A&&... args) {
+cudaError_t launch_after_prev_smem(size_t smem, void (*kern)(P...), dim3 grid, dim3 block,
+                                   cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -112,6 +113,11 @@ cudaError_t launch_after_prev(void (*kern)(P...), dim3 grid, dim3 block, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_after_prev(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream,
+                              A&&... args) {
+  return launch_after_prev_smem(0, kern, grid, block, stream, std::forward<A>(args)...);
 }
 
 // Blocks of a grid-stride kernel over work_items (one per thread): enough
@@ -277,7 +283,7 @@ cudaError_t launch_wait_probe(const DevInfo& dev, unsigned long long limit_ns,
 
 // cuTensorMapEncodeTiled (resolved from the driver at first use), through a
 // small cache of recently encoded maps keyed by address, shape and device.
-// dim2 > 1: a third dimension (rows of planes stride2_bytes apart), box 1 deep.
+// dim2 > 1 or stride2_bytes: a third dimension (planes stride2_bytes apart), box 1 deep.
 CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                       uint64_t dim0, uint64_t dim1, uint64_t stride1_bytes, uint32_t box0,
                       uint32_t box1, CUtensorMapSwizzle swizzle, uint64_t dim2 = 1,

@@ -41,6 +41,7 @@
 
 #include <algorithm>
 
+#include "rg_id_launch.h"
 #include "rg_internal.cuh"
 #include "rg_launch.h"
 
@@ -1028,6 +1029,73 @@ __device__ __forceinline__ int sk_unit_of(uint32_t g, uint32_t rn, int U) {
   return static_cast<int>(((g + 1) * static_cast<uint32_t>(U) - 1) / rn);
 }
 
+// The kernel's last argument: the slots of a GRP kernel, nothing of the others.
+template <bool GRP>
+struct GrpArg {};
+template <>
+struct GrpArg<true> : id::Slots {};
+
+// Rows pos0 .. of one expert's tile (`left` of them, 32 columns of 32 lanes in
+// r: lane = output value k) to their slots' rows.
+template <class A>
+__device__ __forceinline__ void store_slots(const A& g, const uint32_t (&r)[32], int pos0, int left, int k, int K,
+                                            int lane) {
+  // lane i's row: its slot (or -1), and the factor of the row
+  int slot = -1;
+  float mul = 1.0f;
+  if (lane < left) {
+    slot = __ldg(g.order + pos0 + lane);
+    if (static_cast<unsigned>(slot) >= static_cast<unsigned>(g.slots)) slot = -1;
+    if (g.unscale != nullptr) mul = __ldcg(g.unscale + pos0 + lane);
+    if (g.weights != nullptr && slot >= 0) mul *= __ldg(g.weights + slot);
+  }
+  const int orow = slot < 0 ? -1 : slot / g.out_div;
+  if (g.otype == RG_F32) {
+    float* out = static_cast<float*>(g.out) + k;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int row = __shfl_sync(0xffffffffu, orow, i);
+      const float v = __uint_as_float(r[i]) * __shfl_sync(0xffffffffu, mul, i);
+      if (row >= 0 && k < K) {
+        float* o = out + static_cast<int64_t>(row) * g.out_row;
+        *o = g.beta != 0.0f ? fmaf(g.beta, *o, v) : v;
+      }
+    }
+    return;
+  }
+  // 16-bit rows: two lanes exchange halves of two rows, so that each stores two
+  // neighbouring values of one row (even lanes row 2i, odd lanes row 2i + 1)
+  const int odd = lane & 1;
+  uint16_t* out = static_cast<uint16_t*>(g.out) + (k & ~1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1));
+    const int row = __shfl_sync(0xffffffffu, orow, 2 * i + odd);
+    const float m = __shfl_sync(0xffffffffu, mul, 2 * i + odd);
+    float a = (odd ? other : __uint_as_float(r[2 * i])) * m;
+    float b = (odd ? __uint_as_float(r[2 * i + 1]) : other) * m;
+    if (row >= 0 && k < K) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(row) * g.out_row);
+      if (g.otype == RG_F16) {
+        if (g.beta != 0.0f) {
+          const float2 x = __half22float2(u32_as_h2(*o));
+          a = fmaf(g.beta, x.x, a);
+          b = fmaf(g.beta, x.y, b);
+        }
+        *o = h2_as_u32(__floats2half2_rn(a, b));
+      } else {
+        if (g.beta != 0.0f) {
+          const uint32_t x = *o;
+          a = fmaf(g.beta, __uint_as_float(x << 16), a);
+          b = fmaf(g.beta, __uint_as_float(x & 0xFFFF0000u), b);
+        }
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        *o = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+}
+
 // --- the kernel -----------------------------------------------------------------
 //
 // Barriers (8 bytes each, per stage s unless noted):
@@ -1041,7 +1109,13 @@ __device__ __forceinline__ int sk_unit_of(uint32_t g, uint32_t rn, int U) {
 //   acc_full[2], acc_empty[2]   the two tensor-memory accumulators
 //   drain        local: the MMAs issued so far completed (abort path)
 
-template <int WT, int CG, int BT, bool AD, bool SK, bool FWD = false>
+// GRP (products by slot): W is a stack of experts' weights (three-dimensional
+// maps, the expert the third coordinate), dY's copy holds the slots sorted by
+// expert, and a tile of t is up to BT slots of one expert, from the table that
+// the kernel before this one wrote; the epilogue stores each slot's row where
+// the slot's row of the output is.  Tiles of an expert run in the banded order,
+// experts one after another.
+template <int WT, int CG, int BT, bool AD, bool SK, bool FWD = false, bool GRP = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     out_prod_tc_kernel(const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y,
@@ -1051,9 +1125,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                        const __grid_constant__ CUtensorMap map_q, int n_main,
                        float* __restrict__ dX, int64_t ldx, float beta, int T, int K,
                        int n_kunits, int n_ttiles, int band, int n_chunks, int n_splits,
-                       float* __restrict__ part, WaitCtl ctl) {
+                       float* __restrict__ part, WaitCtl ctl, const __grid_constant__ GrpArg<GRP> grp) {
   using C = Cfg<WT, CG, BT, FWD>;
   static_assert(!FWD || (!AD && !SK), "the forward runs without an adapter or stream-K");
+  static_assert(!GRP || (!AD && !SK), "products by slot run without an adapter or stream-K");
   constexpr int S = C::S;
   extern __shared__ uint8_t smem_raw[];
   // align inside the shared window (pointer arithmetic keeps the shared space)
@@ -1085,8 +1160,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // adapter's: their A rows are its dense 16-bit rows (map_l) and their B
   // columns its projected dY, which sit after dY's own columns in the same
   // 16-bit copy.  Without one (AD false) map_l and n_main are not read.
-  const int n_tiles = n_kunits * n_ttiles * n_splits;
-  const int n_tiles1 = n_kunits * n_ttiles;
+  int n_tiles = n_kunits * n_ttiles * n_splits;
+  int n_tiles1 = n_kunits * n_ttiles;
 
   auto wait_any = [&](uint32_t bar, uint32_t parity) {
     if constexpr (CG == 2)
@@ -1134,6 +1209,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // tile -> (k unit, t tile): bands of `band` k units; inside a band the t
   // tiles run outer, so the band's slice of W stays in L2 while every t tile
   // of dY passes by once per band
+  // GRP: the tile's expert, its slots' place in the sorted order and their number
+  struct SlotTile {
+    int expert, pos, rows;
+  };
+  auto coords_grp = [&](int item, int& ku) -> SlotTile {
+    SlotTile st{0, 0, 0};
+    if constexpr (GRP) {
+      const int4 x = __ldcg(reinterpret_cast<const int4*>(grp.tiles) + item / n_kunits);
+      const int ntl = max(1, x.z / BT + (x.z % BT != 0));  // the expert's tiles (an empty tile: one)
+      const int r = item - x.w * n_kunits, per_band = band * ntl, b = r / per_band, rr = r - b * per_band;
+      const int gk = min(band, n_kunits - b * band);
+      const int t = rr / gk;
+      ku = b * band + (rr - t * gk);
+      st = SlotTile{x.x, x.y + t * BT, min(BT, x.z - t * BT)};
+    }
+    return st;
+  };
   auto coords = [&](int item, int& ku, int& tt) {
     const int tile = item % n_tiles1;
     const int per_band = band * n_ttiles;
@@ -1142,6 +1234,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tt = r / gk;
     ku = b * band + (r - tt * gk);
   };
+
+  if constexpr (GRP) {
+    // the table comes from the kernel before this one (read past the wait: __ldcg, since a
+    // load that counts as constant for the kernel's life may be moved before it)
+    pdl_wait();
+    n_tiles = n_tiles1 = __ldcg(grp.n_tiles) * n_kunits;
+  }
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -1158,11 +1257,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Segs<SK> sg(unit, n_units, n_tiles, n_chunks);
     int tile = 0, c0 = 0, c1 = 0;
     while (ok && sg.next(tile, c0, c1)) {
-      int ku, tt;
-      coords(tile, ku, tt);
-      const int cbase = (tile / n_tiles1) * n_chunks;  // first contraction chunk of the split
+      int ku, tt = 0;
+      SlotTile st{};
+      if constexpr (GRP) st = coords_grp(tile, ku);
+      else coords(tile, ku, tt);
+      const int cbase = GRP ? 0 : (tile / n_tiles1) * n_chunks;  // first contraction chunk of the split
       const int kt = ku * CG + static_cast<int>(rank);
-      const int ty = tt * BT + static_cast<int>(rank) * B_ROWS;
+      const int ty = (GRP ? st.pos : tt * BT) + static_cast<int>(rank) * B_ROWS;
+      // W's boxes: of the stack's expert (GRP), or of the one matrix
+      auto load_w = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+        if constexpr (GRP) tma_load_3d(dst, map, bar, x, y, st.expert);
+        else tma_load_2d(dst, map, bar, x, y);
+      };
+      auto load_w_pair = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+        if constexpr (GRP) tma_load_3d_pair(dst, map, bar, x, y, st.expert);
+        else tma_load_2d_pair(dst, map, bar, x, y);
+      };
       for (int c = c0; c < c1; ++c) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ph ^ 1u, ctl, abort_flag));
         if (!ok) break;
@@ -1179,25 +1289,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if constexpr (FWD && WT == RG_Q4_K) {
                 // the super-block headers, then the chunk's nibbles (map_l), 128 rows each
                 const int sb = (gc >> 2) * 144;
-                tma_load_2d(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), sb / 4, kt * BM);
-                tma_load_2d(smem_addr(sP + s * C::P_STAGE) + 128 * 16, &map_l, full_p(s),
+                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), sb / 4, kt * BM);
+                load_w(smem_addr(sP + s * C::P_STAGE) + 128 * 16, &map_l, full_p(s),
                             (sb + 16 + 32 * (gc & 3)) / 4, kt * BM);
               } else if constexpr (FWD && WT == RG_Q6_K) {
                 // the half's low bits, its high bits, the scales and d (three
                 // windows, 128 rows each, one region of the stage apiece)
                 const int sb = (gc >> 2) * 210, h = (gc >> 1) & 1;
                 const uint32_t dst = smem_addr(sP + s * C::P_STAGE);
-                tma_load_2d(dst, &map_w, full_p(s), ((sb + 64 * h) & ~15) / 4, kt * BM);
-                tma_load_2d(dst + 128 * Q6F_A, &map_l, full_p(s), ((sb + 128 + 32 * h) & ~15) / 4, kt * BM);
-                tma_load_2d(dst + 128 * (Q6F_A + Q6F_H), &map_q, full_p(s), ((sb + 192) & ~15) / 4, kt * BM);
+                load_w(dst, &map_w, full_p(s), ((sb + 64 * h) & ~15) / 4, kt * BM);
+                load_w(dst + 128 * Q6F_A, &map_l, full_p(s), ((sb + 128 + 32 * h) & ~15) / 4, kt * BM);
+                load_w(dst + 128 * (Q6F_A + Q6F_H), &map_q, full_p(s), ((sb + 192) & ~15) / 4, kt * BM);
               } else if constexpr (FWD && WT == RG_Q8_0) {  // the chunk's two blocks
-                tma_load_2d(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), ((gc * 68) & ~15) / 4,
+                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), ((gc * 68) & ~15) / 4,
                             kt * BM);
               } else if constexpr (FWD) {  // the window of the 128-value tile holding chunk gc
-                tma_load_2d(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
+                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
                             p_window_start<WT>(gc >> 1) / 4, kt * BM);
               } else
-                tma_load_2d(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
+                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
                             p_window_start<WT>(kt) / 4, gc * BC);
               pend_p |= 1u << s;
             } else {
@@ -1205,15 +1315,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if constexpr (FWD) {
                 // 64 values of 128 rows: the K-major, 128-byte swizzled operand itself
                 if constexpr (CG == 2)
-                  tma_load_2d_pair(a_dst, &map_w, abar, gc * BC, kt * BM);
+                  load_w_pair(a_dst, &map_w, abar, gc * BC, kt * BM);
                 else
-                  tma_load_2d(a_dst, &map_w, abar, gc * BC, kt * BM);
+                  load_w(a_dst, &map_w, abar, gc * BC, kt * BM);
               } else if constexpr (CG == 2) {
-                tma_load_2d_pair(a_dst, &map_w, abar, kt * BM, gc * BC);
-                tma_load_2d_pair(a_dst + A_COLBLK, &map_w, abar, kt * BM + 64, gc * BC);
+                load_w_pair(a_dst, &map_w, abar, kt * BM, gc * BC);
+                load_w_pair(a_dst + A_COLBLK, &map_w, abar, kt * BM + 64, gc * BC);
               } else {
-                tma_load_2d(a_dst, &map_w, abar, kt * BM, gc * BC);
-                tma_load_2d(a_dst + A_COLBLK, &map_w, abar, kt * BM + 64, gc * BC);
+                load_w(a_dst, &map_w, abar, kt * BM, gc * BC);
+                load_w(a_dst + A_COLBLK, &map_w, abar, kt * BM + 64, gc * BC);
               }
             }
           } else {
@@ -1366,7 +1476,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             continue;
           }
           int ku, tt;
-          coords(tile, ku, tt);
+          if constexpr (GRP) {
+            // (one band: the k units run fastest, no table needed)
+            if (band == n_kunits) ku = tile % n_kunits;
+            else (void)coords_grp(tile, ku);
+          } else {
+            coords(tile, ku, tt);
+          }
           const int kt = ku * CG + static_cast<int>(rank);
           // chunks of this item from c_ad on are the adapter's (TMA fills A)
           int c_ad = 0;
@@ -1379,7 +1495,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if constexpr (FWD) {
               // chunk gf: values 64 gf .. 64 gf + 63 of this CTA's 128 rows of W
-              const int gf = (tile / n_tiles1) * n_chunks + cc;
+              const int gf = GRP ? cc : (tile / n_tiles1) * n_chunks + cc;
               decode_fwd_stage<WT>(sP + s * C::P_STAGE, sA + s * A_STAGE, lane, part, gf >> 1, gf & 1);
             } else if (AD && cc >= c_ad) {
               // nothing to decode
@@ -1441,8 +1557,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Segs<SK> sg(unit, n_units, n_tiles, n_chunks);
     int tile = 0, c0 = 0, c1 = 0;
     for (int j = 0; ok && sg.next(tile, c0, c1); ++j) {
-      int ku, tt;
-      coords(tile, ku, tt);
+      int ku, tt = 0;
+      SlotTile st{};
+      if constexpr (GRP) st = coords_grp(tile, ku);
+      else coords(tile, ku, tt);
       const int kt = ku * CG + static_cast<int>(rank);
       const int a = j & 1;
       const uint32_t aph = (static_cast<uint32_t>(j) >> 1) & 1u;
@@ -1451,7 +1569,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const int k = kt * BM + 32 * eq + lane;
       const bool kin = k < K;
-      if (!SK || c0 == 0) {
+      if constexpr (GRP) {
+#pragma unroll 1
+        for (int cb = 0; cb < BT / 32 && 32 * cb < st.rows; ++cb) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(32 * eq) << 16) +
+                                 static_cast<uint32_t>(a * BT + 32 * cb),
+                             r);
+          store_slots(grp, r, st.pos + 32 * cb, st.rows - 32 * cb, k, K, lane);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(empty_leader + 8u * a);
+          else
+            mbar_arrive(acc_empty(a));
+        }
+      } else if (!SK || c0 == 0) {
         // a whole item, or the first piece of a shared tile (the second
         // kernel adds the others to it): straight to dX (or to its split's slab)
         float* out = split_part ? split_part + static_cast<int64_t>(tile / n_tiles1) * T * K : dX;
@@ -1619,7 +1754,7 @@ static cudaError_t launch_tc_t(const CUtensorMap& mw, const CUtensorMap& my,
   cfg.gridDim = dim3(static_cast<unsigned>(units * CG), 1, 1);
   if (SK && part == nullptr) return cudaErrorInvalidValue;
   e = counted(cudaLaunchKernelEx(&cfg, kern, mw, my, ml, mx, mp, mq, n_main, dX, ldx, beta, T, K, p.n_kunits,
-                                 p.n_ttiles, p.band, p.n_chunks, p.n_splits, part, ctl));
+                                 p.n_ttiles, p.band, p.n_chunks, p.n_splits, part, ctl, tc::GrpArg<false>{}));
   if (e != cudaSuccess || !SK) return e;
   // stream-K: the shared tiles' pieces, added in chunk order (the same unit
   // count as the launch: the pieces' slabs follow from it)
