@@ -32,6 +32,29 @@ __device__ __forceinline__ void load_act8(const void* row, int64_t at, float (&v
   }
 }
 
+// Four values of a row, 8-byte aligned (16 for F32).
+template <int AT>
+__device__ __forceinline__ void load_act4(const void* row, int64_t at, float (&v)[4]) {
+  if constexpr (AT == RG_F32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + at));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  } else {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + at));
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (AT == RG_BF16) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
 // Two values to the 16 bits of a type, the first in the low half.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {

@@ -301,11 +301,8 @@ int rg_route(const float* logits, int64_t l_row, int64_t T, int experts, int top
   DevInfo* dev = nullptr;
   if ((st = current_dev(&dev)) != RG_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (T > 0) e = id::launch_route(logits, l_row, T, experts, top, mode, scale, ids, weights, *dev, s);
-  if (e == cudaSuccess && start)
-    e = id::launch_sort(ids, T * top, experts, start, order, nullptr, nullptr, *dev, s);
-  return from_cuda(e);
+  if (T == 0) return from_cuda(id::launch_sort(nullptr, 0, experts, start, order, nullptr, nullptr, *dev, s));
+  return from_cuda(id::launch_route(logits, l_row, T, experts, top, mode, scale, ids, weights, start, order, *dev, s));
 }
 
 int rg_route_back(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale,

@@ -20,9 +20,11 @@ cudaError_t launch_get_rows(int wtype, const void* W, int64_t N, int64_t K, cons
 // or out of range, which is reported) behind the others; sorted (may be NULL):
 // the ids in that order, `groups` where there is none; start (may be NULL, only
 // for groups <= kMaxExperts): where each group begins, and where the last ends.
+// after_prev: the launch may overlap the kernel before it (it waits for its end).
 size_t sort_workspace(int64_t n, int64_t groups);
 cudaError_t launch_sort(const int32_t* ids, int64_t n, int64_t groups, int32_t* start, int32_t* order,
-                        int32_t* sorted, void* ws, const DevInfo& dev, cudaStream_t stream);
+                        int32_t* sorted, void* ws, const DevInfo& dev, cudaStream_t stream,
+                        bool after_prev = true);
 
 // G[r, :] = beta * G[r, :] + scale * sum of dY's rows whose id is r.
 size_t rows_back_workspace(int64_t n, int64_t N, int64_t K);
@@ -33,8 +35,10 @@ cudaError_t launch_rows_back(int atype, const void* dY, int64_t dy_row, const in
 // --- the router (rg_route.cu) ---
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChosen = 32;
+// (start and order: both NULL, or what launch_sort gives for ids)
 cudaError_t launch_route(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode, float scale,
-                         int32_t* ids, float* weights, const DevInfo& dev, cudaStream_t stream);
+                         int32_t* ids, float* weights, int32_t* start, int32_t* order, const DevInfo& dev,
+                         cudaStream_t stream);
 cudaError_t launch_route_back(const float* logits, int64_t l_row, int64_t T, int experts, int top, int mode,
                               float scale, const int32_t* ids, const float* dweights, float* dlogits, int64_t dl_row,
                               const DevInfo& dev, cudaStream_t stream);
