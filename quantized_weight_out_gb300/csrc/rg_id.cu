@@ -95,9 +95,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // top in 2^(e - 127) .. 2^(e - 126); rows of zeros, and those with an infinity, stay as they are
-      const int e = static_cast<int>(__float_as_uint(top) >> 23);
-      const int shift = top == 0.0f || e == 255 ? 0 : min(141 - e, 120);
+      const int shift = row_shift(top);
       mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
       if (lane == 0) unscale[i] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
     }

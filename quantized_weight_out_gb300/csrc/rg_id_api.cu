@@ -80,16 +80,21 @@ bool aligned_rows(int wtype, int64_t K) {
 }
 
 struct Plan {
-  bool simt;
+  bool simt, few;
   int cg, bt, cap;
   bool joined;    // rows of `out` are the tokens'
   bool bf16;
   size_t tiles, count, x16, unscale, live, rows, total;  // offsets, and the bytes of all
 };
 
+// Slots an expert on average up to which the streaming kernel runs.
+constexpr int64_t kFewSlots = 8;
+
 Plan plan(const id::Product& p, const id::Batch& b) {
   Plan r{};
   r.simt = p.wtype == RG_F32 || !aligned_rows(p.wtype, p.K);
+  // a few slots an expert: W's rows streamed once; else tiles of 128 or 256 slots
+  r.few = !r.simt && b.slots <= kFewSlots * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
   r.cg = b.slots > 128 * static_cast<int64_t>(b.experts) ? 2 : 1;
   r.bt = r.simt ? id::kSimtTile : 128 * r.cg;
   r.cap = static_cast<int>(id::max_tiles(b.slots, b.experts, r.bt));
@@ -102,10 +107,10 @@ Plan plan(const id::Product& p, const id::Batch& b) {
     return o;
   };
   const int64_t slots = b.slots;
-  r.tiles = take(static_cast<int64_t>(sizeof(id::Tile)) * r.cap);
-  r.count = take(4);
-  r.x16 = take(r.simt ? 0 : slots * p.wide() * 2);
-  r.unscale = take(r.simt || r.bf16 ? 0 : slots * 4);
+  r.tiles = take(r.few ? 0 : static_cast<int64_t>(sizeof(id::Tile)) * r.cap);
+  r.count = take(r.few ? 0 : 4);
+  r.x16 = take(r.simt || r.few ? 0 : slots * p.wide() * 2);
+  r.unscale = take(r.simt || r.few || r.bf16 ? 0 : slots * 4);
   r.live = take(r.joined ? slots : 0);
   r.rows = take(r.joined ? slots * p.out_w() * 4 : 0);
   r.total = at;
@@ -121,8 +126,6 @@ cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void
   float* unscale = r.simt || r.bf16 ? nullptr : reinterpret_cast<float*>(base + r.unscale);
   uint8_t* live = r.joined ? reinterpret_cast<uint8_t*>(base + r.live) : nullptr;
   float* rows = reinterpret_cast<float*>(base + r.rows);
-  cudaError_t e = id::launch_gather(b, r.bt, tiles, count, r.cap, p, r.bf16, x16, p.wide(), unscale, live, dev, stream);
-  if (e != cudaSuccess) return e;
   id::Slots s{};
   s.tiles = tiles;
   s.n_tiles = count;
@@ -136,6 +139,14 @@ cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void
   s.otype = r.joined ? RG_F32 : p.atype;
   s.out_div = 1;
   s.beta = r.joined ? 0.0f : p.beta;
+  cudaError_t e = cudaSuccess;
+  if (r.few) {
+    e = id::launch_few(p, b, s, live, dev, stream);
+    if (e == cudaSuccess && r.joined) e = id::launch_join(rows, p.out_w(), live, b, p, dev, stream);
+    return e;
+  }
+  e = id::launch_gather(b, r.bt, tiles, count, r.cap, p, r.bf16, x16, p.wide(), unscale, live, dev, stream);
+  if (e != cudaSuccess) return e;
   if (r.simt)
     e = id::launch_simt(p, b, s, r.cap, dev, stream);
   else

@@ -110,6 +110,12 @@ cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int ca
                         cudaStream_t stream);
 constexpr int kSimtTile = 64;
 
+// rg_id_few.cu: the forward for a few slots an expert; whether a batch and product can take it.  Of s, the output and
+// the weights are used; live as launch_gather.
+bool few_fits(const Batch& b, const Product& p);
+cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t* live, const DevInfo& dev,
+                       cudaStream_t stream);
+
 // rg_mm_id.cu, rg_tc_id.cu: the tensor-core kernel over the tile table.
 cudaError_t launch_mm_id(int wtype, const void* W, int64_t experts, int64_t N, int64_t K, const uint16_t* x16,
                          int64_t ld, const Slots& s, int cg, const DevInfo& dev, cudaStream_t stream);

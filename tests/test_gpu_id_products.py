@@ -37,10 +37,10 @@ def test_smallest(rg):
 @pytest.mark.parametrize("wtype", TYPES)
 @pytest.mark.parametrize("fwd", [True, False])
 def test_types(rg, wtype, fwd):
-    """Every weight type, rows of 16-byte multiples and (where the type has them) others, few slots an expert."""
+    """Every weight type, rows of 16-byte multiples and (where the type has them) others, few slots an expert and many."""
     rng = np.random.default_rng(wtype)
-    for K in (2048, 768):
-        s = Stack(torch, rg, wtype, 5, 136, K, _ids(rng, 13, 3, 5, 0.1), 3, seed=K)
+    for K, tokens in ((2048, 3), (2048, 10), (2048, 14), (2048, 70), (2048, 400), (768, 10), (768, 300)):
+        s = Stack(torch, rg, wtype, 5, 136, K, _ids(rng, tokens, 3, 5, 0.1), 3, seed=K)
         s.check(fwd, BF16, TOKEN, SLOT)
 
 
