@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* _
     const int s = s_slot[4 * ty + i];
     if (s < 0) continue;
     const float m = g.weights != nullptr ? __ldg(g.weights + s) : 1.0f;
-    char* to = static_cast<char*>(g.out) + static_cast<int64_t>(s / g.out_div) * g.out_row * act_bytes(g.otype);
+    char* to = static_cast<char*>(g.out) + static_cast<int64_t>(s) * g.out_row * act_bytes(g.otype);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t o = o0 + 4 * tx + j;

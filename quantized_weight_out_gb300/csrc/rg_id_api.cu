@@ -137,7 +137,6 @@ cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void
   s.out = r.joined ? rows : p.out;
   s.out_row = r.joined ? p.out_w() : p.out_row;
   s.otype = r.joined ? RG_F32 : p.atype;
-  s.out_div = 1;
   s.beta = r.joined ? 0.0f : p.beta;
   cudaError_t e = cudaSuccess;
   if (r.few) {

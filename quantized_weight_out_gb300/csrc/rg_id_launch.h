@@ -88,7 +88,6 @@ struct Slots {
   void* out;
   int64_t out_row;
   int otype;              // RG_F32, RG_F16 or RG_BF16
-  int out_div;            // output row of slot s: s / out_div (per_token when a token has one slot)
   float beta;
 };
 

@@ -1035,64 +1035,71 @@ struct GrpArg {};
 template <>
 struct GrpArg<true> : id::Slots {};
 
-// Rows pos0 .. of one expert's tile (`left` of them, 32 columns of 32 lanes in
-// r: lane = output value k) to their slots' rows.
-template <class A>
-__device__ __forceinline__ void store_slots(const A& g, const uint32_t (&r)[32], int pos0, int left, int k, int K,
-                                            int lane) {
-  // lane i's row: its slot (or -1), and the factor of the row
-  int slot = -1;
-  float mul = 1.0f;
-  if (lane < left) {
-    slot = __ldg(g.order + pos0 + lane);
-    if (static_cast<unsigned>(slot) >= static_cast<unsigned>(g.slots)) slot = -1;
-    if (g.unscale != nullptr) mul = __ldcg(g.unscale + pos0 + lane);
-    if (g.weights != nullptr && slot >= 0) mul *= __ldg(g.weights + slot);
-  }
-  const int orow = slot < 0 ? -1 : slot / g.out_div;
-  if (g.otype == RG_F32) {
-    float* out = static_cast<float*>(g.out) + k;
+// One column block of an expert's tile (32 columns of 32 lanes in r: lane =
+// output value k0 + lane) to its slots' rows; lane i holds column i's output
+// row (-1: none) and factor.  The block is turned in shared memory (RB rows of
+// 32 values at a time, `stg` the warp's own), so that four lanes store a row's
+// 32 values, eight each: about 110 instructions a block, where exchanging the
+// values between neighbouring lanes took 400 and held items of 16 stages up.
+template <int RB, class A>
+__device__ __forceinline__ void store_slots(const A& g, const uint32_t (&r)[32], int orow, float mul, int k0, int K,
+                                            int lane, float* stg) {
+  const int c = 8 * (lane & 3), k = k0 + c;
+  // odd rows read their halves in the other order: the two rows of a quarter warp's read on different banks
+  const int flip = 4 * ((lane >> 2) & 1);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int row = __shfl_sync(0xffffffffu, orow, i);
-      const float v = __uint_as_float(r[i]) * __shfl_sync(0xffffffffu, mul, i);
-      if (row >= 0 && k < K) {
-        float* o = out + static_cast<int64_t>(row) * g.out_row;
-        *o = g.beta != 0.0f ? fmaf(g.beta, *o, v) : v;
+  for (int i = 0; i < 4; ++i) {
+    if (8 * i % RB == 0) {
+      __syncwarp();  // (the reads of what lay there)
+#pragma unroll
+      for (int q = 0; q < RB; ++q) stg[q * 32 + lane] = __uint_as_float(r[8 * i + q]);
+      __syncwarp();
+    }
+    const int at = 8 * i + (lane >> 2), in = at % RB;
+    const int row = __shfl_sync(0xffffffffu, orow, at);
+    const float m = __shfl_sync(0xffffffffu, mul, at);
+    const float4 x = *reinterpret_cast<const float4*>(stg + in * 32 + c + flip);
+    const float4 y = *reinterpret_cast<const float4*>(stg + in * 32 + c + (4 - flip));
+    if (row < 0 || k >= K) continue;  // (K is a multiple of 8)
+    const float4 a = flip ? y : x, b = flip ? x : y;
+    float v[8] = {a.x * m, a.y * m, a.z * m, a.w * m, b.x * m, b.y * m, b.z * m, b.w * m};
+    if (g.otype == RG_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
+      if (g.beta != 0.0f) {
+        const float4 p = o[0], q = o[1];
+        v[0] = fmaf(g.beta, p.x, v[0]); v[1] = fmaf(g.beta, p.y, v[1]);
+        v[2] = fmaf(g.beta, p.z, v[2]); v[3] = fmaf(g.beta, p.w, v[3]);
+        v[4] = fmaf(g.beta, q.x, v[4]); v[5] = fmaf(g.beta, q.y, v[5]);
+        v[6] = fmaf(g.beta, q.z, v[6]); v[7] = fmaf(g.beta, q.w, v[7]);
+      }
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+      continue;
+    }
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
+    uint32_t w[4];
+    if (g.beta != 0.0f) {
+      const uint4 q = *o;
+      const uint32_t old[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = g.otype == RG_F16
+                             ? __half22float2(u32_as_h2(old[e]))
+                             : make_float2(__uint_as_float(old[e] << 16), __uint_as_float(old[e] & 0xFFFF0000u));
+        v[2 * e] = fmaf(g.beta, f.x, v[2 * e]);
+        v[2 * e + 1] = fmaf(g.beta, f.y, v[2 * e + 1]);
       }
     }
-    return;
-  }
-  // 16-bit rows: two lanes exchange halves of two rows, so that each stores two
-  // neighbouring values of one row (even lanes row 2i, odd lanes row 2i + 1)
-  const int odd = lane & 1;
-  uint16_t* out = static_cast<uint16_t*>(g.out) + (k & ~1);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1));
-    const int row = __shfl_sync(0xffffffffu, orow, 2 * i + odd);
-    const float m = __shfl_sync(0xffffffffu, mul, 2 * i + odd);
-    float a = (odd ? other : __uint_as_float(r[2 * i])) * m;
-    float b = (odd ? __uint_as_float(r[2 * i + 1]) : other) * m;
-    if (row >= 0 && k < K) {
-      uint32_t* o = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(row) * g.out_row);
+    for (int e = 0; e < 4; ++e) {
       if (g.otype == RG_F16) {
-        if (g.beta != 0.0f) {
-          const float2 x = __half22float2(u32_as_h2(*o));
-          a = fmaf(g.beta, x.x, a);
-          b = fmaf(g.beta, x.y, b);
-        }
-        *o = h2_as_u32(__floats2half2_rn(a, b));
+        w[e] = h2_as_u32(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
       } else {
-        if (g.beta != 0.0f) {
-          const uint32_t x = *o;
-          a = fmaf(g.beta, __uint_as_float(x << 16), a);
-          b = fmaf(g.beta, __uint_as_float(x & 0xFFFF0000u), b);
-        }
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        *o = *reinterpret_cast<const uint32_t*>(&h);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
+    *o = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -1564,19 +1571,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int kt = ku * CG + static_cast<int>(rank);
       const int a = j & 1;
       const uint32_t aph = (static_cast<uint32_t>(j) >> 1) & 1u;
+      // GRP: the tile's slots, all column blocks' loads in flight while the
+      // sums are still being made (one block's after the other's, behind the
+      // wait, held items of 16 to 32 stages up)
+      int orow[GRP ? BT / 32 : 1];
+      float mul[GRP ? BT / 32 : 1];
+      if constexpr (GRP) {
+#pragma unroll
+        for (int cb = 0; cb < BT / 32; ++cb) {
+          const bool in = 32 * cb + lane < st.rows;
+          orow[cb] = in ? __ldg(grp.order + st.pos + 32 * cb + lane) : -1;
+          mul[cb] = in && grp.unscale != nullptr ? __ldcg(grp.unscale + st.pos + 32 * cb + lane) : 1.0f;
+        }
+#pragma unroll
+        for (int cb = 0; cb < BT / 32; ++cb) {
+          if (static_cast<unsigned>(orow[cb]) >= static_cast<unsigned>(grp.slots)) orow[cb] = -1;
+          if (grp.weights != nullptr && orow[cb] >= 0) mul[cb] *= __ldg(grp.weights + orow[cb]);
+        }
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(acc_full(a), aph, ctl, abort_flag));
       if (!ok) break;
       tc_fence_after();
       const int k = kt * BM + 32 * eq + lane;
       const bool kin = k < K;
       if constexpr (GRP) {
-#pragma unroll 1
-        for (int cb = 0; cb < BT / 32 && 32 * cb < st.rows; ++cb) {
+#pragma unroll
+        for (int cb = 0; cb < BT / 32; ++cb) {
+          if (32 * cb >= st.rows) break;
           uint32_t r[32];
           tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(32 * eq) << 16) +
                                  static_cast<uint32_t>(a * BT + 32 * cb),
                              r);
-          store_slots(grp, r, st.pos + 32 * cb, st.rows - 32 * cb, k, K, lane);
+          store_slots<2 * C::EPI_ROWS>(grp, r, orow[cb], mul[cb], kt * BM + 32 * eq, K, lane, stg);
         }
         tc_fence_before();
         __syncwarp();
