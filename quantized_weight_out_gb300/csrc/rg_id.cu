@@ -84,14 +84,21 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
     uint16_t* to = x16 + i * ld;
     const int64_t row = ok ? (in_tokens ? s / b.per_token : s) : 0;
     const char* from = static_cast<const char*>(in) + row * in_row * act_bytes(AT);
+    constexpr int U = 4;  // steps of 256 values in flight
+    float v[U][8];
+    auto fetch = [&](int c0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_act8<AT>(from, min(c0 + 256 * u, wide - 8), v[u]);
+    };
     float mul = 1.0f;
     if constexpr (!BF16) {
       float top = 0.0f;
-      for (int c = 8 * lane; c < wide; c += 256) {
-        float v[8];
-        load_act8<AT>(from, c, v);
+      for (int c0 = 8 * lane; c0 < wide; c0 += 256 * U) {
+        fetch(c0);  // (past the row's end its last values again)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[u][j]));
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -99,12 +106,16 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
       mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
       if (lane == 0) unscale[i] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
     }
-    for (int c = 8 * lane; c < wide; c += 256) {
-      float v[8];
-      load_act8<AT>(from, c, v);
+    for (int c0 = 8 * lane; c0 < wide; c0 += 256 * U) {
+      fetch(c0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ok ? v[j] * mul : 0.0f;
-      store_act8<BF16 ? RG_BF16 : RG_F16>(to, c, v);
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + 256 * u;
+        if (c >= wide) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = ok ? v[u][j] * mul : 0.0f;
+        store_act8<BF16 ? RG_BF16 : RG_F16>(to, c, v[u]);
+      }
     }
   }
 }

@@ -11,7 +11,7 @@ template <int WT, int CG, int BT, bool FWD>
 static cudaError_t launch_grp_t(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& ml,
                                 const CUtensorMap& mq, int K, int n_kunits, int band, int n_chunks, const Slots& s,
                                 const DevInfo& dev, cudaStream_t stream) {
-  using C = tc::Cfg<WT, CG, BT, FWD>;
+  using C = tc::Cfg<WT, CG, BT, FWD, true>;
   auto kern = tc::out_prod_tc_kernel<WT, CG, BT, false, false, FWD, true>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -63,7 +63,7 @@ static cudaError_t launch_grp(int wtype, const void* W, int64_t experts, int64_t
                           n * rb);
     };
     const uint32_t box = static_cast<uint32_t>(with_wtype(wtype, 0, [](auto wt) {
-                           return FWD ? tc::p_fwd_row_bytes<decltype(wt)::value>()
+                           return FWD ? tc::p_fwd_bytes<decltype(wt)::value, true>()
                                       : tc::p_row_bytes<decltype(wt)::value>();
                          })) / 4;
     // (the forward's Q4_K and Q6_K windows are split, as in launch_tc_impl)

@@ -101,17 +101,24 @@ __host__ __device__ constexpr int p_fwd_row_bytes() {
   return WT == RG_Q4_K ? 48 : WT == RG_Q8_0 ? 80 : WT == RG_Q6_K ? 80 + 48 + 32
          : WT == RG_Q3_K ? 144 : WT == RG_Q2_K ? 112 : p_row_bytes<WT>();
 }
+// The forward by slot takes MXFP4's two 17-byte blocks of a chunk inside a
+// 48-byte window (0 .. 14 bytes in), where the whole 128-value window of 112
+// bytes made the L2 the limit (16 + 14 KB a stage of each CTA).
+template <int WT, bool GRP>
+__host__ __device__ constexpr int p_fwd_bytes() {
+  return GRP && WT == RG_MXFP4 ? 48 : p_fwd_row_bytes<WT>();
+}
 // The forward's Q6_K windows, bytes a row: low bits, high bits, scales and d.
 constexpr int Q6F_A = 80, Q6F_H = 48, Q6F_S = 32;
 
-template <int WT, int CG, int BT, bool FWD = false>
+template <int WT, int CG, int BT, bool FWD = false, bool GRP = false>
 struct Cfg {
   static constexpr bool QUANT = is_quant(WT);
   static constexpr bool BF = WT == RG_BF16;
   // rows of W in a packed-window stage: the OUT_PROD's 64 contraction rows,
   // or the forward's 128 output rows (FWD: the contraction runs along the rows)
   static constexpr int P_ROWS = FWD ? 2 * BC : BC;
-  static constexpr int P_ROW = FWD ? p_fwd_row_bytes<WT>() : p_row_bytes<WT>();
+  static constexpr int P_ROW = FWD ? p_fwd_bytes<WT, GRP>() : p_row_bytes<WT>();
   static constexpr int P_STAGE = QUANT ? ((P_ROWS * P_ROW + 1023) / 1024) * 1024 : 0;
   static constexpr int STAGE = A_STAGE + B_STAGE + P_STAGE;
   // quantized: five slots (Q6_K four; fewer when they do not fit), each
@@ -124,18 +131,33 @@ struct Cfg {
   // measured 9 % slower with the same trade, so it keeps 16 rows)
   static constexpr int slots_with(int epi_bytes) { return std::min(S_MAX, (SMEM_BUDGET - epi_bytes) / STAGE); }
   static constexpr int EPI_ROWS =
-      FWD && slots_with(4 * 2 * 8 * 32 * 4) > slots_with(4 * 2 * 16 * 32 * 4) ? 8 : 16;
+      GRP || (FWD && slots_with(4 * 2 * 8 * 32 * 4) > slots_with(4 * 2 * 16 * 32 * 4)) ? 8 : 16;
   static constexpr int EPI_BYTES = 4 * 2 * EPI_ROWS * 32 * 4;
-  static constexpr int S = slots_with(EPI_BYTES);
+  // GRP, quantized: the packed windows have a ring of their own, one or two
+  // stages longer than the operand slots', so that a slot's decoders find their
+  // window there when the slot is free (with one ring a slot went through the
+  // window's load, the decode and the MMA in turn: MXFP4's forward 0.72 us a
+  // stage, the tensor cores a third busy)
+  static constexpr int p_slots(int s) {
+    return std::min(s + 2, (SMEM_BUDGET - EPI_BYTES - s * (A_STAGE + B_STAGE)) / std::max(1, P_STAGE));
+  }
+  static constexpr int grp_slots() {
+    for (int s = S_MAX; s > 3; --s)
+      if (p_slots(s) > s) return s;
+    return 3;
+  }
+  static constexpr bool P_RING = GRP && QUANT && p_slots(grp_slots()) > grp_slots();
+  static constexpr int S = P_RING ? grp_slots() : slots_with(EPI_BYTES);
+  static constexpr int PS = P_RING ? p_slots(S) : S;
   static constexpr int WARPS_PER_SLOT = QUANT ? 2 : 0;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + S * A_STAGE;
   static constexpr int OFF_P = OFF_B + S * B_STAGE;
-  static constexpr int OFF_EPI = OFF_P + S * P_STAGE;
+  static constexpr int OFF_EPI = OFF_P + PS * P_STAGE;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
-  // barriers: full_p, full_ab, full_dec, empty (S each), acc_full[2],
+  // barriers: full_p (PS), full_ab, full_dec, empty (S each), acc_full[2],
   // acc_empty[2], drain
-  static constexpr int NUM_BARS = 4 * S + 5;
+  static constexpr int NUM_BARS = PS + 3 * S + 5;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack for 1024 B alignment
   static constexpr uint32_t P_BYTES = QUANT ? P_ROWS * P_ROW : 0;
@@ -280,19 +302,11 @@ __device__ __forceinline__ void e2m1x4_f16(uint32_t x, uint32_t& o01, uint32_t& 
   o23 = __byte_perm(hb, 0u, 0x3424);
 }
 
-// MXFP4 block B of a 128-value tile whose blocks start o = 0, 4, 8 or 12
-// bytes into the row window (a run-time value: one code path for every
-// offset, so the decoders' instructions stay few).  Block B begins at byte
-// o + 17B: its 16-byte chunk and the next are loaded, the five words from
-// the block's own word on are selected by (o + 17B) mod 16 / 4 (the shift
-// inside a word, B mod 4, is fixed).  Writes its 32 values,
-// E2M1(q) * 2^(e - 127) rounded once to fp16, as chunks 4B .. 4B+3 of row n.
-template <int B>
-__device__ __forceinline__ void dec_mxfp4_block(const uint8_t* row, uint8_t* A, int n, int o) {
-  constexpr int SH = B & 3;  // (o + 17B) mod 4
-  const int S = o + 17 * B;
-  const uint4 c0 = *reinterpret_cast<const uint4*>(row + (S & ~15));
-  const uint4 c1 = *reinterpret_cast<const uint4*>(row + (S & ~15) + 16);
+// MXFP4 block that starts S bytes into a row window (SH = S mod 4; c0 and c1:
+// the 16-byte chunk it begins in and the next) as values 32b .. 32b + 31 of the
+// tile; see dec_mxfp4_block.
+template <int SH>
+__device__ __forceinline__ void dec_mxfp4_of(uint4 c0, uint4 c1, uint8_t* A, int n, int S, int b) {
   const uint32_t q[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   const int j0 = (S & 15) >> 2;  // 0..3: the block's first word in q
   uint32_t w[5];
@@ -316,10 +330,24 @@ __device__ __forceinline__ void dec_mxfp4_block(const uint8_t* row, uint8_t* A, 
     hi[2 * j] = h2_as_u32(__hmul2(u32_as_h2(b0), sc));
     hi[2 * j + 1] = h2_as_u32(__hmul2(u32_as_h2(b1), sc));
   }
-  st_a_chunk(A, n, 4 * B, lo[0], lo[1], lo[2], lo[3]);
-  st_a_chunk(A, n, 4 * B + 1, lo[4], lo[5], lo[6], lo[7]);
-  st_a_chunk(A, n, 4 * B + 2, hi[0], hi[1], hi[2], hi[3]);
-  st_a_chunk(A, n, 4 * B + 3, hi[4], hi[5], hi[6], hi[7]);
+  st_a_chunk(A, n, 4 * b, lo[0], lo[1], lo[2], lo[3]);
+  st_a_chunk(A, n, 4 * b + 1, lo[4], lo[5], lo[6], lo[7]);
+  st_a_chunk(A, n, 4 * b + 2, hi[0], hi[1], hi[2], hi[3]);
+  st_a_chunk(A, n, 4 * b + 3, hi[4], hi[5], hi[6], hi[7]);
+}
+
+// MXFP4 block B of a 128-value tile whose blocks start o = 0, 4, 8 or 12
+// bytes into the row window (a run-time value: one code path for every
+// offset, so the decoders' instructions stay few).  Block B begins at byte
+// o + 17B: its 16-byte chunk and the next are loaded, the five words from
+// the block's own word on are selected by (o + 17B) mod 16 / 4 (the shift
+// inside a word, B mod 4, is fixed).  Writes its 32 values,
+// E2M1(q) * 2^(e - 127) rounded once to fp16, as chunks 4B .. 4B+3 of row n.
+template <int B>
+__device__ __forceinline__ void dec_mxfp4_block(const uint8_t* row, uint8_t* A, int n, int o) {
+  const int S = o + 17 * B;
+  const uint4* c = reinterpret_cast<const uint4*>(row + (S & ~15));
+  dec_mxfp4_of<B & 3>(c[0], c[1], A, n, S, B);
 }
 
 // Two E4M3 bytes (bits 0-7 and 8-15 of w) -> their fp16 pair, exactly: the
@@ -901,6 +929,34 @@ __device__ __forceinline__ void decode_stage_fwd_q8(const uint8_t* __restrict__ 
   }
 }
 
+// The forward's MXFP4 stage by slot: 128 rows' two blocks of the 64-value chunk
+// gf, (34 gf) mod 16 bytes into each row's 48-byte window, as chunks 0..7.
+__device__ __forceinline__ void decode_stage_fwd_mx(const uint8_t* __restrict__ P, uint8_t* __restrict__ A, int lane,
+                                                    int part, int gf) {
+  const int o = (34 * gf) & 15;
+  // every block's bytes first: the decodes' loads do not wait behind the stores of the ones before
+  uint4 c[2][2][2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint4* p = reinterpret_cast<const uint4*>(P + (lane + 32 * (2 * part + r)) * 48 + ((o + 17 * b) & ~15));
+      c[r][b][0] = p[0];
+      c[r][b][1] = p[1];
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int n = lane + 32 * (2 * part + r);
+    if (gf & 1) {
+      dec_mxfp4_of<2>(c[r][0][0], c[r][0][1], A, n, o, 0);
+      dec_mxfp4_of<3>(c[r][1][0], c[r][1][1], A, n, o + 17, 1);
+    } else {
+      dec_mxfp4_of<0>(c[r][0][0], c[r][0][1], A, n, o, 0);
+      dec_mxfp4_of<1>(c[r][1][0], c[r][1][1], A, n, o + 17, 1);
+    }
+  }
+}
+
 // decode_stage_fwd for the run-time tile kw of the row (its parity, and the
 // block offset of the row-half and MXFP4 decoders) and half hv.
 template <int WT>
@@ -1133,10 +1189,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                        float* __restrict__ dX, int64_t ldx, float beta, int T, int K,
                        int n_kunits, int n_ttiles, int band, int n_chunks, int n_splits,
                        float* __restrict__ part, WaitCtl ctl, const __grid_constant__ GrpArg<GRP> grp) {
-  using C = Cfg<WT, CG, BT, FWD>;
+  using C = Cfg<WT, CG, BT, FWD, GRP>;
   static_assert(!FWD || (!AD && !SK), "the forward runs without an adapter or stream-K");
   static_assert(!GRP || (!AD && !SK), "products by slot run without an adapter or stream-K");
-  constexpr int S = C::S;
+  constexpr int S = C::S, PS = C::PS;
   extern __shared__ uint8_t smem_raw[];
   // align inside the shared window (pointer arithmetic keeps the shared space)
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -1145,12 +1201,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sP = smem + C::OFF_P;
   const uint32_t bar0 = smem_addr(smem + C::OFF_BAR);
   auto full_p = [&](int s) { return bar0 + 8u * s; };
-  auto full_ab = [&](int s) { return bar0 + 8u * (S + s); };
-  auto full_dec = [&](int s) { return bar0 + 8u * (2 * S + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (3 * S + s); };
-  auto acc_full = [&](int a) { return bar0 + 8u * (4 * S + a); };
-  auto acc_empty = [&](int a) { return bar0 + 8u * (4 * S + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (4 * S + 4);
+  auto full_ab = [&](int s) { return bar0 + 8u * (PS + s); };
+  auto full_dec = [&](int s) { return bar0 + 8u * (PS + S + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (PS + 2 * S + s); };
+  auto acc_full = [&](int a) { return bar0 + 8u * (PS + 3 * S + a); };
+  auto acc_empty = [&](int a) { return bar0 + 8u * (PS + 3 * S + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (PS + 3 * S + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -1178,8 +1234,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
 
   if (warp == 0 && lane == 0) {
+    for (int s = 0; s < PS; ++s) mbar_init(full_p(s), 1);
     for (int s = 0; s < S; ++s) {
-      mbar_init(full_p(s), 1);
       mbar_init(full_ab(s), 1);
       mbar_init(full_dec(s), C::FULL_DEC_COUNT);
       mbar_init(empty(s), 1);
@@ -1259,7 +1315,69 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t ab_bar_leader = CG == 2 ? mapa_shared(full_ab(0), 0) : full_ab(0);
     int s = 0;
     uint32_t ph = 0;
-    uint32_t pend_p = 0, pend_ab = 0, pend_ph = 0;  // stages with copies in flight
+    uint32_t pend_p = 0, pend_ab = 0, pend_ph = 0, pend_pph = 0;  // stages with copies in flight
+    // a stage's packed window(s) into slot s of their ring: chunk gc of tile kt
+    auto load_window = [&](int s, int gc, int kt, int expert) {
+      auto load_p = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+        if constexpr (GRP) tma_load_3d(dst, map, bar, x, y, expert);
+        else tma_load_2d(dst, map, bar, x, y);
+      };
+      mbar_arrive_expect_tx(full_p(s), C::P_BYTES);
+      if constexpr (FWD && WT == RG_Q4_K) {
+        // the super-block headers, then the chunk's nibbles (map_l), 128 rows each
+        const int sb = (gc >> 2) * 144;
+        load_p(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), sb / 4, kt * BM);
+        load_p(smem_addr(sP + s * C::P_STAGE) + 128 * 16, &map_l, full_p(s),
+               (sb + 16 + 32 * (gc & 3)) / 4, kt * BM);
+      } else if constexpr (FWD && WT == RG_Q6_K) {
+        // the half's low bits, its high bits, the scales and d (three
+        // windows, 128 rows each, one region of the stage apiece)
+        const int sb = (gc >> 2) * 210, h = (gc >> 1) & 1;
+        const uint32_t dst = smem_addr(sP + s * C::P_STAGE);
+        load_p(dst, &map_w, full_p(s), ((sb + 64 * h) & ~15) / 4, kt * BM);
+        load_p(dst + 128 * Q6F_A, &map_l, full_p(s), ((sb + 128 + 32 * h) & ~15) / 4, kt * BM);
+        load_p(dst + 128 * (Q6F_A + Q6F_H), &map_q, full_p(s), ((sb + 192) & ~15) / 4, kt * BM);
+      } else if constexpr (FWD && WT == RG_Q8_0) {  // the chunk's two blocks
+        load_p(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), ((gc * 68) & ~15) / 4,
+               kt * BM);
+      } else if constexpr (FWD && GRP && WT == RG_MXFP4) {  // likewise
+        load_p(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), ((gc * 34) & ~15) / 4, kt * BM);
+      } else if constexpr (FWD) {  // the window of the 128-value tile holding chunk gc
+        load_p(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
+               p_window_start<WT>(gc >> 1) / 4, kt * BM);
+      } else
+        load_p(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
+               p_window_start<WT>(kt) / 4, gc * BC);
+    };
+    // P_RING: the windows run PS - S stages ahead of the slots.  Window j goes to
+    // slot j mod PS, which stage j - PS had: when stage i's slot is free, the MMA
+    // of stage i - S is done, and so is that stage's decode in this CTA, so window
+    // i + PS - S may be loaded.
+    Segs<SK> wsg(unit, n_units, n_tiles, n_chunks);
+    int w_item = 0, w_c = 0, w_c1 = 0, w_kt = 0, w_expert = 0, w_slot = 0;
+    uint32_t w_ph = 0;
+    auto next_window = [&] {
+      if (w_c == w_c1) {
+        int c0;
+        if (!wsg.next(w_item, c0, w_c1)) {
+          w_c = w_c1 = 0;
+          return;
+        }
+        w_c = c0;
+        int ku = 0;
+        w_expert = coords_grp(w_item, ku).expert;
+        w_kt = ku * CG + static_cast<int>(rank);
+      }
+      load_window(w_slot, w_c++, w_kt, w_expert);
+      pend_p |= 1u << w_slot;
+      pend_pph = (pend_pph & ~(1u << w_slot)) | (w_ph << w_slot);
+      if (++w_slot == PS) { w_slot = 0; w_ph ^= 1u; }
+    };
+    if constexpr (C::P_RING) {
+      if (lane == 0)
+        for (int i = 0; i < PS - S; ++i) next_window();
+      __syncwarp();
+    }
     bool ok = true;
     Segs<SK> sg(unit, n_units, n_tiles, n_chunks);
     int tile = 0, c0 = 0, c1 = 0;
@@ -1291,32 +1409,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               mbar_arrive_expect_tx(full_ab(s), C::AB_BYTES_PAIR);
               pend_ab |= 1u << s;
             }
-            if constexpr (C::QUANT) {
-              mbar_arrive_expect_tx(full_p(s), C::P_BYTES);
-              if constexpr (FWD && WT == RG_Q4_K) {
-                // the super-block headers, then the chunk's nibbles (map_l), 128 rows each
-                const int sb = (gc >> 2) * 144;
-                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), sb / 4, kt * BM);
-                load_w(smem_addr(sP + s * C::P_STAGE) + 128 * 16, &map_l, full_p(s),
-                            (sb + 16 + 32 * (gc & 3)) / 4, kt * BM);
-              } else if constexpr (FWD && WT == RG_Q6_K) {
-                // the half's low bits, its high bits, the scales and d (three
-                // windows, 128 rows each, one region of the stage apiece)
-                const int sb = (gc >> 2) * 210, h = (gc >> 1) & 1;
-                const uint32_t dst = smem_addr(sP + s * C::P_STAGE);
-                load_w(dst, &map_w, full_p(s), ((sb + 64 * h) & ~15) / 4, kt * BM);
-                load_w(dst + 128 * Q6F_A, &map_l, full_p(s), ((sb + 128 + 32 * h) & ~15) / 4, kt * BM);
-                load_w(dst + 128 * (Q6F_A + Q6F_H), &map_q, full_p(s), ((sb + 192) & ~15) / 4, kt * BM);
-              } else if constexpr (FWD && WT == RG_Q8_0) {  // the chunk's two blocks
-                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s), ((gc * 68) & ~15) / 4,
-                            kt * BM);
-              } else if constexpr (FWD) {  // the window of the 128-value tile holding chunk gc
-                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
-                            p_window_start<WT>(gc >> 1) / 4, kt * BM);
-              } else
-                load_w(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
-                            p_window_start<WT>(kt) / 4, gc * BC);
+            if constexpr (C::P_RING) {
+              // (the windows run ahead: below)
+            } else if constexpr (C::QUANT) {
+              load_window(s, gc, kt, st.expert);
               pend_p |= 1u << s;
+              pend_pph = (pend_pph & ~(1u << s)) | (ph << s);
             } else {
               const uint32_t a_dst = smem_addr(sA + s * A_STAGE);
               if constexpr (FWD) {
@@ -1350,6 +1448,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 tma_load_2d(smem_addr(sP + s * C::P_STAGE), &map_w, full_p(s),
                             p_window_start<WT>(kt) / 4, gc * BC);
                 pend_p |= 1u << s;
+                pend_pph = (pend_pph & ~(1u << s)) | (ph << s);
               }
             }
             if (dense_a) {
@@ -1370,6 +1469,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           else
             tma_load_2d(smem_addr(sB + s * B_STAGE), &map_y, abar, (cbase + c) * BC, ty);
           pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
+          if constexpr (C::P_RING) next_window();
         }
         __syncwarp();
         if (++s == S) { s = 0; ph ^= 1u; }
@@ -1381,11 +1481,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // issuing CTA's barrier, which that CTA drains, and the follower waits
       // out a copy's latency many times over.
       volatile int no_abort = 0;
-      for (int st = 0; st < S; ++st) {
-        const uint32_t p = (pend_ph >> st) & 1u;
-        if (pend_p & (1u << st)) (void)mbar_wait(full_p(st), p, ctl, &no_abort);
-        if (pend_ab & (1u << st)) (void)mbar_wait(full_ab(st), p, ctl, &no_abort);
-      }
+      for (int st = 0; st < PS; ++st)
+        if (pend_p & (1u << st)) (void)mbar_wait(full_p(st), (pend_pph >> st) & 1u, ctl, &no_abort);
+      for (int st = 0; st < S; ++st)
+        if (pend_ab & (1u << st)) (void)mbar_wait(full_ab(st), (pend_ph >> st) & 1u, ctl, &no_abort);
       if (!leader) {
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 200000ull) {
@@ -1475,6 +1574,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int tile = 0, c0 = 0, c1 = 0;
         int c = s;
         uint32_t ph = 0;
+        int ps = s;  // this stage's window: its slot and phase (P_RING: of a ring of its own)
+        uint32_t pph = 0;
         bool run = true;
         while (run && sg.next(tile, c0, c1)) {
           const int len = c1 - c0;
@@ -1496,21 +1597,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if constexpr (AD) c_ad = n_main - (tile / n_tiles1) * n_chunks;
           for (; c < len; c += S, ph ^= 1u) {
             const int cc = c0 + c;  // the chunk of the item
-            if (!__all_sync(0xffffffffu, mbar_wait(full_p(s), ph, ctl, abort_flag))) {
+            bool got = mbar_wait(full_p(ps), C::P_RING ? pph : ph, ctl, abort_flag);
+            // (with one ring the window was loaded when the slot was free)
+            if constexpr (C::P_RING) got = got && wait_any(empty(s), ph ^ 1u);
+            if (!__all_sync(0xffffffffu, got)) {
               run = false;
               break;
+            }
+            const uint8_t* window = sP + ps * C::P_STAGE;
+            if constexpr (C::P_RING) {
+              ps += S;
+              if (ps >= PS) {
+                ps -= PS;
+                pph ^= 1u;
+              }
             }
             if constexpr (FWD) {
               // chunk gf: values 64 gf .. 64 gf + 63 of this CTA's 128 rows of W
               const int gf = GRP ? cc : (tile / n_tiles1) * n_chunks + cc;
-              decode_fwd_stage<WT>(sP + s * C::P_STAGE, sA + s * A_STAGE, lane, part, gf >> 1, gf & 1);
+              if constexpr (GRP && WT == RG_MXFP4) decode_stage_fwd_mx(window, sA + s * A_STAGE, lane, part, gf);
+              else decode_fwd_stage<WT>(window, sA + s * A_STAGE, lane, part, gf >> 1, gf & 1);
             } else if (AD && cc >= c_ad) {
               // nothing to decode
             } else if constexpr (WT == RG_Q6_K || WT == RG_Q3_K || WT == RG_Q2_K) {
               // the super-block starts o bytes into its window: one decoder per
               // o (Q6_K, Q3_K: any even o; Q2_K: a multiple of 4)
               const int o = ((kt >> 1) * block_bytes(WT)) & 15;
-              const uint8_t* P = sP + s * C::P_STAGE;
+              const uint8_t* P = window;
               uint8_t* Ad = sA + s * A_STAGE;
 #define RG_WIN_CASE(OO)                                                          \
   case OO / 2:                                                                   \
@@ -1528,12 +1641,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             } else if constexpr (WT == RG_MXFP4 || WT == RG_NVFP4) {
               // the tile's blocks start (kt * 68) mod 16 = 0, 4, 8 or 12 (MXFP4)
               // or (kt * 72) mod 16 = 0 or 8 (NVFP4) bytes into the window
-              decode_stage_warp<WT, 0, WPS>(sP + s * C::P_STAGE, sA + s * A_STAGE, lane, part,
+              decode_stage_warp<WT, 0, WPS>(window, sA + s * A_STAGE, lane, part,
                                             WT == RG_MXFP4 ? (kt * 68) & 12 : (kt & 1) * 8);
           } else if (kt & 1) {
-              decode_stage_warp<WT, 1, WPS>(sP + s * C::P_STAGE, sA + s * A_STAGE, lane, part);
+              decode_stage_warp<WT, 1, WPS>(window, sA + s * A_STAGE, lane, part);
             } else {
-              decode_stage_warp<WT, 0, WPS>(sP + s * C::P_STAGE, sA + s * A_STAGE, lane, part);
+              decode_stage_warp<WT, 0, WPS>(window, sA + s * A_STAGE, lane, part);
             }
             if (!AD || cc < c_ad) fence_proxy_async_smem();
             __syncwarp();
