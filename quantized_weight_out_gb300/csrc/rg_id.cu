@@ -53,13 +53,15 @@ __device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
   if (threadIdx.x == 0) *n_tiles = static_cast<int>(base_s < cap ? base_s : cap);
 }
 
-// Block 0 builds the table; the other blocks' warps take the sorted slots in
-// turn.  A row of an fp16 copy is multiplied by the power of two that brings
+// Block 0 builds the table; the other blocks' groups of LANES threads (a warp,
+// or for rows over 4096 values the block: so many rows of warps would be under
+// way that their second reading misses the L2, 103 us for 8186 rows of 14336)
+// take the sorted slots in turn.  A row of an fp16 copy is multiplied by the power of two that brings
 // its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
 // fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
 // and none overflows; the product's rows are multiplied by the inverse, which
 // is exact, in F32.
-template <int AT, bool BF16>
+template <int AT, bool BF16, int LANES>
 __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* tiles, int* n_tiles, int cap,
                                                          const void* __restrict__ in, int64_t in_row, int in_tokens,
                                                          int wide, uint16_t* __restrict__ x16, int64_t ld,
@@ -70,10 +72,11 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
     build_tiles(b, bt, tiles, n_tiles, cap, status);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int step = (gridDim.x - 1) * (THREADS / 32);
+  __shared__ float s_top[THREADS / 32];
+  const int lane = threadIdx.x % LANES;
+  const int step = (gridDim.x - 1) * (THREADS / LANES);
   const int total = __ldg(b.start + b.experts);
-  for (int i = (blockIdx.x - 1) * (THREADS / 32) + (threadIdx.x >> 5); i < b.slots; i += step) {
+  for (int i = (blockIdx.x - 1) * (THREADS / LANES) + threadIdx.x / LANES; i < b.slots; i += step) {
     const int s = __ldg(b.order + i);
     const bool ok = static_cast<unsigned>(s) < static_cast<unsigned>(b.slots);
     if (lane == 0) {
@@ -84,16 +87,16 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
     uint16_t* to = x16 + i * ld;
     const int64_t row = ok ? (in_tokens ? s / b.per_token : s) : 0;
     const char* from = static_cast<const char*>(in) + row * in_row * act_bytes(AT);
-    constexpr int U = 4;  // steps of 256 values in flight
+    constexpr int U = 4;  // steps in flight
     float v[U][8];
     auto fetch = [&](int c0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_act8<AT>(from, min(c0 + 256 * u, wide - 8), v[u]);
+      for (int u = 0; u < U; ++u) load_act8<AT>(from, min(c0 + 8 * LANES * u, wide - 8), v[u]);
     };
     float mul = 1.0f;
     if constexpr (!BF16) {
       float top = 0.0f;
-      for (int c0 = 8 * lane; c0 < wide; c0 += 256 * U) {
+      for (int c0 = 8 * lane; c0 < wide; c0 += 8 * LANES * U) {
         fetch(c0);  // (past the row's end its last values again)
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -102,15 +105,22 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if constexpr (LANES > 32) {
+        __syncthreads();  // (the last row's reads)
+        if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_top[w]);
+      }
       const int shift = row_shift(top);
       mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
       if (lane == 0) unscale[i] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
     }
-    for (int c0 = 8 * lane; c0 < wide; c0 += 256 * U) {
+    for (int c0 = 8 * lane; c0 < wide; c0 += 8 * LANES * U) {
       fetch(c0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = c0 + 256 * u;
+        const int c = c0 + 8 * LANES * u;
         if (c >= wide) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[u][j] = ok ? v[u][j] * mul : 0.0f;
@@ -131,17 +141,29 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* rows, int64_
        g += static_cast<int64_t>(gridDim.x) * THREADS) {
     const int64_t t = g / groups, c = (g - t * groups) * 8;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j = 0; j < per_token; ++j) {
-      const int64_t s = t * per_token + j;
-      if (!__ldcg(live + s)) continue;
-      const float w = weights != nullptr ? __ldg(weights + s) : 1.0f;
-      float v[8];
-      const float4* p = reinterpret_cast<const float4*>(rows + s * width + c);
-      const float4 a = __ldcg(p), b = __ldcg(p + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    constexpr int U = 4;  // slots in flight (rows of slots without an expert are read, and not used)
+    for (int j0 = 0; j0 < per_token; j0 += U) {
+      float4 v[U][2];
+      float w[U];
+      bool on[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t s = t * per_token + min(j0 + u, per_token - 1);
+        const float4* p = reinterpret_cast<const float4*>(rows + s * width + c);
+        v[u][0] = __ldcg(p);
+        v[u][1] = __ldcg(p + 1);
+        on[u] = j0 + u < per_token && __ldcg(live + s);
+        w[u] = weights != nullptr ? __ldg(weights + s) : 1.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on[u]) {
+          const float4 a = v[u][0], b = v[u][1];
+          sum[0] = fmaf(w[u], a.x, sum[0]); sum[1] = fmaf(w[u], a.y, sum[1]);
+          sum[2] = fmaf(w[u], a.z, sum[2]); sum[3] = fmaf(w[u], a.w, sum[3]);
+          sum[4] = fmaf(w[u], b.x, sum[4]); sum[5] = fmaf(w[u], b.y, sum[5]);
+          sum[6] = fmaf(w[u], b.z, sum[6]); sum[7] = fmaf(w[u], b.w, sum[7]);
+        }
     }
     char* to = static_cast<char*>(out) + t * out_row * act_bytes(AT);
     if (beta != 0.0f) {
@@ -251,12 +273,15 @@ cudaError_t with_atype(int atype, F&& f) {
 cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, const Product& p, bool bf16,
                           uint16_t* x16, int64_t ld, float* unscale, uint8_t* live, const DevInfo& dev,
                           cudaStream_t stream) {
+  const bool wide = x16 != nullptr && p.wide() > 4096;
+  const int64_t a_block = wide ? 1 : THREADS / 32;
   const int64_t blocks = x16 == nullptr && live == nullptr
                              ? 0
-                             : std::min<int64_t>((b.slots + THREADS / 32 - 1) / (THREADS / 32), dev.num_sms * 8);
+                             : std::min<int64_t>((b.slots + a_block - 1) / a_block, dev.num_sms * 8);
   return with_atype(p.atype, [&](auto at) {
     constexpr int AT = decltype(at)::value;
-    auto kern = bf16 ? gather_kernel<AT, true> : gather_kernel<AT, false>;
+    auto kern = bf16 ? (wide ? gather_kernel<AT, true, THREADS> : gather_kernel<AT, true, 32>)
+                     : (wide ? gather_kernel<AT, false, THREADS> : gather_kernel<AT, false, 32>);
     kern<<<static_cast<unsigned>(1 + blocks), THREADS, 0, stream>>>(
         b, bt, tiles, n_tiles, cap, p.in, p.in_row, p.in_tokens ? 1 : 0, static_cast<int>(p.wide()), x16, ld, unscale,
         live, dev.status);
