@@ -132,7 +132,8 @@ struct Cfg {
   static constexpr int slots_with(int epi_bytes) { return std::min(S_MAX, (SMEM_BUDGET - epi_bytes) / STAGE); }
   static constexpr int EPI_ROWS =
       GRP || (FWD && slots_with(4 * 2 * 8 * 32 * 4) > slots_with(4 * 2 * 16 * 32 * 4)) ? 8 : 16;
-  static constexpr int EPI_BYTES = 4 * 2 * EPI_ROWS * 32 * 4;
+  // (GRP: two buffers of 4 KB, then a tile's rows and factors)
+  static constexpr int EPI_BYTES = 4 * 2 * EPI_ROWS * 32 * 4 + (GRP ? 2 * BT * 4 : 0);
   // GRP, quantized: the packed windows have a ring of their own, one or two
   // stages longer than the operand slots', so that a slot's decoders find their
   // window there when the slot is free (with one ring a slot went through the
@@ -1091,71 +1092,123 @@ struct GrpArg {};
 template <>
 struct GrpArg<true> : id::Slots {};
 
-// One column block of an expert's tile (32 columns of 32 lanes in r: lane =
-// output value k0 + lane) to its slots' rows; lane i holds column i's output
-// row (-1: none) and factor.  The block is turned in shared memory (RB rows of
-// 32 values at a time, `stg` the warp's own), so that four lanes store a row's
-// 32 values, eight each: about 110 instructions a block, where exchanging the
-// values between neighbouring lanes took 400 and held items of 16 stages up.
-template <int RB, class A>
-__device__ __forceinline__ void store_slots(const A& g, const uint32_t (&r)[32], int orow, float mul, int k0, int K,
-                                            int lane, float* stg) {
-  const int c = 8 * (lane & 3), k = k0 + c;
-  // odd rows read their halves in the other order: the two rows of a quarter warp's read on different banks
-  const int flip = 4 * ((lane >> 2) & 1);
+// The four epilogue warps; whether any thread passed true.
+__device__ __forceinline__ bool epilogue_any(bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(any))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// One column block of an expert's tile to its slots' rows: this warp's 32 of
+// the CTA's 128 values (lane = value) of 32 slots in r, whose output rows (-1:
+// none) and factors are rows[0..31] and muls[0..31].  The four warps turn 16
+// slots at a time (8 for F32 rows) in shared memory, two slots' 16-bit values a
+// word, and each stores whole rows of 128 values: a store instruction covers
+// one row, not pieces of eight, and the words cross shared memory once as 16
+// bits (exchanged between neighbouring lanes in registers, or turned a warp at a
+// time, the same rows cost 4.6 us more an item, taken from the decoders' share
+// of the load-store unit).  buf: two buffers of 4 KB, `step` counts them on.
+template <class A>
+__device__ __forceinline__ void store_slots(const A& g, const uint32_t (&r)[32], const int* rows, const float* muls,
+                                            int left, int k0, int K, int eq, int lane, uint32_t* buf, int& step) {
+  const int k = k0 + 4 * lane;
+  const bool plain = g.unscale == nullptr && g.weights == nullptr;
+  if (g.otype == RG_F32) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (8 * i % RB == 0) {
-      __syncwarp();  // (the reads of what lay there)
+    for (int h = 0; h < 4; ++h) {
+      if (8 * h >= left) break;
+      float* b = reinterpret_cast<float*>(buf + 1024 * (step++ & 1));
 #pragma unroll
-      for (int q = 0; q < RB; ++q) stg[q * 32 + lane] = __uint_as_float(r[8 * i + q]);
-      __syncwarp();
-    }
-    const int at = 8 * i + (lane >> 2), in = at % RB;
-    const int row = __shfl_sync(0xffffffffu, orow, at);
-    const float m = __shfl_sync(0xffffffffu, mul, at);
-    const float4 x = *reinterpret_cast<const float4*>(stg + in * 32 + c + flip);
-    const float4 y = *reinterpret_cast<const float4*>(stg + in * 32 + c + (4 - flip));
-    if (row < 0 || k >= K) continue;  // (K is a multiple of 8)
-    const float4 a = flip ? y : x, b = flip ? x : y;
-    float v[8] = {a.x * m, a.y * m, a.z * m, a.w * m, b.x * m, b.y * m, b.z * m, b.w * m};
-    if (g.otype == RG_F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
-      if (g.beta != 0.0f) {
-        const float4 p = o[0], q = o[1];
-        v[0] = fmaf(g.beta, p.x, v[0]); v[1] = fmaf(g.beta, p.y, v[1]);
-        v[2] = fmaf(g.beta, p.z, v[2]); v[3] = fmaf(g.beta, p.w, v[3]);
-        v[4] = fmaf(g.beta, q.x, v[4]); v[5] = fmaf(g.beta, q.y, v[5]);
-        v[6] = fmaf(g.beta, q.z, v[6]); v[7] = fmaf(g.beta, q.w, v[7]);
+      for (int i = 0; i < 8; ++i) {
+        const float v = __uint_as_float(r[8 * h + i]);
+        b[i * 128 + 32 * eq + lane] = plain ? v : v * muls[8 * h + i];
       }
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-      continue;
-    }
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
-    uint32_t w[4];
-    if (g.beta != 0.0f) {
-      const uint4 q = *o;
-      const uint32_t old[4] = {q.x, q.y, q.z, q.w};
+      epilogue_sync();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = g.otype == RG_F16
-                             ? __half22float2(u32_as_h2(old[e]))
-                             : make_float2(__uint_as_float(old[e] << 16), __uint_as_float(old[e] & 0xFFFF0000u));
-        v[2 * e] = fmaf(g.beta, f.x, v[2 * e]);
-        v[2 * e + 1] = fmaf(g.beta, f.y, v[2 * e + 1]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (g.otype == RG_F16) {
-        w[e] = h2_as_u32(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 2; ++i) {
+        const int at = 4 * i + eq, row = rows[8 * h + at];
+        float4 v = *reinterpret_cast<const float4*>(b + at * 128 + 4 * lane);
+        if (row < 0 || k >= K) continue;
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
+        if (g.beta != 0.0f) {
+          const float4 p = *o;
+          v.x = fmaf(g.beta, p.x, v.x);
+          v.y = fmaf(g.beta, p.y, v.y);
+          v.z = fmaf(g.beta, p.z, v.z);
+          v.w = fmaf(g.beta, p.w, v.w);
+        }
+        *o = v;
       }
     }
-    *o = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+  const bool f16 = g.otype == RG_F16;
+  auto pack = [&](float a, float b) {
+    if (f16) return h2_as_u32(__floats2half2_rn(a, b));
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  auto unpack = [&](uint32_t w) {
+    return f16 ? __half22float2(u32_as_h2(w)) : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  };
+  // (with a beta the sum is rounded, not the product: F32 words, half as many slots a step)
+  if (g.beta != 0.0f) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if (8 * h >= left) break;
+      float* b = reinterpret_cast<float*>(buf + 1024 * (step++ & 1));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i * 128 + 32 * eq + lane] = __uint_as_float(r[8 * h + i]) * muls[8 * h + i];
+      epilogue_sync();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = 4 * i + eq, row = rows[8 * h + at];
+        const float4 v = *reinterpret_cast<const float4*>(b + at * 128 + 4 * lane);
+        if (row < 0 || k >= K) continue;
+        uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + static_cast<int64_t>(row) * g.out_row + k);
+        const uint2 old = *o;
+        const float2 p = unpack(old.x), q = unpack(old.y);
+        *o = make_uint2(pack(fmaf(g.beta, p.x, v.x), fmaf(g.beta, p.y, v.y)),
+                        pack(fmaf(g.beta, q.x, v.z), fmaf(g.beta, q.y, v.w)));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (16 * h >= left) break;
+    uint32_t* b = buf + 1024 * (step++ & 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x = __uint_as_float(r[16 * h + 2 * i]), y = __uint_as_float(r[16 * h + 2 * i + 1]);
+      if (!plain) {
+        const float2 m = *reinterpret_cast<const float2*>(muls + 16 * h + 2 * i);
+        x *= m.x;
+        y *= m.y;
+      }
+      b[i * 128 + 32 * eq + lane] = pack(x, y);
+    }
+    epilogue_sync();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = 4 * i + eq;
+      const int2 row = *reinterpret_cast<const int2*>(rows + 16 * h + 2 * at);
+      const uint4 w = *reinterpret_cast<const uint4*>(b + at * 128 + 4 * lane);
+      if (k >= K) continue;
+      uint16_t* out = static_cast<uint16_t*>(g.out) + k;
+      if (row.x >= 0)
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(row.x) * g.out_row) =
+            make_uint2(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.z, w.w, 0x5410));
+      if (row.y >= 0)
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(row.y) * g.out_row) =
+            make_uint2(__byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x7632));
+    }
   }
 }
 
@@ -1673,6 +1726,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int SLAB_W = BT * 32;
     constexpr int ER = C::EPI_ROWS;  // rows of t in a staged box
     float* stg = reinterpret_cast<float*>(smem + C::OFF_EPI) + eq * (2 * ER * 32);
+    int* g_rows = reinterpret_cast<int*>(smem + C::OFF_EPI + 4 * 2 * ER * 32 * 4);  // GRP
+    float* g_muls = reinterpret_cast<float*>(g_rows + BT);
+    int g_step = 0;
     bool ok = true;
     Segs<SK> sg(unit, n_units, n_tiles, n_chunks);
     int tile = 0, c0 = 0, c1 = 0;
@@ -1684,25 +1740,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int kt = ku * CG + static_cast<int>(rank);
       const int a = j & 1;
       const uint32_t aph = (static_cast<uint32_t>(j) >> 1) & 1u;
-      // GRP: the tile's slots, all column blocks' loads in flight while the
-      // sums are still being made (one block's after the other's, behind the
-      // wait, held items of 16 to 32 stages up)
-      int orow[GRP ? BT / 32 : 1];
-      float mul[GRP ? BT / 32 : 1];
+      // GRP: the tile's rows and factors, each warp a quarter of them, loaded
+      // while the sums are still being made
+      int orow[GRP ? BT / 128 : 1];
+      float mul[GRP ? BT / 128 : 1];
       if constexpr (GRP) {
 #pragma unroll
-        for (int cb = 0; cb < BT / 32; ++cb) {
-          const bool in = 32 * cb + lane < st.rows;
-          orow[cb] = in ? __ldg(grp.order + st.pos + 32 * cb + lane) : -1;
-          mul[cb] = in && grp.unscale != nullptr ? __ldcg(grp.unscale + st.pos + 32 * cb + lane) : 1.0f;
+        for (int q = 0; q < BT / 128; ++q) {
+          const int at = (BT / 4) * eq + 32 * q + lane;
+          const bool in = at < st.rows;
+          orow[q] = in ? __ldg(grp.order + st.pos + at) : -1;
+          mul[q] = in && grp.unscale != nullptr ? __ldcg(grp.unscale + st.pos + at) : 1.0f;
         }
 #pragma unroll
-        for (int cb = 0; cb < BT / 32; ++cb) {
-          if (static_cast<unsigned>(orow[cb]) >= static_cast<unsigned>(grp.slots)) orow[cb] = -1;
-          if (grp.weights != nullptr && orow[cb] >= 0) mul[cb] *= __ldg(grp.weights + orow[cb]);
+        for (int q = 0; q < BT / 128; ++q) {
+          if (static_cast<unsigned>(orow[q]) >= static_cast<unsigned>(grp.slots)) orow[q] = -1;
+          if (grp.weights != nullptr && orow[q] >= 0) mul[q] *= __ldg(grp.weights + orow[q]);
         }
       }
       ok = __all_sync(0xffffffffu, mbar_wait(acc_full(a), aph, ctl, abort_flag));
+      if constexpr (GRP) {
+        // (no warp reads the last tile's rows and factors any more; a wait that
+        // gave up in one warp ends them all)
+        ok = !epilogue_any(!ok);
+#pragma unroll
+        for (int q = 0; q < BT / 128; ++q) {
+          g_rows[(BT / 4) * eq + 32 * q + lane] = orow[q];
+          g_muls[(BT / 4) * eq + 32 * q + lane] = mul[q];
+        }
+        epilogue_sync();
+      }
       if (!ok) break;
       tc_fence_after();
       const int k = kt * BM + 32 * eq + lane;
@@ -1715,7 +1782,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(32 * eq) << 16) +
                                  static_cast<uint32_t>(a * BT + 32 * cb),
                              r);
-          store_slots<2 * C::EPI_ROWS>(grp, r, orow[cb], mul[cb], kt * BM + 32 * eq, K, lane, stg);
+          store_slots(grp, r, g_rows + 32 * cb, g_muls + 32 * cb, st.rows - 32 * cb, kt * BM, K, eq, lane,
+                      reinterpret_cast<uint32_t*>(smem + C::OFF_EPI), g_step);
         }
         tc_fence_before();
         __syncwarp();

@@ -134,6 +134,16 @@ def test_same_bits_and_graphs(rg, fwd, tokens):
         assert np.array_equal(beside, want[1])
 
 
+@pytest.mark.parametrize("fwd", [True, False])
+@pytest.mark.parametrize("wtype", [inputs.Q8_0, inputs.BF16])
+def test_long_rows(rg, fwd, wtype):
+    """Input rows longer than a warp's share of the copy, many slots and few."""
+    rng = np.random.default_rng(6)
+    for tokens in (5, 90):
+        N, K = (72, 17 * 256) if fwd else (4488, 256)
+        Stack(torch, rg, wtype, 2, N, K, _ids(rng, tokens, 2, 2, 0.1), 2).check(fwd, BF16, TOKEN, SLOT, scale=1e-3)
+
+
 def test_bad_indices(rg):
     """Ranges and slots outside the batch are reported and count as none; nothing else is touched."""
     ids = np.array([0, 1, 2, 1, 0, 2], np.int32)
