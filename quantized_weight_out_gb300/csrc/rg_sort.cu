@@ -37,8 +37,10 @@ cudaError_t launch_sort(const int32_t* ids, int64_t n, int64_t groups, int32_t* 
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(sort_kernel), kSortMostSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // more than two steps a warp: eight blocks; few ids: fewer warps
-  const int blocks = n > 64 * SORT_MAX_WARPS ? SORT_MAX_BLOCKS : 1;
+  // more than two steps a warp: eight blocks, more than two with these: sixteen where the GPU
+  // holds such a cluster (65536 slots: the walk and the scattered stores 16 us with eight); few
+  // ids: fewer warps
+  int blocks = n > 64 * SORT_MAX_WARPS ? 8 : 1;
   const int threads = n <= 512 ? 256 : SORT_THREADS;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -53,6 +55,24 @@ cudaError_t launch_sort(const int32_t* ids, int64_t n, int64_t groups, int32_t* 
   attr[1].val.programmaticStreamSerializationAllowed = after_prev ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (n > 8 * 64 * SORT_MAX_WARPS) {
+    static std::atomic<int> sixteen[64];  // per device: 1 + whether a cluster of sixteen may be resident
+    const int yes = resident(sixteen[dev.device & 63], 1, [&](int* ok) {
+      cfg.gridDim = dim3(SORT_MAX_BLOCKS);
+      cfg.dynamicSmemBytes = kSortMostSmem;
+      attr[0].val.clusterDim.x = SORT_MAX_BLOCKS;
+      cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(sort_kernel),
+                                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      int clusters = 0;
+      if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &cfg);
+      *ok = clusters > 0 ? 2 : 1;
+      return r;
+    });
+    if (yes == 2) blocks = SORT_MAX_BLOCKS;
+    cfg.dynamicSmemBytes = static_cast<size_t>(sort_smem(p.bins, threads / 32));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+  }
   return counted(cudaLaunchKernelEx(&cfg, sort_kernel, p, dev.status));
 }
 

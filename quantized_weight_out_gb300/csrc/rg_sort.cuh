@@ -43,7 +43,7 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
 // The bytes of shared memory that sort_block needs: each warp's counts (rows of an odd length, so that the warps' of one
 // digit lie on different banks), the block's, and the digits' places.
 __host__ __device__ constexpr int sort_smem(int bins, int warps) { return (warps + 2) * (bins | 1) * 4; }
-constexpr int SORT_MAX_BLOCKS = 8;
+constexpr int SORT_MAX_BLOCKS = 16;
 
 // By every thread of every block of the cluster (whole warps, a power of two of them, at most 32).  ids are read past any
 // caching that a kernel before this one could have left behind (or lie in shared memory).
