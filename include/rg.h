@@ -476,7 +476,8 @@ size_t rg_kv_attend_workspace_bytes(const rg_kv_cache* cache, const rg_kv_batch*
  * serves every step.  An index below 0 is one that points nowhere (padding):
  * it reads as a row of zeros and adds nothing.  One past the end counts the
  * same and is reported as RG_ERR_INDEX (rg_check).  Results do not depend on
- * timing: no sum's order does.
+ * timing: no sum's order does.  A call's outputs overlap neither its inputs nor
+ * each other.  Rows are at most 2^30 values long (RG_ERR_ARG).
  */
 
 /* out[i, :] = scale * deq(W)[ids[i], :] for i < n: W is a table of N rows of
@@ -492,7 +493,7 @@ int rg_get_rows(int wtype, const void* W, int64_t N, int64_t K, const int32_t* i
  *     G[r, :] = beta * G[r, :] + scale * sum over ids[i] == r of dY[i, :]
  *
  * for every r < N.  dY: [n, K] of atype; G: [N, K] F32, rows g_row apart; K a
- * multiple of 8 (RG_ERR_SHAPE).  With beta 0 the old G is not read; with beta 1
+ * multiple of 8 (RG_ERR_SHAPE), at most 65535 * 1024 (RG_ERR_ARG).  With beta 0 the old G is not read; with beta 1
  * rows that no id names are left alone.  The ids are sorted on the device
  * (stable), and each row's sum is taken in F32 in the order of i, in windows of
  * the sorted order: the same bits every time.  The workspace comes from the
@@ -588,7 +589,7 @@ typedef enum {
  * (times |w_s|) plus the result's own rounding to atype.  F32 W, and rows of W
  * that are not 16-byte aligned (Q6_K, Q3_K with K % 2048 != 0, Q2_K with K %
  * 1024, MXFP4 with K % 512), take a slower route with exact values and F32
- * products.
+ * products (result rows of at most 65535 * 64 values, RG_ERR_ARG).
  *
  * The workspace (rg_*_id_workspace_bytes) comes from the library's
  * stream-ordered pool, or from the caller in the _ws forms (256-byte aligned;

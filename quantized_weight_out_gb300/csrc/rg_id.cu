@@ -305,8 +305,7 @@ cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int ca
   (void)b;
   (void)dev;
   const int64_t rb = p.K / block_values(p.wtype) * block_bytes(p.wtype);
-  const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;
-  if (gy > 65535) return cudaErrorInvalidConfiguration;
+  const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;  // (at most 65535)
   return with_wtype(p.wtype, cudaErrorInvalidValue, [&](auto wt) {
     constexpr int WT = decltype(wt)::value;
     auto kern = p.fwd ? simt_kernel<WT, true> : simt_kernel<WT, false>;

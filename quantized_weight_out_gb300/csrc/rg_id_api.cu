@@ -10,6 +10,10 @@ using namespace rg;
 namespace {
 
 constexpr int64_t kMaxDim = 2147483647;
+// Places inside a row are 32-bit in the kernels, with room for a tile past the end.
+constexpr int64_t kMaxWidth = int64_t{1} << 30;
+// Columns of the widest launches (65535 blocks along a row).
+constexpr int64_t kMaxBackWidth = int64_t{65535} * 1024, kMaxSimtWidth = int64_t{65535} * id::kSimtTile;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool valid_act(int t) { return t == RG_F32 || t == RG_F16 || t == RG_BF16; }
@@ -26,7 +30,7 @@ int check_rows(const void* p, int64_t row, int64_t width, int atype) {
 // A weight of rows of K values (and how many rows): types, sizes and shapes.
 int check_weight(int wtype, int64_t N, int64_t K) {
   if (!valid_wtype(wtype)) return RG_ERR_TYPE;
-  if (N < 0 || K < 0 || N > kMaxDim || K > kMaxDim) return RG_ERR_ARG;
+  if (N < 0 || K < 0 || N > kMaxDim || K > kMaxWidth) return RG_ERR_ARG;
   return K % (is_quant(wtype) ? 256 : 8) ? RG_ERR_SHAPE : RG_OK;
 }
 
@@ -74,9 +78,9 @@ int check_batch(const rg_id_batch* x, id::Batch* b) {
   return RG_OK;
 }
 
-// The rows of W start at multiples of 16 bytes, which TMA needs.
-bool aligned_rows(int wtype, int64_t K) {
-  return (K / block_values(wtype) * block_bytes(wtype)) % 16 == 0;
+// F32 W, and rows of W that do not start at multiples of 16 bytes, which TMA needs.
+bool takes_simt(int wtype, int64_t K) {
+  return wtype == RG_F32 || (K / block_values(wtype) * block_bytes(wtype)) % 16 != 0;
 }
 
 struct Plan {
@@ -92,7 +96,7 @@ constexpr int64_t kFewSlots = 8;
 
 Plan plan(const id::Product& p, const id::Batch& b) {
   Plan r{};
-  r.simt = p.wtype == RG_F32 || !aligned_rows(p.wtype, p.K);
+  r.simt = takes_simt(p.wtype, p.K);
   // a few slots an expert: W's rows streamed once; else tiles of 128 or 256 slots
   r.few = !r.simt && b.slots <= kFewSlots * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
   r.cg = b.slots > 128 * static_cast<int64_t>(b.experts) ? 2 : 1;
@@ -161,13 +165,14 @@ int check_shape(bool fwd, int wtype, int64_t N, int64_t K, const rg_id_batch* ba
   int st = check_batch(batch, b);
   if (st != RG_OK || (st = check_weight(wtype, N, K)) != RG_OK) return st;
   if (N % 8) return RG_ERR_SHAPE;
+  if (N > kMaxWidth) return RG_ERR_ARG;
   if (out_of != RG_ROWS_SLOT && out_of != RG_ROWS_TOKEN) return RG_ERR_ARG;
   p->fwd = fwd;
   p->wtype = wtype;
   p->N = N;
   p->K = K;
   p->out_tokens = out_of == RG_ROWS_TOKEN;
-  return RG_OK;
+  return takes_simt(wtype, K) && p->out_w() > kMaxSimtWidth ? RG_ERR_ARG : RG_OK;
 }
 
 int product(bool fwd, int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype,
@@ -242,7 +247,7 @@ int rg_get_rows(int wtype, const void* W, int64_t N, int64_t K, const int32_t* i
 }
 
 size_t rg_get_rows_back_workspace_bytes(int64_t n, int64_t N, int64_t K) {
-  if (n < 1 || N < 1 || K < 1 || n > kMaxDim || N > kMaxDim || K > kMaxDim || K % 8) return 0;
+  if (n < 1 || N < 1 || K < 1 || n > kMaxDim || N > kMaxDim || K > kMaxBackWidth || K % 8) return 0;
   return id::rows_back_workspace(n, N, K);
 }
 
@@ -254,7 +259,7 @@ int rows_back(int atype, const void* dY, int64_t dy_row, const int32_t* ids, int
               int64_t g_row, int64_t N, int64_t K, float beta, void* ws, size_t ws_bytes, bool own_ws,
               cudaStream_t stream) {
   if (!valid_act(atype)) return RG_ERR_TYPE;
-  if (n < 0 || N < 0 || K < 0 || n > kMaxDim || N > kMaxDim || K > kMaxDim) return RG_ERR_ARG;
+  if (n < 0 || N < 0 || K < 0 || n > kMaxDim || N > kMaxDim || K > kMaxBackWidth) return RG_ERR_ARG;
   if (K % 8) return RG_ERR_SHAPE;
   if (N == 0 || K == 0) return RG_OK;
   int st = check_rows(G, g_row, K, RG_F32);

@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
 
 // Bytes of a row of X in shared memory: 64 off a multiple of 128 apart, so that two rows' 16-byte reads of a quarter
 // warp fall on different banks.
-int x_stride(int64_t K) { return static_cast<int>((K * 2 + 127) / 128 * 128 + 64); }
+int64_t x_stride(int64_t K) { return (K * 2 + 127) / 128 * 128 + 64; }
 
 template <int WT, int NT>
 cudaError_t launch_few_t(Few f, const DevInfo& dev, cudaStream_t stream) {
@@ -637,11 +637,12 @@ cudaError_t launch_few_t(Few f, const DevInfo& dev, cudaStream_t stream) {
 
 }  // namespace
 
-// Slots a chunk: eight to an MMA, as many as an expert has on average three times over (few experts
-// have more) up to 32, no more than there are tokens, while the rows of X take at most 96 KB.
+// Slots a chunk: one MMA's eight, or two's where an expert has more than five on average (40 tokens,
+// 5 slots an expert of 64: 50 us with eight, 59 with sixteen), no more than there are tokens, while
+// the rows of X take at most 96 KB.
 int few_slots(const Batch& b, const Product& p) {
   const int64_t avg = (b.slots + std::min(b.experts, b.slots) - 1) / std::min(b.experts, b.slots);
-  const int64_t want = std::min<int64_t>(avg <= 5 ? 8 : avg <= 10 ? 16 : 32, b.slots / b.per_token);
+  const int64_t want = std::min<int64_t>(avg <= 5 ? 8 : 16, b.slots / b.per_token);
   return static_cast<int>(std::min<int64_t>(want, 96 * 1024 / x_stride(p.K)));
 }
 
@@ -664,7 +665,7 @@ cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t
   f.atype = p.atype;
   f.ns = few_slots(b, p);
   f.cap = static_cast<int>(max_tiles(b.slots, b.experts, f.ns));
-  f.xstride = x_stride(p.K);
+  f.xstride = static_cast<int>(x_stride(p.K));
   f.weights = s.weights;
   f.out = s.out;
   f.out_row = s.out_row;
@@ -677,9 +678,7 @@ cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t
     if constexpr (WT == RG_F32) {
       return cudaErrorInvalidValue;
     } else {
-      return f.ns <= 8    ? launch_few_t<WT, 1>(f, dev, stream)
-             : f.ns <= 16 ? launch_few_t<WT, 2>(f, dev, stream)
-                          : launch_few_t<WT, 4>(f, dev, stream);
+      return f.ns <= 8 ? launch_few_t<WT, 1>(f, dev, stream) : launch_few_t<WT, 2>(f, dev, stream);
     }
   });
 }

@@ -218,8 +218,7 @@ cudaError_t launch_rows_back(int atype, const void* dY, int64_t dy_row, const in
     at += up256(bytes);
     return p;
   };
-  const int64_t windows = (n + WIN - 1) / WIN, chunks = (K + COLS - 1) / COLS;
-  if (chunks > 65535) return cudaErrorInvalidConfiguration;
+  const int64_t windows = (n + WIN - 1) / WIN, chunks = (K + COLS - 1) / COLS;  // (chunks: at most 65535)
   int32_t* order = reinterpret_cast<int32_t*>(take(n * 4));
   int32_t* sorted = reinterpret_cast<int32_t*>(take(n * 4));
   float* head = reinterpret_cast<float*>(take(windows * K * 4));

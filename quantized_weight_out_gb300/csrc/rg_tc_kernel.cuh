@@ -1650,9 +1650,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if constexpr (AD) c_ad = n_main - (tile / n_tiles1) * n_chunks;
           for (; c < len; c += S, ph ^= 1u) {
             const int cc = c0 + c;  // the chunk of the item
-            bool got = mbar_wait(full_p(ps), C::P_RING ? pph : ph, ctl, abort_flag);
-            // (with one ring the window was loaded when the slot was free)
-            if constexpr (C::P_RING) got = got && wait_any(empty(s), ph ^ 1u);
+            // (with one ring the window was loaded when the slot was free.  P_RING:
+            // the slot first.  When it is free, the window that stage i - PS had in
+            // this window's place has been decoded, so its phase is over; before
+            // that, as windows may land out of order, the wait could take the phase
+            // before that one for this stage's.)
+            bool got = true;
+            if constexpr (C::P_RING) got = wait_any(empty(s), ph ^ 1u);
+            got = got && mbar_wait(full_p(ps), C::P_RING ? pph : ph, ctl, abort_flag);
             if (!__all_sync(0xffffffffu, got)) {
               run = false;
               break;

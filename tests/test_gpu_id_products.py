@@ -2,12 +2,13 @@
 import numpy as np
 import pytest
 
+import oracle
 from quantized_weight_out_gb300 import inputs
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from id_common import BF16, F16, F32, SLOT, TOKEN, Stack  # noqa: E402
+from id_common import BF16, F16, F32, SLOT, TOKEN, Stack, product_tolerance  # noqa: E402
 
 TYPES = inputs.ALL_TYPES
 
@@ -49,8 +50,11 @@ def test_types(rg, wtype, fwd):
 @pytest.mark.parametrize("atype", [F32, F16, BF16])
 @pytest.mark.parametrize("x_of,out_of", [(SLOT, SLOT), (TOKEN, SLOT), (SLOT, TOKEN), (TOKEN, TOKEN)])
 def test_forms(rg, wtype, fwd, atype, x_of, out_of):
-    """Whose rows go in and come out, weights, beta, padded rows, a caller's workspace; pairs of CTAs and single ones."""
+    """Whose rows go in and come out, weights, beta, padded rows, a caller's workspace; few slots an expert, tiles of
+    single CTAs and of pairs."""
     rng = np.random.default_rng(7)
+    one = Stack(torch, rg, wtype, 4, 264, 2048, _ids(rng, 6, 2, 4, 0.2), 2)
+    one.check(fwd, atype, x_of, out_of, weigh=True, beta=-1.5, pad=8, ws=True)
     few = Stack(torch, rg, wtype, 4, 264, 2048, _ids(rng, 37, 2, 4, 0.2), 2)
     few.check(fwd, atype, x_of, out_of, weigh=True, beta=0.5, pad=16, ws=True)
     many = Stack(torch, rg, wtype, 3, 264, 2048, _ids(rng, 301, 2, 3, 0.05), 2)
@@ -59,7 +63,8 @@ def test_forms(rg, wtype, fwd, atype, x_of, out_of):
 
 @pytest.mark.parametrize("fwd", [True, False])
 @pytest.mark.parametrize("counts", [
-    [0, 300, 0, 1], [128, 128, 256, 0], [127, 129, 255, 257], [0, 0, 0, 512], [1, 1, 1, 1], [513, 0, 31, 33]])
+    [0, 300, 0, 1], [128, 128, 256, 0], [127, 129, 255, 257], [0, 0, 0, 512], [1, 1, 1, 1], [513, 0, 31, 33],
+    [0, 0, 20, 0], [0, 32, 0, 0], [8, 9, 7, 1], [16, 1, 0, 15]])
 def test_ragged(rg, fwd, counts):
     """Groups that fill tiles exactly, miss by one, or are empty."""
     ids = np.repeat(np.arange(len(counts)), counts)
@@ -142,6 +147,40 @@ def test_long_rows(rg, fwd, wtype):
     for tokens in (5, 90):
         N, K = (72, 17 * 256) if fwd else (4488, 256)
         Stack(torch, rg, wtype, 2, N, K, _ids(rng, tokens, 2, 2, 0.1), 2).check(fwd, BF16, TOKEN, SLOT, scale=1e-3)
+
+
+@pytest.mark.parametrize("fwd", [True, False])
+@pytest.mark.parametrize("wtype", [inputs.Q4_K, inputs.Q8_0, inputs.MXFP4])
+def test_long_pipelines_same_bits(rg, wtype, fwd):
+    """Several items a unit of a hundred and more stages each, over and over: the copies' order of arrival changes, the
+    result does not (and is right)."""
+    rng = np.random.default_rng(13)
+    N, K = (512, 6656) if fwd else (6952, 512)
+    s = Stack(torch, rg, wtype, 16, N, K, _ids(rng, 2300, 5, 16, 0.01), 5, W=_tiled(wtype, 16, N, K))
+    x = s.act(s.slots, K if fwd else N, BF16, 0.1)
+    x_d = s.put(x, BF16)
+    out = torch.zeros(s.slots, N if fwd else K, dtype=torch.bfloat16, device=s.dev)
+    call, st = (rg.rg_mul_mat_id if fwd else rg.rg_out_prod_id), torch.cuda.current_stream()
+    first = None
+    for _ in range(60):
+        rg.check(call(wtype, s.W_d, N, K, s.batch, BF16, x_d, x.shape[1], SLOT, out, out.shape[1], SLOT, None, 0.0, st))
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+    assert rg.rg_check(st) == 0
+    some = rng.choice(np.nonzero(s.ids >= 0)[0], 40, replace=False)
+    few = np.full(s.slots, -1)
+    few[some] = s.ids[some]
+    ref, mag = oracle.product_id(fwd, wtype, s.W, 16, N, K, few, 5, x, False, None)
+    tol = product_tolerance(wtype, K, x.shape[1], BF16, mag[some], ref[some])
+    assert (np.abs(first.float().cpu().numpy()[some] - ref[some]) <= tol).all()
+
+
+def _tiled(wtype, experts, N, K):
+    """A stack from a few generated rows, each expert's in an order of its own."""
+    rows = inputs.gen_weight(wtype, 64, K, seed=3, stream=1)
+    rows = np.ascontiguousarray(rows).view(np.uint8).reshape(64, -1)
+    pick = np.random.default_rng(5).integers(0, 64, experts * N)
+    return rows[pick].reshape(-1)
 
 
 def test_bad_indices(rg):

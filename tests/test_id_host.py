@@ -29,6 +29,7 @@ ROWS = dict(wtype=Q8, W=BAD, N=10, K=256, ids=BAD, n=3, scale=1.0, atype=BF16, o
     (dict(ids=None), rg.RG_ERR_ARG), (dict(out=None), rg.RG_ERR_ARG), (dict(out_row=248), rg.RG_ERR_ARG),
     (dict(out_row=260), rg.RG_ERR_ALIGN), (dict(atype=F32, out_row=258), rg.RG_ERR_ALIGN),
     (dict(W=BAD + 8), rg.RG_ERR_ALIGN), (dict(ids=BAD + 2), rg.RG_ERR_ALIGN), (dict(out=BAD + 8), rg.RG_ERR_ALIGN),
+    (dict(K=(1 << 30) + 256, out_row=1 << 31), rg.RG_ERR_ARG),
     (dict(n=0, W=None, ids=None, out=None), rg.RG_OK), (dict(K=0, W=None, out=None), rg.RG_OK),
 ])
 def test_get_rows_refusals(lib, change, status):
@@ -44,6 +45,7 @@ BACK = dict(atype=BF16, dY=BAD, dy_row=64, ids=BAD, n=3, scale=1.0, G=BAD, g_row
     (dict(dY=None), rg.RG_ERR_ARG), (dict(ids=None), rg.RG_ERR_ARG), (dict(dy_row=56), rg.RG_ERR_ARG),
     (dict(g_row=56), rg.RG_ERR_ARG), (dict(dy_row=68), rg.RG_ERR_ALIGN), (dict(g_row=66), rg.RG_ERR_ALIGN),
     (dict(G=BAD + 4), rg.RG_ERR_ALIGN), (dict(dY=BAD + 8), rg.RG_ERR_ALIGN), (dict(ids=BAD + 1), rg.RG_ERR_ALIGN),
+    (dict(K=65535 * 1024 + 8, dy_row=1 << 28, g_row=1 << 28), rg.RG_ERR_ARG),
     (dict(N=0, G=None, dY=None), rg.RG_OK), (dict(K=0, G=None, dY=None), rg.RG_OK),
 ])
 def test_rows_back_refusals(lib, change, status):
@@ -115,6 +117,7 @@ CALLS = [
     (dict(x_row=56), rg.RG_ERR_ARG), (dict(x_row=1004), rg.RG_ERR_ALIGN), (dict(x_of=2), rg.RG_ERR_ARG),
     (dict(y=None), rg.RG_ERR_ARG), (dict(y=BAD + 4), rg.RG_ERR_ALIGN), (dict(y_row=56), rg.RG_ERR_ARG),
     (dict(y_row=1004), rg.RG_ERR_ALIGN), (dict(y_of=-1), rg.RG_ERR_ARG), (dict(weights=BAD + 2), rg.RG_ERR_ALIGN),
+    (dict(N=(1 << 30) + 8), rg.RG_ERR_ARG), (dict(K=(1 << 30) + 256), rg.RG_ERR_ARG),
 ]
 CALL = dict(wtype=Q8, W=BAD, N=64, K=256, batch=None, atype=BF16, x=BAD, x_row=256, x_of=0, y=BAD, y_row=256, y_of=0,
             weights=None, beta=0.0)
@@ -137,6 +140,15 @@ def test_product_batch_refusals(lib, batch, status):
 @pytest.mark.parametrize("change,status", CALLS)
 def test_product_refusals(lib, change, status):
     _calls(lib, {}, change, status)
+
+
+def test_the_plain_routes_widest_rows(lib):
+    b = rg.rg_id_batch(*BATCH.values())
+    wide = 65535 * 64 + 8
+    a = dict(CALL, batch=b, wtype=F32, N=wide, K=8, x_row=wide, y_row=wide)
+    assert rg.rg_mul_mat_id(*a.values()) == rg.RG_ERR_ARG
+    a = dict(CALL, batch=b, wtype=F32, N=8, K=wide, x_row=wide, y_row=wide)
+    assert rg.rg_out_prod_id(*a.values()) == rg.RG_ERR_ARG
 
 
 def test_product_without_a_batch(lib):
