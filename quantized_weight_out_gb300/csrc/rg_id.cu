@@ -308,10 +308,15 @@ cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int ca
   const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;  // (at most 65535)
   return with_wtype(p.wtype, cudaErrorInvalidValue, [&](auto wt) {
     constexpr int WT = decltype(wt)::value;
-    auto kern = p.fwd ? simt_kernel<WT, true> : simt_kernel<WT, false>;
-    return counted(launch_after_prev(kern, dim3(static_cast<unsigned>(cap), static_cast<unsigned>(gy)), dim3(THREADS),
-                                     stream, s, static_cast<const uint8_t*>(p.W), p.N, p.K, rb, p.in, p.in_row,
-                                     p.in_tokens ? 1 : 0, p.atype));
+    // (the other types' rows are multiples of 16 bytes at every K)
+    if constexpr (WT != RG_F32 && WT != RG_Q6_K && WT != RG_Q3_K && WT != RG_Q2_K && WT != RG_MXFP4) {
+      return cudaErrorInvalidValue;
+    } else {
+      auto kern = p.fwd ? simt_kernel<WT, true> : simt_kernel<WT, false>;
+      return counted(launch_after_prev(kern, dim3(static_cast<unsigned>(cap), static_cast<unsigned>(gy)), dim3(THREADS),
+                                       stream, s, static_cast<const uint8_t*>(p.W), p.N, p.K, rb, p.in, p.in_row,
+                                       p.in_tokens ? 1 : 0, p.atype));
+    }
   });
 }
 

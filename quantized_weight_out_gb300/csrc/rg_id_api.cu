@@ -91,15 +91,43 @@ struct Plan {
   size_t tiles, count, x16, unscale, live, rows, total;  // offsets, and the bytes of all
 };
 
-// Slots an expert on average up to which the streaming kernel runs.
-constexpr int64_t kFewSlots = 8;
+// Slots an expert on average up to which the streaming kernel runs. It decodes
+// W anew for each chunk of an expert's slots, a tile of 128 slots decodes once;
+// so the limit falls where the decoding costs it most. Measured, us of tiles /
+// streaming, 8 experts of 14336 x 4096 at the limit and above it:
+//   Q4_K 5: 156 / 125, 8: 156 / 185; Q8_0 5: 164 / 115, 8: 164 / 173; MXFP4 5: 152 / 167 (64 of
+//   2048 x 1536: 92 / 78), 8: 179 / 224; Q4_0 5: 137 / 105, 8: 161 / 162; Q2_K 5: 166 / 162, 8: 166 / 195;
+//   Q4_1 4: 159 / 144, 5: 159 / 162, 8: 159 / 199
+//   Q6_K 8: 245 / 208, 16: 92 / 107 (32 of 2048 x 2048); Q3_K 8: 270 / 253, 16: 270 / 384
+//   (their tiles take two scales for 32 values)
+//   Q5_0 2: 149 / 136, 4: 150 / 163; Q5_1 2: 70 / 58 (32 of 2048 x 2048), 5: 173 / 212
+//   Q5_K 1: 172 / 99, 2: 152 / 158; BF16 1: 210 / 187, 2: 168 / 183, 4: 173 / 238 (F16 alike)
+constexpr int few_slots_limit(int wtype) {
+  switch (wtype) {
+    case RG_F16:
+    case RG_BF16:
+    case RG_Q5_K: return 1;
+    case RG_Q5_0:
+    case RG_Q5_1: return 2;
+    case RG_Q6_K:
+    case RG_Q3_K: return 8;
+    default: return 5;
+  }
+}
+
+// Slots an expert on average from which a tile is a pair of blocks' (256 slots,
+// each decoding half of W's rows). A half-empty pair costs more than a single
+// block; a group in two single tiles decodes W twice. Single / pair, us, 32
+// experts of 2048 x 2048: 96 slots Q4_K 71 / 75, BF16 79 / 80, MXFP4 84 / 85; 128
+// slots 86 / 78, 88 / 81, 100 / 90; 256 slots 140 / 98, 115 / 100, 161 / 118.
+constexpr int64_t kPairSlots = 128;
 
 Plan plan(const id::Product& p, const id::Batch& b) {
   Plan r{};
   r.simt = takes_simt(p.wtype, p.K);
   // a few slots an expert: W's rows streamed once; else tiles of 128 or 256 slots
-  r.few = !r.simt && b.slots <= kFewSlots * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
-  r.cg = b.slots > 128 * static_cast<int64_t>(b.experts) ? 2 : 1;
+  r.few = !r.simt && b.slots <= few_slots_limit(p.wtype) * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
+  r.cg = b.slots >= kPairSlots * b.experts ? 2 : 1;
   r.bt = r.simt ? id::kSimtTile : 128 * r.cg;
   r.cap = static_cast<int>(id::max_tiles(b.slots, b.experts, r.bt));
   r.joined = p.out_tokens;

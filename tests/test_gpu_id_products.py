@@ -45,6 +45,15 @@ def test_types(rg, wtype, fwd):
         s.check(fwd, BF16, TOKEN, SLOT)
 
 
+@pytest.mark.parametrize("wtype", TYPES)
+@pytest.mark.parametrize("x_of,out_of", [(SLOT, SLOT), (TOKEN, TOKEN)])
+def test_fewest(rg, wtype, x_of, out_of):
+    """Fewer slots than experts, apart or all of one expert: the form of the fewest, whatever the type."""
+    for ids, per in (([30, 2], 2), ([7] * 22, 1), ([0, 31, 0, 4, -1, 0, 31, 5, 0, 6, 0, 0, 0, 0, 0, 0], 2)):
+        s = Stack(torch, rg, wtype, 32, 72, 2048, ids, per)
+        s.check(True, BF16, x_of, out_of, weigh=out_of == TOKEN, beta=0.5, pad=8)
+
+
 @pytest.mark.parametrize("wtype", [inputs.Q4_K, inputs.Q6_K, inputs.BF16, inputs.MXFP4])
 @pytest.mark.parametrize("fwd", [True, False])
 @pytest.mark.parametrize("atype", [F32, F16, BF16])
@@ -225,19 +234,21 @@ def test_far_expert(rg):
     W = torch.zeros(need, dtype=torch.uint8, device="cuda:0")
     last = inputs.gen_weight(inputs.BF16, N, K, seed=4, stream=1)
     W[(E - 1) * N * K * 2:] = torch.from_numpy(np.ascontiguousarray(last).view(np.uint8).reshape(-1)).to("cuda:0")
-    s = Stack(torch, rg, inputs.BF16, 1, N, K, [0, 0, 0], 1, W=last)
-    for fwd in (True, False):
-        x = s.act(3, K if fwd else N, BF16)
-        want = s.run(fwd, BF16, x, SLOT, SLOT)
-        start = torch.tensor([0] * E + [3], dtype=torch.int32, device="cuda:0")
+    for fwd, slots in ((True, 3), (True, 70), (False, 3)):  # slots streamed past W, and tiles of them
+        s = Stack(torch, rg, inputs.BF16, 1, N, K, [0] * slots, 1, W=last)
+        wide = K if fwd else N
+        x = s.act(slots, wide, BF16)
+        ref, mag = oracle.product_id(fwd, inputs.BF16, last, 1, N, K, s.ids, 1, x, False, None)
+        start = torch.tensor([0] * E + [slots], dtype=torch.int32, device="cuda:0")
         batch = rg.id_batch(E, 1, start, s.order_d)
-        out = s.put(np.full(want.shape, np.nan), BF16)
+        out = s.put(np.full(ref.shape, np.nan), BF16)
         st = torch.cuda.current_stream()
         call = rg.rg_mul_mat_id if fwd else rg.rg_out_prod_id
-        rg.check(call(inputs.BF16, W, N, K, batch, BF16, s.put(x, BF16), x.shape[1], SLOT, out, want.shape[1], SLOT, None,
+        rg.check(call(inputs.BF16, W, N, K, batch, BF16, s.put(x, BF16), x.shape[1], SLOT, out, ref.shape[1], SLOT, None,
                       0.0, st))
         assert rg.rg_check(st) == 0
-        assert np.array_equal(out.float().cpu().numpy(), want)
+        err = np.abs(out.float().cpu().numpy() - ref)
+        assert (err <= product_tolerance(inputs.BF16, K, wide, BF16, mag, ref)).all()
 
 
 def test_gradient_is_the_forwards(rg):
