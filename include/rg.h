@@ -586,10 +586,11 @@ typedef enum {
  * once, after a power of two that brings its largest magnitude to 2^14 (fp16),
  * undone exactly afterwards: rows of any magnitude keep 11 bits and none
  * overflows, so RG_ERR_RANGE is not reported.  |err| <= 5e-3 * sum |in||deq W|
- * (times |w_s|) plus the result's own rounding to atype.  F32 W, and rows of W
- * that are not 16-byte aligned (Q6_K, Q3_K with K % 2048 != 0, Q2_K with K %
- * 1024, MXFP4 with K % 512), take a slower route with exact values and F32
- * products (result rows of at most 65535 * 64 values, RG_ERR_ARG).
+ * (times |w_s|) plus the result's own rounding to atype.  F32 W takes a slower
+ * route with F32 products (result rows of at most 65535 * 64 values,
+ * RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K with
+ * K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the
+ * used experts', to such in the workspace, which is larger by W's size.
  *
  * The workspace (rg_*_id_workspace_bytes) comes from the library's
  * stream-ordered pool, or from the caller in the _ws forms (256-byte aligned;

@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* rows, int64_
 }
 
 // A tile of 64 slots by 64 outputs; 32 contraction values a step, each thread
-// 4 x 4 sums.  F32 values of W decoded exactly, F32 products and sums.
-template <int WT, bool FWD>
+// 4 x 4 sums.  F32 weights, products and sums.
+template <bool FWD>
 __global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* __restrict__ W, int64_t N, int64_t K,
                                                        int64_t rb, const void* __restrict__ in, int64_t in_row,
                                                        int in_tokens, int atype) {
@@ -219,12 +219,12 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* _
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if constexpr (FWD) {
         const int n = tid >> 2, cc = 8 * (tid & 3);
-        if (o0 + n < N && c0 + cc < K) decode8_f32<WT>(we + (o0 + n) * rb, static_cast<int>(c0) + cc, v);
+        if (o0 + n < N && c0 + cc < K) decode8_f32<RG_F32>(we + (o0 + n) * rb, static_cast<int>(c0) + cc, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sw[cc + i][n] = v[i];
       } else {
         const int n = tid >> 3, kk = 8 * (tid & 7);
-        if (c0 + n < N && o0 + kk < K) decode8_f32<WT>(we + (c0 + n) * rb, static_cast<int>(o0) + kk, v);
+        if (c0 + n < N && o0 + kk < K) decode8_f32<RG_F32>(we + (c0 + n) * rb, static_cast<int>(o0) + kk, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sw[n][kk + i] = v[i];
       }
@@ -255,6 +255,43 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* _
       float v = acc[i][j] * m;
       if (g.beta != 0.0f) v = fmaf(g.beta, load_act(to, g.otype, o), v);
       store_act(to, g.otype, o, v);
+    }
+  }
+}
+
+// Rows of `rb` bytes (a multiple of 2) copied to rows of `grains` 16-byte
+// grains, zeros behind their end: what TMA needs of the types whose rows are not
+// multiples of 16 bytes (Q6_K, Q3_K, Q2_K, MXFP4 at some K).  A warp a row; an
+// expert without slots is skipped.  Whole products with the copy, against plain
+// threads that read the rows as they lie: 64 Q6_K experts of 2048 x 1536, 2 / 16 /
+// 256 slots an expert, 122 / 187 / 270 us against 745 / 916 / 4449; 128 MXFP4
+// experts of 2048 x 768, 107 / 151 / 282 against 713 / 840 / 4115.
+constexpr int PAD_ROWS = 32;
+
+__global__ void __launch_bounds__(THREADS) pad_kernel(const uint8_t* __restrict__ W, int64_t N, int64_t rb,
+                                                      const int32_t* __restrict__ start, uint4* __restrict__ to,
+                                                      int64_t grains) {
+  const int e = blockIdx.y;
+  if (__ldg(start + e + 1) <= __ldg(start + e)) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * PAD_ROWS;
+  for (int64_t n = first + (threadIdx.x >> 5); n < min(N, first + PAD_ROWS); n += THREADS / 32) {
+    const int64_t row = e * N + n;
+    const uint8_t* from = W + row * rb;
+    const int shift = (row * rb & 2) ? 16 : 0;  // (W is 16-byte aligned)
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(from - (shift >> 3));
+    for (int64_t j = lane; j < grains; j += 32) {
+      uint32_t w[5], v[4];
+#pragma unroll
+      for (int i = 0; i < 5; ++i)  // words that hold bytes of the row
+        w[i] = 16 * j + 4 * i < rb + (shift >> 3) ? __ldg(words + 4 * j + i) : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __funnelshift_r(w[i], w[i + 1], shift);
+        const int64_t left = rb - 16 * j - 4 * i;
+        v[i] = left <= 0 ? 0 : left < 4 ? v[i] & 0xFFFFu : v[i];
+      }
+      to[row * grains + j] = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }
@@ -304,20 +341,20 @@ cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int ca
                         cudaStream_t stream) {
   (void)b;
   (void)dev;
-  const int64_t rb = p.K / block_values(p.wtype) * block_bytes(p.wtype);
+  const int64_t rb = row_bytes(p.wtype, p.K);
   const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;  // (at most 65535)
-  return with_wtype(p.wtype, cudaErrorInvalidValue, [&](auto wt) {
-    constexpr int WT = decltype(wt)::value;
-    // (the other types' rows are multiples of 16 bytes at every K)
-    if constexpr (WT != RG_F32 && WT != RG_Q6_K && WT != RG_Q3_K && WT != RG_Q2_K && WT != RG_MXFP4) {
-      return cudaErrorInvalidValue;
-    } else {
-      auto kern = p.fwd ? simt_kernel<WT, true> : simt_kernel<WT, false>;
-      return counted(launch_after_prev(kern, dim3(static_cast<unsigned>(cap), static_cast<unsigned>(gy)), dim3(THREADS),
-                                       stream, s, static_cast<const uint8_t*>(p.W), p.N, p.K, rb, p.in, p.in_row,
-                                       p.in_tokens ? 1 : 0, p.atype));
-    }
-  });
+  auto kern = p.fwd ? simt_kernel<true> : simt_kernel<false>;
+  return counted(launch_after_prev(kern, dim3(static_cast<unsigned>(cap), static_cast<unsigned>(gy)), dim3(THREADS),
+                                   stream, s, static_cast<const uint8_t*>(p.W), p.N, p.K, rb, p.in, p.in_row,
+                                   p.in_tokens ? 1 : 0, p.atype));
+}
+
+cudaError_t launch_pad(const Product& p, const Batch& b, void* to, cudaStream_t stream) {
+  const unsigned gx = static_cast<unsigned>((p.N + PAD_ROWS - 1) / PAD_ROWS);
+  pad_kernel<<<dim3(gx, static_cast<unsigned>(b.experts)), THREADS, 0, stream>>>(
+      static_cast<const uint8_t*>(p.W), p.N, row_bytes(p.wtype, p.K), b.start, static_cast<uint4*>(to),
+      padded_row_bytes(p.wtype, p.K) / 16);
+  return counted(cudaGetLastError());
 }
 
 }  // namespace id

@@ -78,17 +78,13 @@ int check_batch(const rg_id_batch* x, id::Batch* b) {
   return RG_OK;
 }
 
-// F32 W, and rows of W that do not start at multiples of 16 bytes, which TMA needs.
-bool takes_simt(int wtype, int64_t K) {
-  return wtype == RG_F32 || (K / block_values(wtype) * block_bytes(wtype)) % 16 != 0;
-}
-
 struct Plan {
   bool simt, few;
+  bool padded;    // W's rows are copied first, to multiples of 16 bytes
   int cg, bt, cap;
   bool joined;    // rows of `out` are the tokens'
   bool bf16;
-  size_t tiles, count, x16, unscale, live, rows, total;  // offsets, and the bytes of all
+  size_t tiles, count, x16, unscale, live, rows, w, total;  // offsets, and the bytes of all
 };
 
 // Slots an expert on average up to which the streaming kernel runs. It decodes
@@ -124,7 +120,8 @@ constexpr int64_t kPairSlots = 128;
 
 Plan plan(const id::Product& p, const id::Batch& b) {
   Plan r{};
-  r.simt = takes_simt(p.wtype, p.K);
+  r.simt = p.wtype == RG_F32;
+  r.padded = !r.simt && id::padded_row_bytes(p.wtype, p.K) != id::row_bytes(p.wtype, p.K);
   // a few slots an expert: W's rows streamed once; else tiles of 128 or 256 slots
   r.few = !r.simt && b.slots <= few_slots_limit(p.wtype) * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
   r.cg = b.slots >= kPairSlots * b.experts ? 2 : 1;
@@ -145,11 +142,12 @@ Plan plan(const id::Product& p, const id::Batch& b) {
   r.unscale = take(r.simt || r.few || r.bf16 ? 0 : slots * 4);
   r.live = take(r.joined ? slots : 0);
   r.rows = take(r.joined ? slots * p.out_w() * 4 : 0);
+  r.w = take(r.padded ? b.experts * p.N * id::padded_row_bytes(p.wtype, p.K) : 0);
   r.total = at;
   return r;
 }
 
-cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void* ws, const DevInfo& dev,
+cudaError_t launch(id::Product p, const id::Batch& b, const Plan& r, void* ws, const DevInfo& dev,
                    cudaStream_t stream) {
   char* base = static_cast<char*>(ws);
   id::Tile* tiles = reinterpret_cast<id::Tile*>(base + r.tiles);
@@ -171,6 +169,11 @@ cudaError_t launch(const id::Product& p, const id::Batch& b, const Plan& r, void
   s.otype = r.joined ? RG_F32 : p.atype;
   s.beta = r.joined ? 0.0f : p.beta;
   cudaError_t e = cudaSuccess;
+  if (r.padded) {
+    e = id::launch_pad(p, b, base + r.w, stream);
+    if (e != cudaSuccess) return e;
+    p.W = base + r.w;
+  }
   if (r.few) {
     e = id::launch_few(p, b, s, live, dev, stream);
     if (e == cudaSuccess && r.joined) e = id::launch_join(rows, p.out_w(), live, b, p, dev, stream);
@@ -200,7 +203,7 @@ int check_shape(bool fwd, int wtype, int64_t N, int64_t K, const rg_id_batch* ba
   p->N = N;
   p->K = K;
   p->out_tokens = out_of == RG_ROWS_TOKEN;
-  return takes_simt(wtype, K) && p->out_w() > kMaxSimtWidth ? RG_ERR_ARG : RG_OK;
+  return wtype == RG_F32 && p->out_w() > kMaxSimtWidth ? RG_ERR_ARG : RG_OK;
 }
 
 int product(bool fwd, int wtype, const void* W, int64_t N, int64_t K, const rg_id_batch* batch, int atype,

@@ -658,7 +658,7 @@ cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t
   f.W = p.W;
   f.N = p.N;
   f.K = static_cast<int>(p.K);
-  f.rb = p.K / block_values(p.wtype) * block_bytes(p.wtype);
+  f.rb = padded_row_bytes(p.wtype, p.K);
   f.in = p.in;
   f.in_row = p.in_row;
   f.in_tokens = p.in_tokens ? 1 : 0;

@@ -3,6 +3,7 @@
 // public C ABI).
 #pragma once
 
+#include "rg_internal.cuh"
 #include "rg_launch.h"
 
 namespace rg {
@@ -57,7 +58,7 @@ struct Batch {
 struct Product {
   bool fwd;
   int wtype;
-  const void* W;
+  const void* W;        // rows padded_row_bytes apart once a launch of the tensor cores has it
   int64_t N, K;
   int atype;
   const void* in;
@@ -104,7 +105,12 @@ cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int
 // out[t] = beta * out[t] + sum of its slots' rows (F32, by slot, `width` values), each times its weight.
 cudaError_t launch_join(const float* rows, int64_t width, const uint8_t* live, const Batch& b, const Product& p,
                         const DevInfo& dev, cudaStream_t stream);
-// The product in F32 by plain threads, any type and alignment of rows.
+// Rows of W from one to the next, in bytes: as W lies, and as TMA can address them (multiples of 16).
+inline int64_t row_bytes(int wtype, int64_t K) { return K / block_values(wtype) * block_bytes(wtype); }
+inline int64_t padded_row_bytes(int wtype, int64_t K) { return (row_bytes(wtype, K) + 15) / 16 * 16; }
+// The used experts' rows of W, padded_row_bytes apart.
+cudaError_t launch_pad(const Product& p, const Batch& b, void* to, cudaStream_t stream);
+// The product with F32 weights, by plain threads.
 cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int cap, const DevInfo& dev,
                         cudaStream_t stream);
 constexpr int kSimtTile = 64;

@@ -40,7 +40,7 @@ static cudaError_t launch_grp_t(const CUtensorMap& mw, const CUtensorMap& mx, co
                                     static_cast<float*>(nullptr), ctl, tc::GrpArg<true>{s}));
 }
 
-// W: `experts` matrices of N rows of K values, one after another; x16: the
+// W: `experts` matrices of N rows of K values, padded_row_bytes apart; x16: the
 // slots' 16-bit copy in sorted order.
 template <bool FWD>
 static cudaError_t launch_grp(int wtype, const void* W, int64_t experts, int64_t N, int64_t K, const uint16_t* x16,
@@ -57,7 +57,7 @@ static cudaError_t launch_grp(int wtype, const void* W, int64_t experts, int64_t
   const uint64_t n = static_cast<uint64_t>(N), e = static_cast<uint64_t>(experts);
   CUresult r;
   if (is_quant(wtype)) {
-    const uint64_t rb = static_cast<uint64_t>(K / block_values(wtype) * block_bytes(wtype));
+    const uint64_t rb = static_cast<uint64_t>(padded_row_bytes(wtype, K));
     auto words = [&](CUtensorMap* m, uint32_t w) {
       return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, W, rb / 4, n, rb, w, rows, CU_TENSOR_MAP_SWIZZLE_NONE, e,
                           n * rb);

@@ -28,16 +28,12 @@ def weight_error(wtype, K):
     return 4e-3
 
 
-def aligned(wtype, K):
-    return inputs.row_bytes(wtype, K) % 16 == 0
-
-
 def product_tolerance(wtype, K, wide, atype, mag, ref, beta=0.0, old=0.0):
     """The error that a product's result may have: the input row's rounding to the operands' kind (nothing where the
     activations' type is within it; fp16 copies keep 11 bits down to 2^-28 of a row's largest value), the weights',
     the F32 sums' (one half step a term, twice for the tensor cores' truncated additions) and the result's own."""
     kind = BF16 if wtype == BF16 else F16
-    simt = wtype == F32 or not aligned(wtype, K)
+    simt = wtype == F32
     into = 0.0 if simt or atype == kind or (kind == F16 and atype == BF16) else HALF_STEP[kind]
     each = into + (0.0 if simt else weight_error(wtype, K)) + 2 * (wide + 8) * 2.0 ** -24
     return each * mag * 1.01 + HALF_STEP[atype] * (np.abs(ref) + each * mag + np.abs(beta * old)) * 1.01 + \

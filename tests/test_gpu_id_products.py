@@ -226,6 +226,19 @@ def test_bad_indices(rg):
                 assert np.isnan(got[lost]).all()
 
 
+@pytest.mark.parametrize("wtype", [inputs.Q6_K, inputs.Q3_K, inputs.Q2_K, inputs.MXFP4])
+@pytest.mark.parametrize("K", [256, 768, 1280, 1536])
+@pytest.mark.parametrize("fwd", [True, False])
+def test_rows_off_sixteen_bytes(rg, wtype, K, fwd):
+    """Rows of W that are not multiples of 16 bytes, at every phase of them: one row block and several, few slots,
+    tiles and pairs, experts without slots, a caller's workspace."""
+    rng = np.random.default_rng(K)
+    for N, tokens in ((8, 2), (104, 3), (72, 40), (264, 330)):
+        ids = _ids(rng, tokens, 2, 5, 0.1)
+        ids[ids == 3] = -1
+        Stack(torch, rg, wtype, 5, N, K, ids, 2, seed=N).check(fwd, BF16, TOKEN, SLOT, ws=tokens != 3)
+
+
 def test_far_expert(rg):
     """The last of a stack of more than 2^32 bytes."""
     E, N, K = 66, 8192, 4096
