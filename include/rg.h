@@ -591,6 +591,7 @@ typedef enum {
  * RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K with
  * K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the
  * used experts', to such in the workspace, which is larger by W's size.
+ * W of more than 2^46 bytes: RG_ERR_ARG.
  *
  * The workspace (rg_*_id_workspace_bytes) comes from the library's
  * stream-ordered pool, or from the caller in the _ws forms (256-byte aligned;

@@ -203,6 +203,8 @@ int check_shape(bool fwd, int wtype, int64_t N, int64_t K, const rg_id_batch* ba
   p->N = N;
   p->K = K;
   p->out_tokens = out_of == RG_ROWS_TOKEN;
+  // (a stack of 2^46 bytes lies in no device's memory; its copy's size stays within 64 bits)
+  if (K > 0 && b->experts * N > (int64_t{1} << 46) / id::padded_row_bytes(wtype, K)) return RG_ERR_ARG;
   return wtype == RG_F32 && p->out_w() > kMaxSimtWidth ? RG_ERR_ARG : RG_OK;
 }
 

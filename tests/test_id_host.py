@@ -166,6 +166,9 @@ def test_product_workspace(lib):
         assert by_token >= by_slot + 600 * 4 * 64 > 0
         assert query(0, 64, 256, b, 0) == 0 and query(Q8, 60, 256, b, 0) == 0 and query(Q8, 64, 256, b, 2) == 0
         assert query(Q8, 64, 256, rg.rg_id_batch(4, 2, 0, BAD, BAD), 0) == 0
+        # rows of 210 bytes get a copy with rows of 224; no stack has 2^46 bytes
+        assert query(inputs.Q6_K, 64, 256, b, 0) >= query(Q8, 64, 256, b, 0) + 4 * 64 * 224
+        assert query(inputs.Q6_K, 1 << 30, 1 << 20, b, 0) == 0
     assert ctypes.sizeof(rg.rg_id_batch) == 32
 
 
