@@ -545,10 +545,11 @@ int rg_route_back(const float* logits, int64_t l_row, int64_t T, int experts, in
 int rg_group(const int32_t* ids, int64_t n, int groups, int32_t* start, int32_t* order, void* stream);
 
 /* The slots of one call of the products below: per_token of them a token, slot
- * s token s / per_token's.  start and order as rg_route or rg_group gives them;
- * the kernels check what they read (a range of start that is none counts as
- * empty, an entry of order outside the slots as none, either is reported as
- * RG_ERR_INDEX).  order is a permutation of the slots; where it is not, rows
+ * s token s / per_token's.  start and order as rg_route or rg_group gives them,
+ * or a part of start: with W and start from an expert on, the slots of the
+ * experts before it and behind the last have no expert in the call.  The kernels
+ * check what they read (a range of start that is none counts as empty, an entry
+ * of order outside the slots as none, either is reported as RG_ERR_INDEX).  order is a permutation of the slots; where it is not, rows
  * named twice hold either of their results and sums over tokens are undefined. */
 typedef struct rg_id_batch {
   int32_t experts;       /* matrices in W, at most 1024 (RG_ERR_SHAPE)     */

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
     const bool ok = static_cast<unsigned>(s) < static_cast<unsigned>(b.slots);
     if (lane == 0) {
       if (!ok) report_index(status);
-      else if (live != nullptr) live[s] = i < total;
+      if (live != nullptr) live[i] = 0;
     }
     if (x16 == nullptr || i >= total) continue;
     uint16_t* to = x16 + i * ld;
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(THREADS) simt_kernel(Slots g, const uint8_t* _
     int s = tid < rows ? __ldg(g.order + pos + tid) : -1;
     if (static_cast<unsigned>(s) >= static_cast<unsigned>(g.slots)) s = -1;
     s_slot[tid] = s;
+    if (g.live != nullptr && blockIdx.y == 0 && s >= 0) g.live[s] = 1;
   }
   __syncthreads();
   float acc[4][4] = {};

@@ -168,6 +168,7 @@ cudaError_t launch(id::Product p, const id::Batch& b, const Plan& r, void* ws, c
   s.out_row = r.joined ? p.out_w() : p.out_row;
   s.otype = r.joined ? RG_F32 : p.atype;
   s.beta = r.joined ? 0.0f : p.beta;
+  s.live = live;
   cudaError_t e = cudaSuccess;
   if (r.padded) {
     e = id::launch_pad(p, b, base + r.w, stream);
@@ -175,7 +176,7 @@ cudaError_t launch(id::Product p, const id::Batch& b, const Plan& r, void* ws, c
     p.W = base + r.w;
   }
   if (r.few) {
-    e = id::launch_few(p, b, s, live, dev, stream);
+    e = id::launch_few(p, b, s, dev, stream);
     if (e == cudaSuccess && r.joined) e = id::launch_join(rows, p.out_w(), live, b, p, dev, stream);
     return e;
   }

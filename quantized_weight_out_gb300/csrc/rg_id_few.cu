@@ -408,12 +408,18 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
     }
   };
   if (blockIdx.x == 0 && f.live != nullptr) {
-    const int total = __ldg(f.b.start + f.b.experts);
-    for (int i = tid; i < f.b.slots; i += THREADS + 32) {
-      const int s = __ldg(f.b.order + i);
-      if (static_cast<unsigned>(s) < static_cast<unsigned>(f.b.slots)) f.live[s] = i < total;
-      else report_index(f.ctl.status);
+    // the slots of the chunks, and no others: rows of slots outside them are not written
+    for (int i = tid; i < f.b.slots; i += THREADS + 32) f.live[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n_chunks * f.ns; i += THREADS + 32) {
+      const Chunk ch = chunks[i / f.ns];
+      const int r = i % f.ns;
+      if (r >= ch.rows) continue;
+      const int s = __ldg(f.b.order + ch.first + r);
+      if (static_cast<unsigned>(s) < static_cast<unsigned>(f.b.slots)) f.live[s] = 1;
     }
+    for (int i = tid; i < f.b.slots; i += THREADS + 32)
+      if (static_cast<unsigned>(__ldg(f.b.order + i)) >= static_cast<unsigned>(f.b.slots)) report_index(f.ctl.status);
   }
 
   if (warp == WARPS) {
@@ -651,8 +657,7 @@ bool few_fits(const Batch& b, const Product& p) {
   return p.fwd && ns >= 1 && p.N <= (1 << 30) && max_tiles(b.slots, b.experts, ns) <= 1024;
 }
 
-cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t* live, const DevInfo& dev,
-                       cudaStream_t stream) {
+cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, const DevInfo& dev, cudaStream_t stream) {
   Few f{};
   f.b = b;
   f.W = p.W;
@@ -671,7 +676,7 @@ cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t
   f.out_row = s.out_row;
   f.otype = s.otype;
   f.beta = s.beta;
-  f.live = live;
+  f.live = s.live;
   f.ctl = WaitCtl{dev.status, dev.wait_limit_ns};
   return with_wtype(p.wtype, cudaErrorInvalidValue, [&](auto wt) {
     constexpr int WT = decltype(wt)::value;

@@ -90,6 +90,7 @@ struct Slots {
   int64_t out_row;
   int otype;              // RG_F32, RG_F16 or RG_BF16
   float beta;
+  uint8_t* live;          // per slot (NULL: not wanted): set for the slots whose rows are written
 };
 
 constexpr int64_t max_tiles(int64_t slots, int64_t experts, int64_t bt) {
@@ -98,11 +99,11 @@ constexpr int64_t max_tiles(int64_t slots, int64_t experts, int64_t bt) {
 
 // rg_id.cu: the tile table; the input's 16-bit copy in sorted order (x16 NULL: the table alone), rows ld
 // apart, each row scaled by a power of two (fp16 copies) whose inverse goes to `unscale`; `live` [slots]
-// (may be NULL): whether the slot has an expert.
+// (may be NULL) is cleared, for the product's kernel to set.
 cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, const Product& p, bool bf16,
                           uint16_t* x16, int64_t ld, float* unscale, uint8_t* live, const DevInfo& dev,
                           cudaStream_t stream);
-// out[t] = beta * out[t] + sum of its slots' rows (F32, by slot, `width` values), each times its weight.
+// out[t] = beta * out[t] + sum of its live slots' rows (F32, by slot, `width` values), each times its weight.
 cudaError_t launch_join(const float* rows, int64_t width, const uint8_t* live, const Batch& b, const Product& p,
                         const DevInfo& dev, cudaStream_t stream);
 // Rows of W from one to the next, in bytes: as W lies, and as TMA can address them (multiples of 16).
@@ -115,11 +116,10 @@ cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int ca
                         cudaStream_t stream);
 constexpr int kSimtTile = 64;
 
-// rg_id_few.cu: the forward for a few slots an expert; whether a batch and product can take it.  Of s, the output and
-// the weights are used; live as launch_gather.
+// rg_id_few.cu: the forward for a few slots an expert; whether a batch and product can take it.  Of s, the output, the
+// weights and `live` (cleared and set here) are used.
 bool few_fits(const Batch& b, const Product& p);
-cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, uint8_t* live, const DevInfo& dev,
-                       cudaStream_t stream);
+cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, const DevInfo& dev, cudaStream_t stream);
 
 // rg_mm_id.cu, rg_tc_id.cu: the tensor-core kernel over the tile table.
 cudaError_t launch_mm_id(int wtype, const void* W, int64_t experts, int64_t N, int64_t K, const uint16_t* x16,

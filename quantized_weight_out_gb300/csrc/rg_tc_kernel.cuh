@@ -1760,6 +1760,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int q = 0; q < BT / 128; ++q) {
           if (static_cast<unsigned>(orow[q]) >= static_cast<unsigned>(grp.slots)) orow[q] = -1;
+          if (grp.live != nullptr && kt == 0 && orow[q] >= 0) grp.live[orow[q]] = 1;
           if (grp.weights != nullptr && orow[q] >= 0) mul[q] *= __ldg(grp.weights + orow[q]);
         }
       }
