@@ -75,7 +75,15 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
   __shared__ float s_top[THREADS / 32];
   const int lane = threadIdx.x % LANES;
   const int step = (gridDim.x - 1) * (THREADS / LANES);
-  const int total = __ldg(b.start + b.experts);
+  // the sorted places of the ranges that the table takes: between start's ends where start ascends,
+  // all of them where a range is refused (those of the others may lie anywhere)
+  bool refused = false;
+  for (int e = threadIdx.x; e < b.experts; e += THREADS) {
+    const int lo = __ldg(b.start + e), hi = __ldg(b.start + e + 1);
+    refused |= lo < 0 || hi < lo || hi > b.slots;
+  }
+  const bool all = __syncthreads_or(refused);
+  const int begin = all ? 0 : __ldg(b.start), end = all ? b.slots : __ldg(b.start + b.experts);
   for (int i = (blockIdx.x - 1) * (THREADS / LANES) + threadIdx.x / LANES; i < b.slots; i += step) {
     const int s = __ldg(b.order + i);
     const bool ok = static_cast<unsigned>(s) < static_cast<unsigned>(b.slots);
@@ -83,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
       if (!ok) report_index(status);
       if (live != nullptr) live[i] = 0;
     }
-    if (x16 == nullptr || i >= total) continue;
+    if (x16 == nullptr || i < begin || i >= end) continue;
     uint16_t* to = x16 + i * ld;
     const int64_t row = ok ? (in_tokens ? s / b.per_token : s) : 0;
     const char* from = static_cast<const char*>(in) + row * in_row * act_bytes(AT);

@@ -122,3 +122,17 @@ def test_ranges_that_overlap(rg, tokens, fwd):
     rg.check(call(s.wtype, s.W_d, s.N, s.K, batch, BF16, x_d, wide, TOKEN, out, width, TOKEN, None, 0.0, work, size, st))
     assert rg.rg_check(st) == rg.RG_ERR_INDEX
     assert bool(torch.isfinite(out.float()).all())
+
+
+# The input's copy, tile routes: which rows it holds.
+@pytest.mark.parametrize("wtype,tokens,K", ROUTES)
+@pytest.mark.parametrize("fwd", [True, False])
+@pytest.mark.parametrize("last", ["negative", "too small"])
+def test_a_last_entry_below_the_ranges(rg, wtype, tokens, K, fwd, last):
+    """Only the last expert's range is spoiled by it; the others' rows are right."""
+    s = _stack(rg, wtype, tokens, K)
+    start = s.start.copy()
+    start[E] = -1 if last == "negative" else 1
+    for x_of in (SLOT, TOKEN):
+        for out_of in (SLOT, TOKEN):
+            _check(rg, s, fwd, x_of, out_of, start, rg.RG_ERR_INDEX, weigh=True)
