@@ -92,7 +92,7 @@ constexpr bool x_split() { return WT == RG_Q4_0 || WT == RG_MXFP4 || WT == RG_Q6
 template <int WT>
 constexpr bool x_cross() { return WT == RG_Q4_0 || WT == RG_Q4_K; }
 // Types whose nibbles are used in place, as the fp16 subnormals q 2^-24: their sums are 2^-24 of the values', and with
-// them the sums of X's blocks of 32 that join them (for a minimum, or q - 8); a row's last factor undoes it.
+// them the sums of X's blocks of 32 that join them (for a minimum, or q - 8); the row's sum is multiplied by 2^24.
 template <int WT>
 constexpr bool x_sums() { return WT == RG_Q4_0 || WT == RG_Q4_K; }
 
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
             const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
 #pragma unroll
             for (int j = 0; j < 8; ++j) w8[j] *= mul;
-            if (k == 0) s_mul[r] *= __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) * (x_sums<WT>() ? 0x1p24f : 1.0f);
+            if (k == 0) s_mul[r] *= __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
           }
           uint8_t* to = xs + r * f.xstride;
           // two groups of four values of the block: group q goes to its lane's first or second eight bytes
@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
       if (slot < 0 || n0 + row >= N) continue;
       float v = 0.0f;
       for (int w = 0; w < f.wk; ++w) v += first[w * RED + col * 17 + row];
+      if (x_sums<WT>()) v *= 0x1p24f;  // (exact, and apart: with a row's power of two it can pass F32's range)
       v *= s_mul[col];
       char* to = static_cast<char*>(f.out) + static_cast<int64_t>(slot) * f.out_row * act_bytes(f.otype);
       if (f.beta != 0.0f) v = fmaf(f.beta, load_act(to, f.otype, n0 + row), v);
