@@ -586,8 +586,11 @@ typedef enum {
  * W's values are decoded into them as in rg_mul_mat, and an input row is rounded
  * once, after a power of two that brings its largest magnitude to 2^14 (fp16),
  * undone exactly afterwards: rows of any magnitude keep 11 bits and none
- * overflows, so RG_ERR_RANGE is not reported.  |err| <= 5e-3 * sum |in||deq W|
- * (times |w_s|) plus the result's own rounding to atype.  F32 W takes a slower
+ * overflows.  |err| <= 5e-3 * sum |in||deq W| (times |w_s|) plus the result's own
+ * rounding to atype, and 2^-135 * sum |deq W| by slot with weights.  (There a
+ * weight may be multiplied with the row's power of two first: a factor that
+ * passes F32's range, |w_s| times the row's largest magnitude of 2^141 and more,
+ * is reported as RG_ERR_RANGE where it is.)  F32 W takes a slower
  * route with F32 products (result rows of at most 65535 * 64 values,
  * RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K with
  * K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the

@@ -60,11 +60,14 @@ __device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
 // its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
 // fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
 // and none overflows; the product's rows are multiplied by the inverse, which
-// is exact, in F32.
+// is exact, in F32.  Where they are multiplied by weights too, that is by one
+// factor; one that F32 does not hold is reported here (a second multiplication
+// in the tensor-core kernel's epilogue cost calls without weights 1 to 10 %).
 template <int AT, bool BF16, int LANES>
 __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* tiles, int* n_tiles, int cap,
                                                          const void* __restrict__ in, int64_t in_row, int in_tokens,
-                                                         int wide, uint16_t* __restrict__ x16, int64_t ld,
+                                                         const float* __restrict__ weights, int wide,
+                                                         uint16_t* __restrict__ x16, int64_t ld,
                                                          float* __restrict__ unscale, uint8_t* __restrict__ live,
                                                          int* status) {
   pdl_launch_dependents();
@@ -122,7 +125,12 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
       }
       const int shift = row_shift(top);
       mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      if (lane == 0) unscale[i] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      if (lane == 0) {
+        const float back = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        unscale[i] = back;
+        const float weight = weights != nullptr && ok ? __ldg(weights + s) : 0.0f;
+        if (fabsf(weight) < INFINITY && fabsf(weight * back) == INFINITY) report_range(status);
+      }
     }
     for (int c0 = 8 * lane; c0 < wide; c0 += 8 * LANES * U) {
       fetch(c0);
@@ -329,8 +337,8 @@ cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int
     auto kern = bf16 ? (wide ? gather_kernel<AT, true, THREADS> : gather_kernel<AT, true, 32>)
                      : (wide ? gather_kernel<AT, false, THREADS> : gather_kernel<AT, false, 32>);
     kern<<<static_cast<unsigned>(1 + blocks), THREADS, 0, stream>>>(
-        b, bt, tiles, n_tiles, cap, p.in, p.in_row, p.in_tokens ? 1 : 0, static_cast<int>(p.wide()), x16, ld, unscale,
-        live, dev.status);
+        b, bt, tiles, n_tiles, cap, p.in, p.in_row, p.in_tokens ? 1 : 0, p.out_tokens ? nullptr : p.weights,
+        static_cast<int>(p.wide()), x16, ld, unscale, live, dev.status);
     return counted(cudaGetLastError());
   });
 }

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
   Chunk* chunks = reinterpret_cast<Chunk*>(sums + (x_sums<WT>() ? (f.K + 31) / 32 * COLS : 0));  // [cap]
   __shared__ uint64_t bars[16];                                         // full, empty: up to eight stages
   __shared__ int s_warp[WARPS + 1], s_base, s_abort, s_slot[COLS], s_top[COLS];
-  __shared__ float s_mul[COLS];
+  __shared__ float s_mul[COLS], s_weight[COLS];  // what undoes a row's power of two; the slot's weight
   __shared__ const char* s_from[COLS];
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
         slot = max(slot, 0);
         s_from[tid] = static_cast<const char*>(f.in) +
                       static_cast<int64_t>(f.in_tokens ? slot / f.b.per_token : slot) * f.in_row * act_bytes(f.atype);
-        s_mul[tid] = f.weights != nullptr ? __ldg(f.weights + slot) : 1.0f;
+        s_mul[tid] = 1.0f;
+        s_weight[tid] = f.weights != nullptr ? __ldg(f.weights + slot) : 1.0f;
         s_top[tid] = 0;
       }
       bar_consumers();
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
             const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
 #pragma unroll
             for (int j = 0; j < 8; ++j) w8[j] *= mul;
-            if (k == 0) s_mul[r] *= __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+            if (k == 0) s_mul[r] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
           }
           uint8_t* to = xs + r * f.xstride;
           // two groups of four values of the block: group q goes to its lane's first or second eight bytes
@@ -583,8 +584,9 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
       if (slot < 0 || n0 + row >= N) continue;
       float v = 0.0f;
       for (int w = 0; w < f.wk; ++w) v += first[w * RED + col * 17 + row];
-      if (x_sums<WT>()) v *= 0x1p24f;  // (exact, and apart: with a row's power of two it can pass F32's range)
-      v *= s_mul[col];
+      // (one after another: the factors' product can pass F32's range where the result does not)
+      if (x_sums<WT>()) v *= 0x1p24f;
+      v = v * s_mul[col] * s_weight[col];
       char* to = static_cast<char*>(f.out) + static_cast<int64_t>(slot) * f.out_row * act_bytes(f.otype);
       if (f.beta != 0.0f) v = fmaf(f.beta, load_act(to, f.otype, n0 + row), v);
       store_act(to, f.otype, n0 + row, v);
