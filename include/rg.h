@@ -590,7 +590,9 @@ typedef enum {
  * rounding to atype, and 2^-135 * sum |deq W| by slot with weights.  (There a
  * weight may be multiplied with the row's power of two first: a factor that
  * passes F32's range, |w_s| times the row's largest magnitude of 2^141 and more,
- * is reported as RG_ERR_RANGE where it is.)  F32 W takes a slower
+ * is reported as RG_ERR_RANGE where it is.)  An infinity among a row's values
+ * makes results of that row infinite, or NaN where the weight's operand is 0;
+ * with few slots an expert and Q4_0 or Q4_K weights they may all be NaN.  F32 W takes a slower
  * route with F32 products (result rows of at most 65535 * 64 values,
  * RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K with
  * K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the

@@ -93,10 +93,11 @@ __device__ __forceinline__ void store_act(void* row, int atype, int64_t at, floa
 }
 
 // The power of two that brings a row's largest magnitude `top` to 2^14 .. 2^15 (an fp16 copy of it then keeps fp16's 11
-// bits down to 2^-28 of that, and none overflows); rows of zeros, and those with an infinity, stay as they are.
+// bits down to 2^-28 of that, and none overflows); rows of zeros stay as they are, and one with an infinity is scaled as
+// the largest finite magnitudes are, so that no finite value of it becomes infinite, too.
 __device__ __forceinline__ int row_shift(float top) {
   const int e = static_cast<int>(__float_as_uint(top) >> 23);  // top in 2^(e - 127) .. 2^(e - 126)
-  return top == 0.0f || e == 255 ? 0 : min(141 - e, 120);
+  return top == 0.0f ? 0 : min(141 - min(e, 254), 120);
 }
 
 __device__ __forceinline__ void report_index(int* status) { atomicCAS(status, 0, (int)RG_ERR_INDEX); }

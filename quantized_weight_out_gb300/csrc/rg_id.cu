@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
         const float back = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
         unscale[i] = back;
         const float weight = weights != nullptr && ok ? __ldg(weights + s) : 0.0f;
-        if (fabsf(weight) < INFINITY && fabsf(weight * back) == INFINITY) report_range(status);
+        if (top < INFINITY && fabsf(weight) < INFINITY && fabsf(weight * back) == INFINITY) report_range(status);
       }
     }
     for (int c0 = 8 * lane; c0 < wide; c0 += 8 * LANES * U) {

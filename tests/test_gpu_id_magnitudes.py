@@ -85,3 +85,21 @@ def test_weights_beside_magnitudes(rg, wtype, fwd, large):
             w = np.abs(oracle.dequant(wtype, s.W, 4 * 72, 512).astype(np.float64).reshape(4, 72, 512)[s.ids])
             tol = tol + 2.0 ** -135 * w.sum(2 if fwd else 1)
         assert (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("wtype", [inputs.F16, inputs.Q8_0, inputs.Q6_K, inputs.MXFP4])
+@pytest.mark.parametrize("fwd", [True, False])
+def test_an_infinity_beside_large_values(rg, wtype, fwd):
+    """A row with one infinity gives infinities of the signs of its weights (NaN for zeros), whatever else it holds: its
+    finite values beyond the operands' range are not infinite."""
+    for tokens in (2, 150):
+        s = _stack(rg, wtype, tokens, K=2048)
+        wide = 2048 if fwd else 72
+        x = s.act(s.slots, wide, F32, 1e30)
+        x[1, 5] = np.inf
+        got = s.run(fwd, F32, x, SLOT, SLOT)
+        w = oracle.dequant(wtype, s.W.reshape(4, -1)[s.ids[1]], 72, 2048)
+        along = w[:, 5] if fwd else w[5]
+        big = np.abs(along) > 2.0 ** -14   # (a decoded operand is a normal fp16 there)
+        assert big.any() and np.array_equal(got[1][big], np.inf * np.sign(along[big]))
+        assert np.isnan(got[1][along == 0]).all()
