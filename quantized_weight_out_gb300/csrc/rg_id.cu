@@ -56,7 +56,7 @@ __device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
 // Block 0 builds the table; the other blocks' groups of LANES threads (a warp,
 // or for rows over 4096 values the block: so many rows of warps would be under
 // way that their second reading misses the L2, 103 us for 8186 rows of 14336)
-// take the sorted slots in turn.  A row of an fp16 copy is multiplied by the power of two that brings
+// take the sorted slots in turn, and report those that are none.  A row of an fp16 copy is multiplied by the power of two that brings
 // its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
 // fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
 // and none overflows; the product's rows are multiplied by the inverse, which
@@ -329,9 +329,7 @@ cudaError_t launch_gather(const Batch& b, int bt, Tile* tiles, int* n_tiles, int
                           cudaStream_t stream) {
   const bool wide = x16 != nullptr && p.wide() > 4096;
   const int64_t a_block = wide ? 1 : THREADS / 32;
-  const int64_t blocks = x16 == nullptr && live == nullptr
-                             ? 0
-                             : std::min<int64_t>((b.slots + a_block - 1) / a_block, dev.num_sms * 8);
+  const int64_t blocks = std::min<int64_t>((b.slots + a_block - 1) / a_block, dev.num_sms * 8);
   return with_atype(p.atype, [&](auto at) {
     constexpr int AT = decltype(at)::value;
     auto kern = bf16 ? (wide ? gather_kernel<AT, true, THREADS> : gather_kernel<AT, true, 32>)

@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
     fence_mbar_init();
     tma_prefetch_map(&map);
   }
+  // (every entry of order is looked at by some block; the load is under way while start is read)
+  int at_order = static_cast<int>(blockIdx.x) * (THREADS + 32) + tid;
+  int named = at_order < f.b.slots ? __ldg(f.b.order + at_order) : 0;
   // the chunks: a running sum of the experts'
   __syncthreads();
   for (int e0 = 0; e0 < f.b.experts; e0 += THREADS + 32) {
@@ -394,6 +397,11 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
     if (tid == THREADS + 31) s_base = at + mine;
     __syncthreads();
   }
+  while (at_order < f.b.slots) {
+    if (static_cast<unsigned>(named) >= static_cast<unsigned>(f.b.slots)) report_index(f.ctl.status);
+    at_order += static_cast<int>(gridDim.x) * (THREADS + 32);
+    named = at_order < f.b.slots ? __ldg(f.b.order + at_order) : 0;
+  }
   const int n_chunks = min(f.cap, s_base);
   const int N = static_cast<int>(f.N), strips = (N + strip - 1) / strip, pieces = (f.K + PV - 1) / PV;
   const int64_t items = static_cast<int64_t>(n_chunks) * strips;
@@ -418,8 +426,6 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
       const int s = __ldg(f.b.order + ch.first + r);
       if (static_cast<unsigned>(s) < static_cast<unsigned>(f.b.slots)) f.live[s] = 1;
     }
-    for (int i = tid; i < f.b.slots; i += THREADS + 32)
-      if (static_cast<unsigned>(__ldg(f.b.order + i)) >= static_cast<unsigned>(f.b.slots)) report_index(f.ctl.status);
   }
 
   if (warp == WARPS) {
@@ -467,10 +473,7 @@ __global__ void __launch_bounds__(THREADS + 32, 2) few_kernel(const __grid_const
       count = ch.rows;
       if (tid < count) {
         int slot = __ldg(f.b.order + ch.first + tid);
-        if (static_cast<unsigned>(slot) >= static_cast<unsigned>(f.b.slots)) {
-          report_index(f.ctl.status);
-          slot = -1;
-        }
+        if (static_cast<unsigned>(slot) >= static_cast<unsigned>(f.b.slots)) slot = -1;
         s_slot[tid] = slot;
         slot = max(slot, 0);
         s_from[tid] = static_cast<const char*>(f.in) +
