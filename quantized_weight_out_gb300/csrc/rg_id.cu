@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
   }
   __shared__ float s_top[THREADS / 32];
   const int lane = threadIdx.x % LANES;
-  const int step = (gridDim.x - 1) * (THREADS / LANES);
+  // (unsigned: within a step of 2^31 slots the next place passes 31 bits)
+  const unsigned step = (gridDim.x - 1) * (THREADS / LANES), slots = static_cast<unsigned>(b.slots);
   // the sorted places of the ranges that the table takes: between start's ends where start ascends,
   // all of them where a range is refused (those of the others may lie anywhere)
   bool refused = false;
@@ -86,10 +87,10 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
     refused |= lo < 0 || hi < lo || hi > b.slots;
   }
   const bool all = __syncthreads_or(refused);
-  const int begin = all ? 0 : __ldg(b.start), end = all ? b.slots : __ldg(b.start + b.experts);
-  for (int i = (blockIdx.x - 1) * (THREADS / LANES) + threadIdx.x / LANES; i < b.slots; i += step) {
+  const unsigned begin = all ? 0 : __ldg(b.start), end = all ? slots : __ldg(b.start + b.experts);
+  for (unsigned i = (blockIdx.x - 1) * (THREADS / LANES) + threadIdx.x / LANES; i < slots; i += step) {
     const int s = __ldg(b.order + i);
-    const bool ok = static_cast<unsigned>(s) < static_cast<unsigned>(b.slots);
+    const bool ok = static_cast<unsigned>(s) < slots;
     if (lane == 0) {
       if (!ok) report_index(status);
       if (live != nullptr) live[i] = 0;

@@ -1441,7 +1441,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       else coords(tile, ku, tt);
       const int cbase = GRP ? 0 : (tile / n_tiles1) * n_chunks;  // first contraction chunk of the split
       const int kt = ku * CG + static_cast<int>(rank);
-      const int ty = (GRP ? st.pos : tt * BT) + static_cast<int>(rank) * B_ROWS;
+      // (unsigned: the second half of a tile at the end of 2^31 slots starts past them all)
+      const int ty = static_cast<int>(static_cast<uint32_t>(GRP ? st.pos : tt * BT) + rank * B_ROWS);
       // W's boxes: of the stack's expert (GRP), or of the one matrix
       auto load_w = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
         if constexpr (GRP) tma_load_3d(dst, map, bar, x, y, st.expert);
