@@ -16,11 +16,12 @@ constexpr int THREADS = 256;
 // The table of tiles, by one block: a running sum of the experts' tiles.  An
 // expert whose range is not one (reported) has no slots; one whose tiles would
 // pass the table's end (ranges that overlap) is reported, and empty tiles stand
-// where its would.
-__device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, int* status) {
+// where its would.  Returns whether a range was refused.
+__device__ bool build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, int cap, int* status) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ int64_t base_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool refused = false;
   if (threadIdx.x == 0) base_s = 0;
   __syncthreads();
   for (int e0 = 0; e0 < b.experts; e0 += THREADS) {
@@ -28,7 +29,7 @@ __device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
     int first = 0, rows = 0;
     if (e < b.experts) {
       const int lo = __ldg(b.start + e), hi = __ldg(b.start + e + 1);
-      if (lo < 0 || hi < lo || hi > b.slots) report_index(status);
+      if (lo < 0 || hi < lo || hi > b.slots) refused = true;
       else first = lo, rows = hi - lo;
     }
     const int64_t mine = rows / bt + (rows % bt != 0);
@@ -51,12 +52,17 @@ __device__ void build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
     __syncthreads();
   }
   if (threadIdx.x == 0) *n_tiles = static_cast<int>(base_s < cap ? base_s : cap);
+  if (refused) report_index(status);
+  return __syncthreads_or(refused);
 }
 
 // Block 0 builds the table; the other blocks' groups of LANES threads (a warp,
 // or for rows over 4096 values the block: so many rows of warps would be under
 // way that their second reading misses the L2, 103 us for 8186 rows of 14336)
-// take the sorted slots in turn, and report those that are none.  A row of an fp16 copy is multiplied by the power of two that brings
+// take the sorted slots in turn, and report those that are none.  Where start
+// ascends, the ranges that the table takes lie between its ends, and those are
+// the rows copied; where a range is refused, the others may lie anywhere, and
+// block 0 copies the rest (a look at all of start by every block took 1 us).  A row of an fp16 copy is multiplied by the power of two that brings
 // its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
 // fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
 // and none overflows; the product's rows are multiplied by the inverse, which
@@ -71,31 +77,26 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(Batch b, int bt, Tile* 
                                                          float* __restrict__ unscale, uint8_t* __restrict__ live,
                                                          int* status) {
   pdl_launch_dependents();
-  if (blockIdx.x == 0) {
-    build_tiles(b, bt, tiles, n_tiles, cap, status);
-    return;
+  // (unsigned: within a step of 2^31 slots the next place passes 31 bits)
+  unsigned step = (gridDim.x - 1) * (THREADS / LANES), block = blockIdx.x - 1;
+  const bool rest = blockIdx.x == 0;
+  if (rest) {
+    if (!build_tiles(b, bt, tiles, n_tiles, cap, status)) return;
+    step = THREADS / LANES;
+    block = 0;
   }
   __shared__ float s_top[THREADS / 32];
   const int lane = threadIdx.x % LANES;
-  // (unsigned: within a step of 2^31 slots the next place passes 31 bits)
-  const unsigned step = (gridDim.x - 1) * (THREADS / LANES), slots = static_cast<unsigned>(b.slots);
-  // the sorted places of the ranges that the table takes: between start's ends where start ascends,
-  // all of them where a range is refused (those of the others may lie anywhere)
-  bool refused = false;
-  for (int e = threadIdx.x; e < b.experts; e += THREADS) {
-    const int lo = __ldg(b.start + e), hi = __ldg(b.start + e + 1);
-    refused |= lo < 0 || hi < lo || hi > b.slots;
-  }
-  const bool all = __syncthreads_or(refused);
-  const unsigned begin = all ? 0 : __ldg(b.start), end = all ? slots : __ldg(b.start + b.experts);
-  for (unsigned i = (blockIdx.x - 1) * (THREADS / LANES) + threadIdx.x / LANES; i < slots; i += step) {
+  const unsigned slots = static_cast<unsigned>(b.slots);
+  const unsigned begin = __ldg(b.start), end = __ldg(b.start + b.experts);
+  for (unsigned i = block * (THREADS / LANES) + threadIdx.x / LANES; i < slots; i += step) {
     const int s = __ldg(b.order + i);
     const bool ok = static_cast<unsigned>(s) < slots;
     if (lane == 0) {
       if (!ok) report_index(status);
       if (live != nullptr) live[i] = 0;
     }
-    if (x16 == nullptr || i < begin || i >= end) continue;
+    if (x16 == nullptr || (i >= begin && i < end) == rest) continue;
     uint16_t* to = x16 + i * ld;
     const int64_t row = ok ? (in_tokens ? s / b.per_token : s) : 0;
     const char* from = static_cast<const char*>(in) + row * in_row * act_bytes(AT);
