@@ -1735,6 +1735,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int* g_rows = reinterpret_cast<int*>(smem + C::OFF_EPI + 4 * 2 * ER * 32 * 4);  // GRP
     float* g_muls = reinterpret_cast<float*>(g_rows + BT);
     int g_step = 0;
+    // GRP: the slots of the table's tiles are marked here, where these warps wait for
+    // the first sums (beside each tile's rows it cost MXFP4's forward 1 to 4 %)
+    if constexpr (GRP) {
+      if (grp.live != nullptr)
+        for (int t = blockIdx.x; t < __ldcg(grp.n_tiles); t += gridDim.x) {
+          const int4 x = __ldcg(reinterpret_cast<const int4*>(grp.tiles) + t);
+          const int pos = x.y + (t - x.w) * BT, rows = min(BT, x.y + x.z - pos);
+          for (int at = 32 * eq + lane; at < rows; at += 128) {
+            const int s = __ldg(grp.order + pos + at);
+            if (static_cast<unsigned>(s) < static_cast<unsigned>(grp.slots)) grp.live[s] = 1;
+          }
+        }
+    }
     bool ok = true;
     Segs<SK> sg(unit, n_units, n_tiles, n_chunks);
     int tile = 0, c0 = 0, c1 = 0;
@@ -1761,7 +1774,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int q = 0; q < BT / 128; ++q) {
           if (static_cast<unsigned>(orow[q]) >= static_cast<unsigned>(grp.slots)) orow[q] = -1;
-          if (grp.live != nullptr && kt == 0 && orow[q] >= 0) grp.live[orow[q]] = 1;
           if (grp.weights != nullptr && orow[q] >= 0) mul[q] *= __ldg(grp.weights + orow[q]);
         }
       }
