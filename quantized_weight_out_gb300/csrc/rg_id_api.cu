@@ -87,28 +87,48 @@ struct Plan {
   size_t tiles, count, x16, unscale, live, rows, w, total;  // offsets, and the bytes of all
 };
 
-// Slots an expert on average up to which the streaming kernel runs. It decodes
-// W anew for each chunk of an expert's slots, a tile of 128 slots decodes once;
-// so the limit falls where the decoding costs it most. Measured, us of tiles /
-// streaming, 8 experts of 14336 x 4096 at the limit and above it:
-//   Q4_K 5: 156 / 125, 8: 156 / 185; Q8_0 5: 164 / 115, 8: 164 / 173; MXFP4 5: 152 / 167 (64 of
-//   2048 x 1536: 92 / 78), 8: 179 / 224; Q4_0 5: 137 / 105, 8: 161 / 162; Q2_K 5: 166 / 162, 8: 166 / 195;
-//   Q4_1 4: 159 / 144, 5: 159 / 162, 8: 159 / 199
-//   Q6_K 8: 245 / 208, 16: 92 / 107 (32 of 2048 x 2048); Q3_K 8: 270 / 253, 16: 270 / 384
-//   (their tiles take two scales for 32 values)
-//   Q5_0 2: 149 / 136, 4: 150 / 163; Q5_1 2: 70 / 58 (32 of 2048 x 2048), 5: 173 / 212
-//   Q5_K 1: 172 / 99, 2: 152 / 158; BF16 1: 210 / 187, 2: 168 / 183, 4: 173 / 238 (F16 alike)
-constexpr int few_slots_limit(int wtype) {
+// The most slots with which the streaming kernel runs. It decodes W anew for each
+// chunk of an expert's slots (`rows`, at most 8, fewer where rows of X are long),
+// a tile of 128 slots decodes once: so the limit, in eighths of a slot an expert
+// on average, falls where the decoding costs it most, and with the chunks that an
+// expert's slots make. us of tiles / streaming, a batch of random routes to 2 and
+// 4 experts a token; [8a] 8 experts of 14336 x 4096 (rows 8), [8b] 4096 x 14336
+// (rows 3), [8c] 4096 x 8192 (rows 5), [32] 4096 x 4096, [64] 2048 x 2048, [128] 1536
+// x 2048; at the limit, then above it:
+//   Q4_K 5 slots an expert: [8a] 150 / 101, 150 / 99 [64] 94 / 66, 95 / 64; [8b] 3: 168 / 148, 168 / 143,
+//     4: 168 / 176, 168 / 173; 6: [64] 94 / 98, 96 / 96, [32] 174 / 170, 8: 174 / 195 (but [8a] 8: 152 / 140)
+//   Q8_0 [8b] 3: 172 / 157, 4: 172 / 194; 6: [64] 97 / 97, 8: 96 / 105; Q4_0 as Q4_K
+//   MXFP4 5: [8a] 174 / 166, [64] 110 / 93, [32] 202 / 216, 202 / 209; [8b] 2: 195 / 194, 196 / 166, 3: 196 / 236;
+//     [8c] 3: 117 / 127, 118 / 112, 4: 117 / 134; 6: [8a] 174 / 188, [64] 110 / 125; Q4_1, Q2_K alike
+//   Q6_K 8: [8a] 236 / 160, [64] 144 / 117, [32] 275 / 213; [8b] 3: 265 / 225, 5: 265 / 269; [8c] 5: 156 / 147,
+//     6: 156 / 162; Q3_K 8: [8a] 262 / 204, [32] 305 / 279; [8b] 3: 297 / 259, 4: 297 / 303
+//     (their tiles take two scales for 32 values)
+//   Q5_0 2: [8a] 141 / 131, [64] 92 / 96, [32] 191 / 181; [8b] 1: 182 / 141, 2: 183 / 206; 3: [8a] 167 / 170
+//   Q5_1 1: [8a] 179 / 125, [64] 78 / 64, [32] 140 / 140; 2: [8a] 140 / 158, [32] 189 / 217, [128] 133 / 117
+//   Q5_K 1: [8a] 266 / 125, [64] 80 / 74, [32] 144 / 149, [128] 108 / 108; 2: [8a] 144 / 152, [64] 94 / 107
+//   BF16 (F16 alike), experts of 64 MB and more: 1: [8a] 174 / 101, [8c] 95 / 91, but [8b] 158 / 255 (1/2: 122 /
+//     122); 2: [8a] 129 / 155.  Of 32 MB: 1/2: [32] 87 / 77, 1: 131 / 176.  Smaller: 1/16: [128] 23 / 20,
+//     1/8: 35 / 30, [64] 24 / 25; 1/2: [64] 47 / 57, 1: 69 / 85 (but [128] 93 / 85)
+//   NVFP4, slots in all: 2: [8a] 96 / 80, [8b] 99 / 98, [64] 22 / 12; 4: [8a] 147 / 152, [64] 23 / 19; 8: [64] 31 /
+//     32, [32] 93 / 105; 5 an expert: [8a] 170 / 316 (a nibble's E2M1 value and its scale through F32 and back)
+// Up to four slots in all the launch counts, whatever the rest: [64] BF16 20 / 15, Q5_K 22 / 15.
+int64_t few_slots_limit(int wtype, int64_t experts, int64_t expert_bytes, int rows) {
+  int64_t eighths;
   switch (wtype) {
+    case RG_NVFP4: return 2;
     case RG_F16:
-    case RG_BF16:
-    case RG_Q5_K: return 1;
-    case RG_Q5_0:
-    case RG_Q5_1: return 2;
+    case RG_BF16: eighths = expert_bytes < (16 << 20) ? 1 : expert_bytes < (64 << 20) || rows < 5 ? 4 : 8; break;
+    case RG_Q5_K: eighths = 8; break;
+    case RG_Q5_1: eighths = std::min(8, 4 * rows); break;
+    case RG_Q5_0: eighths = std::min(16, 4 * rows); break;
     case RG_Q6_K:
-    case RG_Q3_K: return 8;
-    default: return 5;
+    case RG_Q3_K: eighths = 8 * rows; break;
+    case RG_MXFP4:
+    case RG_Q4_1:
+    case RG_Q2_K: eighths = std::min(40, 16 * rows / 3); break;
+    default: eighths = std::min(40, 8 * rows); break;
   }
+  return std::max<int64_t>(4, experts * eighths / 8);
 }
 
 // Slots an expert on average from which a tile is a pair of blocks' (256 slots,
@@ -123,7 +143,8 @@ Plan plan(const id::Product& p, const id::Batch& b) {
   r.simt = p.wtype == RG_F32;
   r.padded = !r.simt && id::padded_row_bytes(p.wtype, p.K) != id::row_bytes(p.wtype, p.K);
   // a few slots an expert: W's rows streamed once; else tiles of 128 or 256 slots
-  r.few = !r.simt && b.slots <= few_slots_limit(p.wtype) * static_cast<int64_t>(b.experts) && id::few_fits(b, p);
+  r.few = !r.simt && id::few_fits(b, p) &&
+          b.slots <= few_slots_limit(p.wtype, b.experts, p.N * id::row_bytes(p.wtype, p.K), id::few_rows(p.K));
   r.cg = b.slots >= kPairSlots * b.experts ? 2 : 1;
   r.bt = r.simt ? id::kSimtTile : 128 * r.cg;
   r.cap = static_cast<int>(id::max_tiles(b.slots, b.experts, r.bt));

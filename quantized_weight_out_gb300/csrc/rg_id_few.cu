@@ -649,13 +649,20 @@ cudaError_t launch_few_t(Few f, const DevInfo& dev, cudaStream_t stream) {
 
 }  // namespace
 
+constexpr int64_t X_ROOM = 96 * 1024;  // what a chunk's rows of X take at most
+
+int few_rows(int64_t K) { return static_cast<int>(std::min<int64_t>(8, X_ROOM / x_stride(K))); }
+
+// Whether a type has chunks of two MMAs' columns: those that stream more than five slots an expert.
+constexpr bool two_mmas(int wtype) { return wtype == RG_Q6_K || wtype == RG_Q3_K; }
+
 // Slots a chunk: one MMA's eight, or two's where an expert has more than five on average (40 tokens,
 // 5 slots an expert of 64: 50 us with eight, 59 with sixteen), no more than there are tokens, while
-// the rows of X take at most 96 KB.
+// the rows of X fit.
 int few_slots(const Batch& b, const Product& p) {
   const int64_t avg = (b.slots + std::min(b.experts, b.slots) - 1) / std::min(b.experts, b.slots);
-  const int64_t want = std::min<int64_t>(avg <= 5 ? 8 : 16, b.slots / b.per_token);
-  return static_cast<int>(std::min<int64_t>(want, 96 * 1024 / x_stride(p.K)));
+  const int64_t want = std::min<int64_t>(avg > 5 && two_mmas(p.wtype) ? 16 : 8, b.slots / b.per_token);
+  return static_cast<int>(std::min<int64_t>(want, X_ROOM / x_stride(p.K)));
 }
 
 bool few_fits(const Batch& b, const Product& p) {
@@ -689,7 +696,9 @@ cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, const D
     if constexpr (WT == RG_F32) {
       return cudaErrorInvalidValue;
     } else {
-      return f.ns <= 8 ? launch_few_t<WT, 1>(f, dev, stream) : launch_few_t<WT, 2>(f, dev, stream);
+      if constexpr (two_mmas(WT))
+        if (f.ns > 8) return launch_few_t<WT, 2>(f, dev, stream);
+      return launch_few_t<WT, 1>(f, dev, stream);
     }
   });
 }

@@ -119,6 +119,7 @@ constexpr int kSimtTile = 64;
 // rg_id_few.cu: the forward for a few slots an expert; whether a batch and product can take it.  Of s, the output, the
 // weights and `live` (cleared and set here) are used.
 bool few_fits(const Batch& b, const Product& p);
+int few_rows(int64_t K);  // slots a chunk of one MMA's columns: up to eight, as their rows of X fit
 cudaError_t launch_few(const Product& p, const Batch& b, const Slots& s, const DevInfo& dev, cudaStream_t stream);
 
 // rg_mm_id.cu, rg_tc_id.cu: the tensor-core kernel over the tile table.
