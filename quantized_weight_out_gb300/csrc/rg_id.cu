@@ -1,6 +1,7 @@
 // rg_id.cu - products by slot around the tensor-core kernel: the table of
-// tiles and the input's copy in sorted order, the sum over a token's slots, and
-// the product in F32 by plain threads for rows of W that TMA cannot address.
+// tiles and the input's copy in sorted order, the sum over a token's slots, the
+// copy of W whose rows TMA cannot address as they lie, and the product in F32 by
+// plain threads for F32 weights.
 #include <algorithm>
 
 #include "rg_act.cuh"
@@ -354,10 +355,7 @@ cudaError_t launch_join(const float* rows, int64_t width, const uint8_t* live, c
   });
 }
 
-cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int cap, const DevInfo& dev,
-                        cudaStream_t stream) {
-  (void)b;
-  (void)dev;
+cudaError_t launch_simt(const Product& p, const Slots& s, int cap, cudaStream_t stream) {
   const int64_t rb = row_bytes(p.wtype, p.K);
   const int64_t gy = (p.out_w() + kSimtTile - 1) / kSimtTile;  // (at most 65535)
   auto kern = p.fwd ? simt_kernel<true> : simt_kernel<false>;

@@ -204,7 +204,7 @@ cudaError_t launch(id::Product p, const id::Batch& b, const Plan& r, void* ws, c
   e = id::launch_gather(b, r.bt, tiles, count, r.cap, p, r.bf16, x16, p.wide(), unscale, live, dev, stream);
   if (e != cudaSuccess) return e;
   if (r.simt)
-    e = id::launch_simt(p, b, s, r.cap, dev, stream);
+    e = id::launch_simt(p, s, r.cap, stream);
   else
     e = (p.fwd ? id::launch_mm_id : id::launch_tc_id)(p.wtype, p.W, b.experts, p.N, p.K, x16, p.wide(), s, r.cg, dev,
                                                       stream);

@@ -112,8 +112,7 @@ inline int64_t padded_row_bytes(int wtype, int64_t K) { return (row_bytes(wtype,
 // The used experts' rows of W, padded_row_bytes apart.
 cudaError_t launch_pad(const Product& p, const Batch& b, void* to, cudaStream_t stream);
 // The product with F32 weights, by plain threads.
-cudaError_t launch_simt(const Product& p, const Batch& b, const Slots& s, int cap, const DevInfo& dev,
-                        cudaStream_t stream);
+cudaError_t launch_simt(const Product& p, const Slots& s, int cap, cudaStream_t stream);
 constexpr int kSimtTile = 64;
 
 // rg_id_few.cu: the forward for a few slots an expert; whether a batch and product can take it.  Of s, the output, the
