@@ -582,20 +582,35 @@ typedef enum {
  * (RG_ERR_SHAPE).  No slots: RG_OK, nothing launched; no experts or an empty
  * contraction: RG_ERR_SHAPE.
  *
- * Sums are F32.  The tensor cores take 16-bit operands, fp16 (bf16 for BF16 W):
- * W's values are decoded into them as in rg_mul_mat, and an input row is rounded
- * once, after a power of two that brings its largest magnitude to 2^14 (fp16),
- * undone exactly afterwards: rows of any magnitude keep 11 bits and none
- * overflows.  |err| <= 5e-3 * sum |in||deq W| (times |w_s|) plus the result's own
- * rounding to atype, and 2^-135 * sum |deq W| by slot with weights.  (There a
- * weight may be multiplied with the row's power of two first: a factor that
- * passes F32's range, |w_s| times the row's largest magnitude of 2^141 and more,
- * is reported as RG_ERR_RANGE where it is.)  An infinity among a row's values
- * makes results of that row infinite, or NaN where the weight's operand is 0;
- * with few slots an expert and Q4_0 or Q4_K weights they may all be NaN.  F32 W takes a slower
- * route with F32 products (result rows of at most 65535 * 64 values,
- * RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K with
- * K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the
+ * Sums are F32.  The tensor cores take 16-bit operands, fp16 (bf16 for BF16 W).
+ * An input row is rounded to them once, in fp16 after a power of two that brings
+ * its largest magnitude to 2^14, undone exactly afterwards: rows of any magnitude
+ * keep 11 bits and none overflows.  bf16 keeps 8 bits of F32 and F16 rows, and has
+ * F32's range (magnitudes above 3.389e38 become infinite).
+ *
+ * W's values become operands in one of two forms, by the number of slots an
+ * expert, the type, the size of an expert and the length of its rows.  Many slots,
+ * and rg_out_prod_id: F16, BF16 and NVFP4 exactly, MXFP4 exactly for block scales
+ * of 2^-24 .. 2^15, the others rounded to fp16 (once; Q6_K and Q3_K their scale
+ * before it; Q4_K, Q5_K and Q2_K, of s q - t: s and c s - t, with c in the middle
+ * of the codes, then the value), so values beyond fp16's range are infinite.  Few
+ * slots of rg_mul_mat_id: Q8_0, Q4_0, Q4_K, Q6_K and MXFP4 exactly, whatever their
+ * magnitude, the others rounded once.  So a result may change within its error
+ * where the number of slots changes the form.
+ *
+ * |err| <= 5e-3 * sum |in||deq W| (times |w_s|; Q4_K, Q5_K, Q2_K: of |s (q - c)| +
+ * |c s - t| where that is more than |deq W|) plus the result's own rounding to
+ * atype, and 2^-135 * sum |deq W| by slot with weights.  (There a weight may be
+ * multiplied with the row's power of two first: a factor that passes F32's range,
+ * |w_s| times the row's largest magnitude of 2^141 and more, is reported as
+ * RG_ERR_RANGE where it is.)  By token a slot's row is an F32 value before its
+ * weight.  An infinity among a row's values makes results of that row infinite, or
+ * NaN where the weight's operand is 0; with few slots an expert and Q4_0 or Q4_K
+ * weights they may all be NaN.
+ *
+ * F32 W takes a slower route with F32 products (result rows of at most 65535 * 64
+ * values, RG_ERR_ARG).  Rows of W that are not multiples of 16 bytes (Q6_K, Q3_K
+ * with K % 2048 != 0, Q2_K with K % 1024, MXFP4 with K % 512) are first copied, the
  * used experts', to such in the workspace, which is larger by W's size.
  * W of more than 2^46 bytes: RG_ERR_ARG.
  *

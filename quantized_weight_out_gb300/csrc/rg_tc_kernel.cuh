@@ -204,11 +204,23 @@ __device__ __forceinline__ void four_scaled(uint32_t u, __half2 off, __half2 d, 
   o0 = h2_as_u32(__hmul2(__hsub2(bytes_plus1024(u, SEL_B01), off), d));
   o1 = h2_as_u32(__hmul2(__hsub2(bytes_plus1024(u, SEL_B23), off), d));
 }
-// Four nibble values in bytes -> two half2 of q * ds + nm (Q4_K).
+// Four nibble values in bytes -> two half2 of (q - c) * ds + nm (Q4_K; magic:
+// 1024 + c).  Products by slot (the decoders' MID) have c in the middle of q's
+// range, 8, 16 or 2 for Q4_K, Q5_K, Q2_K, and nm = fp16(c * d*sc - dmin*m), small
+// where the values lie around zero: the rounding of ds is multiplied by q - c, not
+// q, and nm's is of a small number (4.6 half steps of d*sc in root mean square
+// instead of 8.8, and up to 7.5 for nm).  The products with one matrix keep c = 0,
+// and with it their results.
 __device__ __forceinline__ void four_affine(uint32_t u, __half2 magic, __half2 ds, __half2 nm,
                                             uint32_t& o0, uint32_t& o1) {
   o0 = h2_as_u32(__hfma2(__hsub2(bytes_plus1024(u, SEL_B01), magic), ds, nm));
   o1 = h2_as_u32(__hfma2(__hsub2(bytes_plus1024(u, SEL_B23), magic), ds, nm));
+}
+
+// What four_affine adds, in F32 (s and min are exact products): -min, with MID c * s - min.
+template <bool MID>
+__device__ __forceinline__ float middle(float c, float s, float min) {
+  return MID ? fmaf(c, s, -min) : -min;
 }
 
 // Store a 16-byte chunk (8 fp16 values of k = 8*cidx .. 8*cidx+7 of the tile)
@@ -412,7 +424,7 @@ __device__ __forceinline__ uint32_t byte_of(uint32_t h1, uint32_t h2, uint32_t h
 // sub-block 2c+1) of the super-block at `row`; chunk cl of this CTA's half.
 // `q32`: the chunk's 32 nibble bytes (row + 16 + 32c in a whole super-block;
 // the forward copies them apart from the 16-byte header `row`).
-template <int H2, int CL, int HH>
+template <int H2, int CL, int HH, bool MID = false>
 __device__ __forceinline__ void dec_q4_k_part(const uint8_t* row, const uint8_t* q32, uint8_t* A,
                                               int n) {
   constexpr int c = 2 * H2 + CL;
@@ -433,11 +445,13 @@ __device__ __forceinline__ void dec_q4_k_part(const uint8_t* row, const uint8_t*
       m[h] = (e >> 4) | ((byte_of(hdr.y, hdr.z, hdr.w, j) >> 6) << 4);
     }
   }
-  const __half2 magic = __float2half2_rn(1024.0f);
-  const __half2 ds0 = __float2half2_rn(d * static_cast<float>(sc[0]));
-  const __half2 nm0 = __float2half2_rn(-(dmin * static_cast<float>(m[0])));
-  const __half2 ds1 = __float2half2_rn(d * static_cast<float>(sc[1]));
-  const __half2 nm1 = __float2half2_rn(-(dmin * static_cast<float>(m[1])));
+  constexpr float C0 = MID ? 8.0f : 0.0f;
+  const __half2 magic = __float2half2_rn(1024.0f + C0);
+  const float s0 = d * static_cast<float>(sc[0]), s1 = d * static_cast<float>(sc[1]);
+  const __half2 ds0 = __float2half2_rn(s0);
+  const __half2 nm0 = __float2half2_rn(middle<MID>(C0, s0, dmin * static_cast<float>(m[0])));
+  const __half2 ds1 = __float2half2_rn(s1);
+  const __half2 nm1 = __float2half2_rn(middle<MID>(C0, s1, dmin * static_cast<float>(m[1])));
   const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
   uint32_t lo[8], hi[8];
 #pragma unroll
@@ -499,7 +513,7 @@ __device__ __forceinline__ void dec_q41_q5_block(const uint8_t* row, uint8_t* A,
 // Q5_K: as dec_q4_k_part, with the fifth bit of each value from qh: bit 2c
 // (low nibbles) or 2c+1 (high nibbles) of qh[l]; this part covers l = 16HH ..
 // 16HH+15, i.e. qh bytes 16HH .. 16HH+15 at window offset 16.
-template <int H2, int CL, int HH>
+template <int H2, int CL, int HH, bool MID = false>
 __device__ __forceinline__ void dec_q5_k_part(const uint8_t* row, uint8_t* A, int n) {
   constexpr int c = 2 * H2 + CL;
   const uint4 hdr = *reinterpret_cast<const uint4*>(row);
@@ -520,11 +534,13 @@ __device__ __forceinline__ void dec_q5_k_part(const uint8_t* row, uint8_t* A, in
       m[h] = (e >> 4) | ((byte_of(hdr.y, hdr.z, hdr.w, j) >> 6) << 4);
     }
   }
-  const __half2 magic = __float2half2_rn(1024.0f);
-  const __half2 ds0 = __float2half2_rn(d * static_cast<float>(sc[0]));
-  const __half2 nm0 = __float2half2_rn(-(dmin * static_cast<float>(m[0])));
-  const __half2 ds1 = __float2half2_rn(d * static_cast<float>(sc[1]));
-  const __half2 nm1 = __float2half2_rn(-(dmin * static_cast<float>(m[1])));
+  constexpr float C0 = MID ? 16.0f : 0.0f;
+  const __half2 magic = __float2half2_rn(1024.0f + C0);
+  const float s0 = d * static_cast<float>(sc[0]), s1 = d * static_cast<float>(sc[1]);
+  const __half2 ds0 = __float2half2_rn(s0);
+  const __half2 nm0 = __float2half2_rn(middle<MID>(C0, s0, dmin * static_cast<float>(m[0])));
+  const __half2 ds1 = __float2half2_rn(s1);
+  const __half2 nm1 = __float2half2_rn(middle<MID>(C0, s1, dmin * static_cast<float>(m[1])));
   const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
   const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w};
   uint32_t lo[8], hi[8];
@@ -649,7 +665,7 @@ __device__ __forceinline__ void dec_q6_k_fwd(const uint8_t* pa, const uint8_t* p
 // + l: bits 2j..2j+1 of qs[32H + 16s + l]; its scales byte 8H + 2j + s gives
 // sc (low nibble) and m; the operand is fp16(q * fp16(d*sc) - fp16(dmin*m)).
 // G >= 0: only the 64 values 64G .. 64G+63 of the half.
-template <int O, int H, int G = -1>
+template <int O, int H, int G = -1, bool MID = false>
 __device__ __forceinline__ void dec_q2_k_row(const uint8_t* row, uint8_t* A, int n) {
   constexpr int QSB = O + 8 * H, QQ = O + 16 + 32 * H, QD = O + 80;
   static_assert(O % 4 == 0 && QD + 4 <= p_row_bytes<RG_Q2_K>(), "aligned words inside the window");
@@ -663,15 +679,17 @@ __device__ __forceinline__ void dec_q2_k_row(const uint8_t* row, uint8_t* A, int
   const float d = __half2float(__ushort_as_half(static_cast<uint16_t>(dw & 0xFFFFu)));
   const float dmin = __half2float(__ushort_as_half(static_cast<uint16_t>(dw >> 16)));
   const uint32_t sw[2] = {rs.word_at(QSB - 16 * CS), rs.word_at(QSB - 16 * CS + 4)};
-  const __half2 magic = __float2half2_rn(1024.0f);
+  constexpr float C0 = MID ? 2.0f : 0.0f;
+  const __half2 magic = __float2half2_rn(1024.0f + C0);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
       if (G >= 0 && (j >> 1) != G) continue;
       const uint32_t b = (sw[j >> 1] >> (8 * (2 * (j & 1) + sb))) & 0xFFu;  // byte 2j + sb
-      const __half2 ds = __float2half2_rn(d * static_cast<float>(b & 15u));       // exact product
-      const __half2 nm = __float2half2_rn(-(dmin * static_cast<float>(b >> 4)));  // exact product
+      const float s = d * static_cast<float>(b & 15u);  // (an exact product)
+      const __half2 ds = __float2half2_rn(s);
+      const __half2 nm = __float2half2_rn(middle<MID>(C0, s, dmin * static_cast<float>(b >> 4)));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {  // l = 8c .. 8c+7
         const int x = QQ - 16 * CQ + 16 * sb + 8 * c;
@@ -736,7 +754,7 @@ __device__ __forceinline__ void dec_q3_k_row(const uint8_t* row, uint8_t* A, int
 // window whose super-block starts O bytes in; O (0, 4, 8, 12) and H at run
 // time (one instance for every super-block), every word an aligned 32-bit
 // load.  Values as dec_q2_k_row.
-template <int G>
+template <int G, bool MID = false>
 __device__ __forceinline__ void dec_q2_k_fwd(const uint8_t* row, int O, int H, uint8_t* A, int n) {
   const uint8_t* b = row + O;
   const uint32_t dw = *reinterpret_cast<const uint32_t*>(b + 80);
@@ -744,15 +762,17 @@ __device__ __forceinline__ void dec_q2_k_fwd(const uint8_t* row, int O, int H, u
   const float dmin = __half2float(__ushort_as_half(static_cast<uint16_t>(dw >> 16)));
   const uint32_t sw = *reinterpret_cast<const uint32_t*>(b + 8 * H + 4 * G);  // scale bytes 8H + 4G ..
   const uint8_t* qb = b + 16 + 32 * H;
-  const __half2 magic = __float2half2_rn(1024.0f);
+  constexpr float C0 = MID ? 2.0f : 0.0f;
+  const __half2 magic = __float2half2_rn(1024.0f + C0);
 #pragma unroll
   for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
       const int j = 2 * G + jj;
       const uint32_t sc = (sw >> (8 * (2 * jj + sb))) & 0xFFu;  // scales byte 8H + 2j + sb
-      const __half2 ds = __float2half2_rn(d * static_cast<float>(sc & 15u));       // exact product
-      const __half2 nm = __float2half2_rn(-(dmin * static_cast<float>(sc >> 4)));  // exact product
+      const float s = d * static_cast<float>(sc & 15u);  // (an exact product)
+      const __half2 ds = __float2half2_rn(s);
+      const __half2 nm = __float2half2_rn(middle<MID>(C0, s, dmin * static_cast<float>(sc >> 4)));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {  // l = 8c .. 8c+7
         const uint32_t* qw = reinterpret_cast<const uint32_t*>(qb + 16 * sb + 8 * c);
@@ -809,7 +829,7 @@ __device__ __forceinline__ void dec_q3_k_fwd(const uint8_t* row, int O, int H, u
 
 // Block b (32-value types) or part b (Q4_K, Q5_K: chunk b >> 1 of the
 // half, 16 bytes b & 1) of row n of a stage.
-template <int WT, int ODD, int B>
+template <int WT, int ODD, int B, bool MID = false>
 __device__ __forceinline__ void dec_item(const uint8_t* row, uint8_t* A, int n, int o) {
   if constexpr (WT == RG_MXFP4) dec_mxfp4_block<B>(row, A, n, o);
   else if constexpr (WT == RG_NVFP4) dec_nvfp4_item<B>(row, A, n, o);
@@ -818,8 +838,9 @@ __device__ __forceinline__ void dec_item(const uint8_t* row, uint8_t* A, int n, 
   else if constexpr (WT == RG_Q4_1) dec_q41_q5_block<WT, 20 * B>(row, A, n, B);
   else if constexpr (WT == RG_Q5_0) dec_q41_q5_block<WT, 8 * ODD + 22 * B>(row, A, n, B);
   else if constexpr (WT == RG_Q5_1) dec_q41_q5_block<WT, 24 * B>(row, A, n, B);
-  else if constexpr (WT == RG_Q4_K) dec_q4_k_part<ODD, B / 2, B % 2>(row, row + 16 + 32 * (2 * ODD + B / 2), A, n);
-  else dec_q5_k_part<ODD, B / 2, B % 2>(row, A, n);
+  else if constexpr (WT == RG_Q4_K)
+    dec_q4_k_part<ODD, B / 2, B % 2, MID>(row, row + 16 + 32 * (2 * ODD + B / 2), A, n);
+  else dec_q5_k_part<ODD, B / 2, B % 2, MID>(row, A, n);
 }
 
 // One warp decodes a whole stage: P holds BC packed rows (row stride
@@ -830,7 +851,7 @@ __device__ __forceinline__ void dec_item(const uint8_t* row, uint8_t* A, int n, 
 // odd (window offset 8 for Q8_0 / Q4_0, second half of a Q4_K super-block).
 // o: the MXFP4 and NVFP4 run-time window offset (0, 4, 8 or 12; 0 or 8); O: the super-block
 // offset of the row-half decoders.
-template <int WT, int ODD, int NPART, int O = 0>
+template <int WT, int ODD, int NPART, int O = 0, bool MID = false>
 __device__ __forceinline__ void decode_stage_warp(const uint8_t* __restrict__ P,
                                                   uint8_t* __restrict__ A, int lane, int part,
                                                   int o = 0) {
@@ -840,7 +861,7 @@ __device__ __forceinline__ void decode_stage_warp(const uint8_t* __restrict__ P,
     const int n = lane + 32 * part;
     if constexpr (WT == RG_Q6_K) dec_q6_k_row<O, ODD>(P + n * PR, A, n);
     else if constexpr (WT == RG_Q3_K) dec_q3_k_row<O, ODD>(P + n * PR, A, n);
-    else dec_q2_k_row<O, ODD>(P + n * PR, A, n);
+    else dec_q2_k_row<O, ODD, -1, MID>(P + n * PR, A, n);
     return;
   }
 #pragma unroll
@@ -849,10 +870,10 @@ __device__ __forceinline__ void decode_stage_warp(const uint8_t* __restrict__ P,
     const int n = lane + 32 * (i & 1);
     const uint8_t* row = P + n * PR;
     switch (i >> 1) {
-      case 0: dec_item<WT, ODD, 0>(row, A, n, o); break;
-      case 1: dec_item<WT, ODD, 1>(row, A, n, o); break;
-      case 2: dec_item<WT, ODD, 2>(row, A, n, o); break;
-      default: dec_item<WT, ODD, 3>(row, A, n, o); break;
+      case 0: dec_item<WT, ODD, 0, MID>(row, A, n, o); break;
+      case 1: dec_item<WT, ODD, 1, MID>(row, A, n, o); break;
+      case 2: dec_item<WT, ODD, 2, MID>(row, A, n, o); break;
+      default: dec_item<WT, ODD, 3, MID>(row, A, n, o); break;
     }
   }
 }
@@ -864,7 +885,7 @@ __device__ __forceinline__ void decode_stage_warp(const uint8_t* __restrict__ P,
 // block is taken as the tile (A - HV column blocks), with 128 rows instead
 // of 64.  Warp `part` of the slot's two takes rows lane + 32 (2 part + r),
 // r = 0, 1, and of each row the items (blocks, Q4_K parts) of half HV.
-template <int WT, int ODD, int HV, int O = 0>
+template <int WT, int ODD, int HV, bool MID>
 __device__ __forceinline__ void decode_stage_fwd(const uint8_t* __restrict__ P, uint8_t* __restrict__ A,
                                                  int lane, int part, int o = 0) {
   constexpr int PR = p_row_bytes<WT>();
@@ -877,20 +898,20 @@ __device__ __forceinline__ void decode_stage_fwd(const uint8_t* __restrict__ P, 
       // the 16-byte headers of the stage's 128 rows, then their 32 nibble bytes
       const uint8_t* hdr = P + n * 16;
       const uint8_t* q32 = P + 128 * 16 + n * 32;
-      dec_q4_k_part<ODD, HV, 0>(hdr, q32, Ah, n);
-      dec_q4_k_part<ODD, HV, 1>(hdr, q32, Ah, n);
+      dec_q4_k_part<ODD, HV, 0, MID>(hdr, q32, Ah, n);
+      dec_q4_k_part<ODD, HV, 1, MID>(hdr, q32, Ah, n);
     } else {
       static_assert(WT != RG_Q6_K && WT != RG_Q3_K && WT != RG_Q2_K,
                     "the forward's K-quant stages are decode_stage_fwd_q6 and decode_stage_fwd_k");
-      dec_item<WT, ODD, 2 * HV>(row, Ah, n, o);
-      dec_item<WT, ODD, 2 * HV + 1>(row, Ah, n, o);
+      dec_item<WT, ODD, 2 * HV, MID>(row, Ah, n, o);
+      dec_item<WT, ODD, 2 * HV + 1, MID>(row, Ah, n, o);
     }
   }
 }
 
 // The forward's Q3_K and Q2_K stages: 128 rows of the chunk from their
 // whole windows, the super-block O bytes in, half H, quarter HV.
-template <int WT, bool U, int HV>
+template <int WT, bool U, int HV, bool MID>
 __device__ __forceinline__ void decode_stage_fwd_k(const uint8_t* __restrict__ P, uint8_t* __restrict__ A,
                                                    int lane, int part, int O, int H) {
   uint8_t* Ah = A - HV * A_COLBLK;
@@ -898,7 +919,7 @@ __device__ __forceinline__ void decode_stage_fwd_k(const uint8_t* __restrict__ P
   for (int r = 0; r < 2; ++r) {
     const int n = lane + 32 * (2 * part + r);
     if constexpr (WT == RG_Q3_K) dec_q3_k_fwd<U, HV>(P + n * p_fwd_row_bytes<WT>(), O, H, Ah, n);
-    else dec_q2_k_fwd<HV>(P + n * p_fwd_row_bytes<WT>(), O, H, Ah, n);
+    else dec_q2_k_fwd<HV, MID>(P + n * p_fwd_row_bytes<WT>(), O, H, Ah, n);
   }
 }
 
@@ -960,7 +981,7 @@ __device__ __forceinline__ void decode_stage_fwd_mx(const uint8_t* __restrict__ 
 
 // decode_stage_fwd for the run-time tile kw of the row (its parity, and the
 // block offset of the row-half and MXFP4 decoders) and half hv.
-template <int WT>
+template <int WT, bool MID = false>
 __device__ __forceinline__ void decode_fwd_stage(const uint8_t* __restrict__ P, uint8_t* __restrict__ A,
                                                  int lane, int part, int kw, int hv) {
   if constexpr (WT == RG_Q6_K) {
@@ -981,13 +1002,13 @@ __device__ __forceinline__ void decode_fwd_stage(const uint8_t* __restrict__ P, 
     if constexpr (WT == RG_Q3_K) shifted = (o & 2) != 0;
     if constexpr (WT == RG_Q3_K) {
       if (shifted) {
-        if (hv) decode_stage_fwd_k<WT, true, 1>(P, A, lane, part, o, kw & 1);
-        else decode_stage_fwd_k<WT, true, 0>(P, A, lane, part, o, kw & 1);
+        if (hv) decode_stage_fwd_k<WT, true, 1, MID>(P, A, lane, part, o, kw & 1);
+        else decode_stage_fwd_k<WT, true, 0, MID>(P, A, lane, part, o, kw & 1);
         return;
       }
     }
-    if (hv) decode_stage_fwd_k<WT, false, 1>(P, A, lane, part, o, kw & 1);
-    else decode_stage_fwd_k<WT, false, 0>(P, A, lane, part, o, kw & 1);
+    if (hv) decode_stage_fwd_k<WT, false, 1, MID>(P, A, lane, part, o, kw & 1);
+    else decode_stage_fwd_k<WT, false, 0, MID>(P, A, lane, part, o, kw & 1);
   } else if constexpr (WT == RG_Q8_0) {
     // the 64-value chunk's two blocks start (68 gf) mod 16 bytes into its window
     switch ((((2 * kw + hv) * 68) & 15) >> 2) {
@@ -999,14 +1020,14 @@ __device__ __forceinline__ void decode_fwd_stage(const uint8_t* __restrict__ P, 
   } else if constexpr (WT == RG_MXFP4 || WT == RG_NVFP4) {
     // the tile's blocks start 0, 4, 8 or 12 (MXFP4) or 0 or 8 (NVFP4) bytes into the window
     const int o = WT == RG_MXFP4 ? (kw * 68) & 12 : (kw & 1) * 8;
-    if (hv) decode_stage_fwd<WT, 0, 1>(P, A, lane, part, o);
-    else decode_stage_fwd<WT, 0, 0>(P, A, lane, part, o);
+    if (hv) decode_stage_fwd<WT, 0, 1, MID>(P, A, lane, part, o);
+    else decode_stage_fwd<WT, 0, 0, MID>(P, A, lane, part, o);
   } else if (kw & 1) {
-    if (hv) decode_stage_fwd<WT, 1, 1>(P, A, lane, part);
-    else decode_stage_fwd<WT, 1, 0>(P, A, lane, part);
+    if (hv) decode_stage_fwd<WT, 1, 1, MID>(P, A, lane, part);
+    else decode_stage_fwd<WT, 1, 0, MID>(P, A, lane, part);
   } else {
-    if (hv) decode_stage_fwd<WT, 0, 1>(P, A, lane, part);
-    else decode_stage_fwd<WT, 0, 0>(P, A, lane, part);
+    if (hv) decode_stage_fwd<WT, 0, 1, MID>(P, A, lane, part);
+    else decode_stage_fwd<WT, 0, 0, MID>(P, A, lane, part);
   }
 }
 
@@ -1675,7 +1696,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               // chunk gf: values 64 gf .. 64 gf + 63 of this CTA's 128 rows of W
               const int gf = GRP ? cc : (tile / n_tiles1) * n_chunks + cc;
               if constexpr (GRP && WT == RG_MXFP4) decode_stage_fwd_mx(window, sA + s * A_STAGE, lane, part, gf);
-              else decode_fwd_stage<WT>(window, sA + s * A_STAGE, lane, part, gf >> 1, gf & 1);
+              else decode_fwd_stage<WT, GRP>(window, sA + s * A_STAGE, lane, part, gf >> 1, gf & 1);
             } else if (AD && cc >= c_ad) {
               // nothing to decode
             } else if constexpr (WT == RG_Q6_K || WT == RG_Q3_K || WT == RG_Q2_K) {
@@ -1687,8 +1708,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #define RG_WIN_CASE(OO)                                                          \
   case OO / 2:                                                                   \
     if constexpr (WT != RG_Q2_K || OO % 4 == 0) {                                \
-      if (kt & 1) decode_stage_warp<WT, 1, WPS, OO>(P, Ad, lane, part);          \
-      else decode_stage_warp<WT, 0, WPS, OO>(P, Ad, lane, part);                 \
+      if (kt & 1) decode_stage_warp<WT, 1, WPS, OO, GRP>(P, Ad, lane, part);     \
+      else decode_stage_warp<WT, 0, WPS, OO, GRP>(P, Ad, lane, part);            \
     }                                                                            \
     break;
               switch (o >> 1) {
@@ -1703,9 +1724,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               decode_stage_warp<WT, 0, WPS>(window, sA + s * A_STAGE, lane, part,
                                             WT == RG_MXFP4 ? (kt * 68) & 12 : (kt & 1) * 8);
           } else if (kt & 1) {
-              decode_stage_warp<WT, 1, WPS>(window, sA + s * A_STAGE, lane, part);
+              decode_stage_warp<WT, 1, WPS, 0, GRP>(window, sA + s * A_STAGE, lane, part);
             } else {
-              decode_stage_warp<WT, 0, WPS>(window, sA + s * A_STAGE, lane, part);
+              decode_stage_warp<WT, 0, WPS, 0, GRP>(window, sA + s * A_STAGE, lane, part);
             }
             if (!AD || cc < c_ad) fence_proxy_async_smem();
             __syncwarp();
