@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(THREADS) route_back_kernel(const float* __rest
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     float part = 0.0f;
+    uint32_t in = 0;  // bit j: this lane's j-th expert takes part
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
+      if (l[j] > -INFINITY) in |= 1u << j;
       l[j] = l[j] > -INFINITY ? expf(l[j] - most) : 0.0f;
       part += l[j];
     }
@@ -180,14 +182,14 @@ __global__ void __launch_bounds__(THREADS) route_back_kernel(const float* __rest
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      l[j] = l[j] != 0.0f ? l[j] / total : 0.0f;
+      l[j] = in >> j & 1u ? l[j] / total : 0.0f;  // (a logit of +inf: NaN for all that take part, as in the weights)
       if (chosen >> j & 1u) dot = fmaf(l[j], up[j], dot);
     }
     dot = warp_sum(dot);
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = lane + 32 * j;
-      if (e < experts) dlogits[t * dl_row + e] = l[j] != 0.0f ? scale * (l[j] * (up[j] - dot)) : 0.0f;
+      if (e < experts) dlogits[t * dl_row + e] = in >> j & 1u ? scale * (l[j] * (up[j] - dot)) : 0.0f;
     }
   }
 }
