@@ -118,7 +118,8 @@ typedef enum {
                             operand copy: the call's dX holds inf or NaN (reported by
                             rg_check; rerun with RG_VARIANT_SIMT32 or a scaled dY).
                             Paged cache: a finite key, value or query outside the fp16
-                            operands' range (rg_kv_write, rg_kv_attend)                */
+                            operands' range (rg_kv_write, rg_kv_attend).  Products by
+                            slot: a weight beside a row too large for it (rg_mul_mat_id) */
     RG_ERR_INDEX = -8    /* paged cache: a length, a first token or a page number in a device
                             array lies outside the batch or the cache (reported by rg_check;
                             the sequence counts as empty, the page's tokens as not there).

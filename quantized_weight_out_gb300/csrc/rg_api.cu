@@ -856,7 +856,7 @@ const char* rg_strerror(int status) {
     case RG_ERR_TIMEOUT: return "a bounded device-side wait gave up";
     case RG_ERR_RANGE:
       return "a finite value (dY, X; a cached key or value, a query) lay outside the range of the 16-bit "
-             "tensor-core operands (fp16: 65504)";
+             "tensor-core operands (fp16: 65504), or a slot's weight times its row's magnitude that of F32";
     case RG_ERR_INDEX:
       return "a device array of lengths, page numbers, ids or slots holds a value outside the cache, the "
              "table, the experts or the batch";

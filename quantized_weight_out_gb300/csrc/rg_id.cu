@@ -63,7 +63,8 @@ __device__ bool build_tiles(const Batch& b, int bt, Tile* tiles, int* n_tiles, i
 // take the sorted slots in turn, and report those that are none.  Where start
 // ascends, the ranges that the table takes lie between its ends, and those are
 // the rows copied; where a range is refused, the others may lie anywhere, and
-// block 0 copies the rest (a look at all of start by every block took 1 us).  A row of an fp16 copy is multiplied by the power of two that brings
+// block 0 copies the rest (a look at all of start by every block took 1 us).
+// A row of an fp16 copy is multiplied by the power of two that brings
 // its largest magnitude to 2^14 .. 2^15, so that gradients of any size keep
 // fp16's 11 bits (values down to 2^-28 of the row's largest are not subnormal)
 // and none overflows; the product's rows are multiplied by the inverse, which
